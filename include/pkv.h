@@ -20,6 +20,15 @@
  *                           tokens attending their slots' keys through pages
  *   pkv_decode_attention  - one query token per row, GQA, over the pages
  *   pkv_prefill_attention - packed document-causal attention over fresh k/v
+ * and, for serving with drafted tokens and shared prefixes over the same
+ * cache (the pages have no counterpart; these are operators of this library):
+ *   pkv_tree_attention    - a tree of drafted tokens over the cached context
+ *   pkv_verify_tree       - which drafted tokens the target accepts, and the
+ *                           next token
+ *   pkv_commit_path       - the accepted path's K/V rows moved next to the
+ *                           committed context
+ *   pkv_update_pages      - fork, reserve, copy on write, truncate and free
+ *   pkv_compact_pages     - live pages moved to the low end of the pool
  *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -68,6 +77,13 @@ typedef enum {
 #define PKV_DEV_ERR_BAD_POS    0x4  /* position/seq_len < 0 or past max_blocks   */
 #define PKV_DEV_ERR_LAYOUT     0x8  /* prefill packing precondition violated     */
 #define PKV_DEV_ERR_TIMEOUT    0x10 /* a bounded wait inside a kernel gave up    */
+#define PKV_DEV_ERR_BAD_TREE   0x20 /* tree size, parent, path or token invalid  */
+#define PKV_DEV_ERR_NO_PAGES   0x40 /* not enough free pages for a row           */
+#define PKV_DEV_ERR_BAD_PROBS  0x80 /* a probability row sums to 0, inf or NaN   */
+
+/* Most nodes of a tree of drafted tokens (a node's ancestors are one 64-bit
+ * mask). */
+#define PKV_MAX_TREE_NODES 64
 
 /* Geometry of one layer's paged cache. */
 typedef struct {
@@ -381,6 +397,207 @@ pkv_status pkv_mixed_attention(const pkv_cache_desc* cache, const void* k_pool,
  */
 pkv_status pkv_stage_from_host(void* dst, const void* src, size_t bytes,
                                cudaStream_t stream);
+
+/*
+ * pkv_tree_workspace_size - bytes of workspace pkv_tree_attention needs on the
+ * CURRENT device for `batch` rows of n_nodes nodes (0 for invalid arguments).
+ */
+size_t pkv_tree_workspace_size(const pkv_cache_desc* cache, int batch, int n_nodes,
+                               int num_q_heads);
+
+/*
+ * pkv_tree_attention - attention of a tree of drafted tokens per sequence over
+ * the paged cache, on tcgen05 tensor cores.
+ *
+ * Row b is one sequence: slot c = batch_idx[b] holds ctx = ctx_lens[b]
+ * committed tokens, and the K/V of its tree's nodes 0 .. tree_lens[b]-1 are in
+ * the pools at positions ctx + 0, ctx + 1, ... (pkv_append first; whatever
+ * position the rotary embedding used is the caller's affair). parents:
+ * int32 [batch, n_nodes]; parents[b, i] in [-1, i) is the node that node i
+ * follows, -1 for one that follows the context (any number of nodes may).
+ * Node i attends the context, itself and its ancestors:
+ *   T(i) = {0 .. ctx-1} + {ctx + a : a = i, parent(i), parent(parent(i)), ..}
+ *   lse[b, i, h] = ln sum_{t in T(i)} exp(scale * q[b,i,h] . K[c,t,kvh])   (fp32)
+ *   out[b, i, h] = sum_{t in T(i)} exp(scale * q[b,i,h] . K[c,t,kvh] - lse) V[c,t,kvh]
+ * with kvh = h / (num_q_heads / num_kv_heads).
+ * q: bf16 [batch, n_nodes, num_q_heads, D]; batch_idx, ctx_lens, tree_lens:
+ * int32 [batch]; out: bf16 like q; lse: fp32 [batch, n_nodes, num_q_heads].
+ * Nodes at or past tree_lens[b] (padding) and every node of a row with slot 0
+ * give out 0, lse -inf. n_nodes is 1 .. PKV_MAX_TREE_NODES; ctx_lens[b] may be
+ * 0. A slot outside [0, max_batch) sets PKV_DEV_ERR_BAD_SLOT, a tree_lens[b]
+ * outside [0, n_nodes] PKV_DEV_ERR_BAD_TREE, a negative ctx_lens[b] or
+ * ctx + tree_lens[b] past the table PKV_DEV_ERR_BAD_POS: the row gives 0 /
+ * -inf. A parent outside [-1, i) sets PKV_DEV_ERR_BAD_TREE; that node and
+ * every node below it give 0 / -inf, the others are computed. An unreserved
+ * page entry among a row's keys sets PKV_DEV_ERR_BAD_PAGE and leaves the row
+ * unspecified. The pools are only read; slots past the last node may hold any
+ * bits. The K/V of a row's own nodes and context must be finite: a NaN or
+ * infinity in one node's V reaches the other nodes of its row.
+ * page_size must be 16, 32, 64 or a multiple of 128; scale finite and > 0.
+ * batch may be any count >= 0 (above 256 rows the call runs as equal launches
+ * that share the workspace). workspace: at least pkv_tree_workspace_size()
+ * bytes, 256-byte aligned, owned by the caller, no initialisation needed;
+ * calls that share one must be stream-ordered. All tensors are device memory.
+ */
+pkv_status pkv_tree_attention(const pkv_cache_desc* cache, const void* k_pool,
+                              const void* v_pool, const int32_t* page_table, const void* q,
+                              int num_q_heads, const int32_t* parents,
+                              const int32_t* tree_lens, const int32_t* batch_idx,
+                              const int32_t* ctx_lens, int batch, int n_nodes, float scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_err, cudaStream_t stream);
+
+/* Element types of probabilities. */
+#define PKV_PROBS_FP32 0
+#define PKV_PROBS_BF16 1
+
+/*
+ * pkv_verify_tree - acceptance of a tree of drafted tokens against the
+ * target's probabilities, from given random numbers.
+ *
+ * target_probs: [batch, n_nodes, vocab]; row (b, i) is the target's
+ * distribution of the token that follows node i. draft_probs: the same shape,
+ * row (b, i) the distribution that node i's children were drawn from one after
+ * another, or null: then every drafted token counts as drawn from a point mass
+ * on it (guessed tokens). Both have the element type `probs_type`
+ * (PKV_PROBS_*) and are 16-byte aligned; rows sum to 1 up to rounding; an entry
+ * that is negative or NaN counts as 0. draft_tokens, parents: int32 [batch,
+ * n_nodes]; tree_lens: int32 [batch]. Node 0 is the sequence's last token: it
+ * is accepted as it stands and its draft_tokens entry is not read; node i >= 1
+ * follows node parents[b, i] in [0, i).
+ *
+ * The walk starts at node 0. At node c its children x are tried in order of
+ * their number. With p, q the rows of c, r = p and R = 1 to begin with:
+ *   x is accepted iff u_accept[b, x] * q(tok x) * R < r(tok x)   (q(..) = 1 without
+ *   draft_probs); the walk goes on at x.
+ *   Otherwise r and R become those of the rest: with draft_probs
+ *     r(v) = max(r(v) - R q(v), 0), R = sum_v r(v);
+ *   without, R = max(R - r(tok x), 0), r(tok x) = 0.
+ * Where no child is accepted the next token is drawn from r: the lowest v with
+ * r(v) > 0 and sum_{w <= v} r(w) > u_sample[b] * sum_w r(w), or the highest v
+ * with r(v) > 0 where rounding leaves none; from p where r has no mass. (The
+ * accepted tokens and the next one are then distributed as the target's.)
+ * Decisions and sums are held to about 2^-45 of their terms, so that they do
+ * not depend on an order of summation in fp32.
+ *
+ * path: int32 [batch, n_nodes], the accepted nodes (0 first), -1 behind them;
+ * n_accepted: int32 [batch], their number (>= 1); tokens: int32 [batch,
+ * n_nodes], the tokens of the accepted nodes after node 0, then the drawn one
+ * (n_accepted in all), -1 behind them. tree_lens[b] = 0 (a padding row) gives
+ * n_accepted 0 and -1 throughout. A tree_lens[b] outside [0, n_nodes] sets
+ * PKV_DEV_ERR_BAD_TREE and is treated as 0; a parent outside [-1, i) or a
+ * drafted token outside [0, vocab) sets it too and leaves that node and all
+ * below it out (so does, without an error, a parent of -1 at i >= 1). A row
+ * to draw from that sums to 0 or is not finite sets PKV_DEV_ERR_BAD_PROBS and
+ * gives the token -1. n_nodes is 1 .. PKV_MAX_TREE_NODES. Results are the same
+ * on every run.
+ */
+pkv_status pkv_verify_tree(const void* target_probs, const void* draft_probs, int probs_type,
+                           int vocab, const int32_t* draft_tokens, const int32_t* parents,
+                           const int32_t* tree_lens, const float* u_accept,
+                           const float* u_sample, int batch, int n_nodes, int32_t* path,
+                           int32_t* tokens, int32_t* n_accepted, int32_t* dev_err,
+                           cudaStream_t stream);
+
+/*
+ * pkv_commit_path - moves the K/V rows of an accepted path next to the
+ * committed context, in place.
+ *
+ * For row b with slot c = batch_idx[b], ctx = ctx_lens[b] and n =
+ * n_accepted[b]: the rows at position ctx + path[b, i] of the slot go to
+ * position ctx + i, for 0 <= i < n (bit-exact byte copies; each row is read
+ * before anything overwrites it). path: int32 [batch, n_nodes] with
+ * path[b, 0..n) strictly increasing in [0, n_nodes), as pkv_verify_tree
+ * writes it. new_lens: int32 [batch] or null; new_lens[b] = ctx + n (it may be
+ * ctx_lens itself). Rows with slot 0 or n = 0 move nothing and give ctx. A
+ * slot out of range sets PKV_DEV_ERR_BAD_SLOT, an n or a path that breaks the
+ * above PKV_DEV_ERR_BAD_TREE, a position past the table PKV_DEV_ERR_BAD_POS, a
+ * page entry out of range at a moved position PKV_DEV_ERR_BAD_PAGE: the row
+ * moves nothing and gives ctx. A live slot must appear at most once, and no
+ * page that a row writes may belong to another slot as well (reserve the
+ * drafts' positions with pkv_update_pages).
+ */
+pkv_status pkv_commit_path(const pkv_cache_desc* cache, void* k_pool, void* v_pool,
+                           const int32_t* page_table, const int32_t* path,
+                           const int32_t* n_accepted, const int32_t* batch_idx,
+                           const int32_t* ctx_lens, int batch, int n_nodes, int32_t* new_lens,
+                           int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * pkv_update_workspace_size - bytes of workspace pkv_update_pages needs for n
+ * rows (0 for invalid arguments).
+ */
+size_t pkv_update_workspace_size(const pkv_cache_desc* cache, int n);
+
+/*
+ * pkv_update_pages - fork, reserve, copy on write, truncate and free.
+ *
+ * page_refs: int32 [num_pages], owned by the caller like the page table: how
+ * many table entries (and holds of the caller's own) use each page. A page
+ * with count 0 is free; page 0 is never handed out, whatever its count.
+ * Row i gives slot d = dst_slots[i] the first keep = keep_lens[i] tokens of
+ * slot s = src_slots[i] and makes positions keep .. new_lens[i]-1 writable:
+ *   s == d, new > keep : room for the next tokens (reserve)
+ *   s == d, new = keep : truncation; keep = 0 frees the slot
+ *   s != d             : fork: whole pages are shared, counted once more
+ *   s = 0, keep = 0    : a new sequence
+ * A block that holds one of the positions [keep, new) gets a page that is the
+ * slot's alone: the one it has when s == d and its count is 1, else a free
+ * page, into which the rows before `keep` of a partly kept block are copied
+ * (K and V, byte for byte). The slot's other entries up to new are the
+ * source's, those past new are -1; every entry that the slot gives up counts
+ * its page down. Writing only such positions, no sequence ever changes
+ * another's tokens.
+ *
+ * Counts are those at the start of the call: two slots that share a partly
+ * filled page and both reserve in one call both get a copy, and a page that
+ * one row gives up is free from the next call on. Free pages are handed out
+ * lowest number first, in row order and block order within a row, so the
+ * result does not depend on timing.
+ * A row with d = 0 is padding and does nothing. A row that cannot be served
+ * changes nothing, sets its bit, and the others go on: PKV_DEV_ERR_BAD_SLOT (a
+ * slot outside [0, max_batch); s = 0 with keep > 0; a destination that an
+ * earlier row has; a source, with keep > 0, that is another row's destination),
+ * PKV_DEV_ERR_BAD_POS (keep < 0, new < keep, new past the table),
+ * PKV_DEV_ERR_BAD_PAGE (a kept block without a page in [1, num_pages), or a
+ * page in use with a count below 1), PKV_DEV_ERR_NO_PAGES (a row that needs
+ * pages where the needs of the rows up to it exceed the free ones). Entries of
+ * the destination outside [1, num_pages) count as unreserved.
+ * page_table, page_refs, k_pool and v_pool are updated in place. workspace: at
+ * least pkv_update_workspace_size() bytes, 256-byte aligned, no initialisation
+ * needed; calls that share one must be stream-ordered.
+ */
+pkv_status pkv_update_pages(const pkv_cache_desc* cache, void* k_pool, void* v_pool,
+                            int32_t* page_table, int32_t* page_refs, const int32_t* dst_slots,
+                            const int32_t* src_slots, const int32_t* keep_lens,
+                            const int32_t* new_lens, int n, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * pkv_compact_workspace_size - bytes of workspace pkv_compact_pages needs
+ * (0 for invalid arguments).
+ */
+size_t pkv_compact_workspace_size(const pkv_cache_desc* cache);
+
+/*
+ * pkv_compact_pages - moves the live pages to the low end of the pool.
+ *
+ * With L the number of live pages (count > 0; page 0 always is), the k-th live
+ * page numbered L or more, in ascending order, moves to the k-th free page
+ * below L: its K and V rows are copied, every entry of page_table that names
+ * it is rewritten, and its count goes with it. Pages below L that are live
+ * stay where they are; afterwards the live pages are 0 .. L-1. num_live: int32
+ * [1] or null, receives L. page_refs as for pkv_update_pages, none negative. An
+ * entry of page_table that names a free page at or past L sets
+ * PKV_DEV_ERR_BAD_PAGE and is left as it is; other entries outside
+ * [0, num_pages) are left too. workspace: at least
+ * pkv_compact_workspace_size() bytes, 256-byte aligned, no initialisation
+ * needed; calls that share one must be stream-ordered.
+ */
+pkv_status pkv_compact_pages(const pkv_cache_desc* cache, void* k_pool, void* v_pool,
+                             int32_t* page_table, int32_t* page_refs, int32_t* num_live,
+                             void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                             cudaStream_t stream);
 
 /* Static, human-readable name of a status. */
 const char* pkv_status_string(pkv_status status);

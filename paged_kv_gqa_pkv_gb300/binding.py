@@ -13,8 +13,11 @@ Functions keep the names of the C entry points: ``pkv_append``,
 ``pkv_decode_append_attention``, ``pkv_decode_attention_static_scratch``,
 ``pkv_prefill_attention``, ``pkv_prefill_paged_attention``,
 ``pkv_mixed_workspace_size``, ``pkv_mixed_attention``,
-``pkv_stage_from_host``, ``pkv_status_string``,
-``pkv_status_from_device_error`` and ``pkv_last_cuda_error_string``.
+``pkv_stage_from_host``, ``pkv_tree_workspace_size``, ``pkv_tree_attention``,
+``pkv_verify_tree``, ``pkv_commit_path``, ``pkv_update_workspace_size``,
+``pkv_update_pages``, ``pkv_compact_workspace_size``, ``pkv_compact_pages``,
+``pkv_status_string``, ``pkv_status_from_device_error`` and
+``pkv_last_cuda_error_string``.
 """
 
 from __future__ import annotations
@@ -36,12 +39,19 @@ DEV_ERR_BAD_SLOT = 0x2
 DEV_ERR_BAD_POS = 0x4
 DEV_ERR_LAYOUT = 0x8
 DEV_ERR_TIMEOUT = 0x10
+DEV_ERR_BAD_TREE = 0x20
+DEV_ERR_NO_PAGES = 0x40
+DEV_ERR_BAD_PROBS = 0x80
+MAX_TREE_NODES = 64
 
 EXPORTED = ("pkv_append", "pkv_append_rope", "pkv_decode_workspace_size", "pkv_decode_attention",
             "pkv_decode_append_attention", "pkv_decode_attention_static_scratch",
             "pkv_prefill_paged_attention",
             "pkv_prefill_attention", "pkv_mixed_workspace_size", "pkv_mixed_attention",
-            "pkv_stage_from_host", "pkv_status_string",
+            "pkv_stage_from_host", "pkv_tree_workspace_size", "pkv_tree_attention",
+            "pkv_verify_tree", "pkv_commit_path", "pkv_update_workspace_size",
+            "pkv_update_pages", "pkv_compact_workspace_size", "pkv_compact_pages",
+            "pkv_status_string",
             "pkv_status_from_device_error", "pkv_last_cuda_error_string")
 
 
@@ -108,6 +118,26 @@ def load_library() -> ctypes.CDLL:
     lib.pkv_mixed_attention.restype = c_int
     lib.pkv_stage_from_host.argtypes = [vp, vp, c_size, vp]
     lib.pkv_stage_from_host.restype = c_int
+    lib.pkv_tree_workspace_size.argtypes = [desc_p, c_int, c_int, c_int]
+    lib.pkv_tree_workspace_size.restype = c_size
+    lib.pkv_tree_attention.argtypes = [desc_p, vp, vp, i32p, vp, c_int, i32p, i32p, i32p, i32p,
+                                       c_int, c_int, c_float, vp, f32p, vp, c_size, i32p, vp]
+    lib.pkv_tree_attention.restype = c_int
+    lib.pkv_verify_tree.argtypes = [vp, vp, c_int, c_int, i32p, i32p, i32p, f32p, f32p, c_int,
+                                    c_int, i32p, i32p, i32p, i32p, vp]
+    lib.pkv_verify_tree.restype = c_int
+    lib.pkv_commit_path.argtypes = [desc_p, vp, vp, i32p, i32p, i32p, i32p, i32p, c_int, c_int,
+                                    i32p, i32p, vp]
+    lib.pkv_commit_path.restype = c_int
+    lib.pkv_update_workspace_size.argtypes = [desc_p, c_int]
+    lib.pkv_update_workspace_size.restype = c_size
+    lib.pkv_update_pages.argtypes = [desc_p, vp, vp, i32p, i32p, i32p, i32p, i32p, i32p, c_int,
+                                     vp, c_size, i32p, vp]
+    lib.pkv_update_pages.restype = c_int
+    lib.pkv_compact_workspace_size.argtypes = [desc_p]
+    lib.pkv_compact_workspace_size.restype = c_size
+    lib.pkv_compact_pages.argtypes = [desc_p, vp, vp, i32p, i32p, i32p, vp, c_size, i32p, vp]
+    lib.pkv_compact_pages.restype = c_int
     lib.pkv_status_string.argtypes = [c_int]
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error_string.argtypes = []
@@ -432,3 +462,219 @@ def pkv_stage_from_host(dst: torch.Tensor, src: torch.Tensor, stream=None) -> No
         raise ValueError("dst and src must hold the same number of bytes")
     st = load_library().pkv_stage_from_host(_ptr(dst), _ptr(src), nbytes, _stream(stream))
     _check("pkv_stage_from_host", st)
+
+
+def _rows(name: str, t: torch.Tensor, *shape: int) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _cache_args(k_pool, v_pool, page_table) -> None:
+    _need(k_pool, "k_pool", torch.bfloat16, 3)
+    _need(v_pool, "v_pool", torch.bfloat16, 3)
+    _need(page_table, "page_table", torch.int32, 2)
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have one shape")
+
+
+def _scratch(workspace, nbytes: int, device) -> torch.Tensor:
+    """The caller's workspace, or one of the size the call needs."""
+    if workspace is None:
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace
+
+
+def pkv_tree_workspace_size(k_pool, page_table, page_size: int, batch: int, n_nodes: int,
+                            num_q_heads: int) -> int:
+    desc = cache_desc(k_pool, page_table, page_size)
+    n = load_library().pkv_tree_workspace_size(ctypes.byref(desc), batch, n_nodes, num_q_heads)
+    if n == 0:
+        raise PkvError("pkv_tree_workspace_size", 1)
+    return int(n)
+
+
+def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_idx, ctx_lens,
+                       page_size: int, scale: float, out=None, lse=None, workspace=None,
+                       dev_err=None, stream=None):
+    """Attention of a tree of drafted tokens per sequence: node i of row b of
+    q [B, N, Hq, D] attends the ctx_lens[b] committed tokens of slot
+    batch_idx[b], itself and its ancestors by parents [B, N]; the nodes' own
+    K/V are in the pools at positions ctx_lens[b] + node (appended first).
+    Returns (out [B, N, Hq, D] bf16, lse [B, N, Hq] fp32)."""
+    _cache_args(k_pool, v_pool, page_table)
+    _need(q, "q", torch.bfloat16, 4)
+    for name, t, nd in (("parents", parents, 2), ("tree_lens", tree_lens, 1),
+                        ("batch_idx", batch_idx, 1), ("ctx_lens", ctx_lens, 1)):
+        _need(t, name, torch.int32, nd)
+    B, N, hq, d = q.shape
+    if d != k_pool.shape[2]:
+        raise ValueError("q and the pools must have one head dim")
+    _rows("parents", parents, B, N)
+    for name, t in (("tree_lens", tree_lens), ("batch_idx", batch_idx), ("ctx_lens", ctx_lens)):
+        _rows(name, t, B)
+    if out is None:
+        out = torch.empty((B, N, hq, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", torch.bfloat16, 4)
+        _rows("out", out, B, N, hq, d)
+    if lse is None:
+        lse = torch.empty((B, N, hq), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", torch.float32, 3)
+        _rows("lse", lse, B, N, hq)
+    desc = cache_desc(k_pool, page_table, page_size)
+    lib = load_library()
+    need = 0
+    if workspace is None:
+        need = lib.pkv_tree_workspace_size(ctypes.byref(desc), B, N, hq)
+    workspace = _scratch(workspace, need, q.device)
+    st = lib.pkv_tree_attention(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(q), hq,
+        _ptr(parents), _ptr(tree_lens), _ptr(batch_idx), _ptr(ctx_lens), B, N, float(scale),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_err), _stream(stream))
+    _check("pkv_tree_attention", st)
+    return out, lse
+
+
+_PROBS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_sample,
+                    draft_probs=None, path=None, tokens=None, n_accepted=None, dev_err=None,
+                    stream=None):
+    """Acceptance of drafted tokens against the target's probabilities
+    target_probs [B, N, V] (fp32 or bf16), from the random numbers u_accept
+    [B, N] and u_sample [B]; draft_probs is like target_probs, or None for
+    guessed tokens. Returns (path [B, N], tokens [B, N], n_accepted [B])
+    int32: the accepted nodes, their tokens and the next one."""
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dtype not in _PROBS_TYPES:
+        raise ValueError("target_probs must be an fp32 or bf16 tensor")
+    kind = target_probs.dtype
+    _need(target_probs, "target_probs", kind, 3)
+    B, N, V = target_probs.shape
+    if draft_probs is not None:
+        _need(draft_probs, "draft_probs", kind, 3)
+        _rows("draft_probs", draft_probs, B, N, V)
+    for name, t, dt, shape in (("draft_tokens", draft_tokens, torch.int32, (B, N)),
+                               ("parents", parents, torch.int32, (B, N)),
+                               ("tree_lens", tree_lens, torch.int32, (B,)),
+                               ("u_accept", u_accept, torch.float32, (B, N)),
+                               ("u_sample", u_sample, torch.float32, (B,))):
+        _need(t, name, dt, len(shape))
+        _rows(name, t, *shape)
+    outs = []
+    for name, t, shape in (("path", path, (B, N)), ("tokens", tokens, (B, N)),
+                           ("n_accepted", n_accepted, (B,))):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=target_probs.device)
+        else:
+            _need(t, name, torch.int32, len(shape))
+            _rows(name, t, *shape)
+        outs.append(t)
+    st = load_library().pkv_verify_tree(
+        _ptr(target_probs), _ptr(draft_probs), _PROBS_TYPES[kind], V, _ptr(draft_tokens),
+        _ptr(parents), _ptr(tree_lens), _ptr(u_accept), _ptr(u_sample), B, N, _ptr(outs[0]),
+        _ptr(outs[1]), _ptr(outs[2]), _ptr(dev_err), _stream(stream))
+    _check("pkv_verify_tree", st)
+    return tuple(outs)
+
+
+def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx_lens,
+                    page_size: int, new_lens=None, dev_err=None, stream=None):
+    """Moves the K/V rows of the accepted nodes path[b, :n_accepted[b]] from
+    positions ctx_lens[b] + node to ctx_lens[b], ctx_lens[b] + 1, ... in
+    place. Returns new_lens [B] = ctx_lens + n_accepted (``new_lens`` may be
+    ctx_lens itself)."""
+    _cache_args(k_pool, v_pool, page_table)
+    _need(path, "path", torch.int32, 2)
+    B, N = path.shape
+    for name, t in (("n_accepted", n_accepted), ("batch_idx", batch_idx),
+                    ("ctx_lens", ctx_lens)):
+        _need(t, name, torch.int32, 1)
+        _rows(name, t, B)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=path.device)
+    else:
+        _need(new_lens, "new_lens", torch.int32, 1)
+        _rows("new_lens", new_lens, B)
+    desc = cache_desc(k_pool, page_table, page_size)
+    st = load_library().pkv_commit_path(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(path),
+        _ptr(n_accepted), _ptr(batch_idx), _ptr(ctx_lens), B, N, _ptr(new_lens), _ptr(dev_err),
+        _stream(stream))
+    _check("pkv_commit_path", st)
+    return new_lens
+
+
+def pkv_update_workspace_size(k_pool, page_table, page_size: int, n: int) -> int:
+    desc = cache_desc(k_pool, page_table, page_size)
+    size = load_library().pkv_update_workspace_size(ctypes.byref(desc), n)
+    if size == 0:
+        raise PkvError("pkv_update_workspace_size", 1)
+    return int(size)
+
+
+def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots, keep_lens,
+                     new_lens, page_size: int, workspace=None, dev_err=None,
+                     stream=None) -> None:
+    """Fork, reserve, copy on write, truncate and free, in place: slot
+    dst_slots[i] gets the first keep_lens[i] tokens of slot src_slots[i] (pages
+    shared) and pages of its own for the positions up to new_lens[i].
+    page_refs [num_pages] counts the table entries that use each page (0: free)."""
+    _cache_args(k_pool, v_pool, page_table)
+    _need(page_refs, "page_refs", torch.int32, 1)
+    _need(dst_slots, "dst_slots", torch.int32, 1)
+    n = dst_slots.numel()
+    for name, t in (("src_slots", src_slots), ("keep_lens", keep_lens), ("new_lens", new_lens)):
+        _need(t, name, torch.int32, 1)
+        _rows(name, t, n)
+    desc = cache_desc(k_pool, page_table, page_size)
+    _rows("page_refs", page_refs, desc.num_pages)
+    lib = load_library()
+    need = 0
+    if workspace is None:
+        need = lib.pkv_update_workspace_size(ctypes.byref(desc), n)
+    workspace = _scratch(workspace, need, k_pool.device)
+    st = lib.pkv_update_pages(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(page_refs),
+        _ptr(dst_slots), _ptr(src_slots), _ptr(keep_lens), _ptr(new_lens), n, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream))
+    _check("pkv_update_pages", st)
+
+
+def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
+    desc = cache_desc(k_pool, page_table, page_size)
+    size = load_library().pkv_compact_workspace_size(ctypes.byref(desc))
+    if size == 0:
+        raise PkvError("pkv_compact_workspace_size", 1)
+    return int(size)
+
+
+def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num_live=None,
+                      workspace=None, dev_err=None, stream=None):
+    """Moves the live pages to the low end of the pool (K/V rows, table
+    entries and counts), in place. Returns num_live [1], how many there are."""
+    _cache_args(k_pool, v_pool, page_table)
+    _need(page_refs, "page_refs", torch.int32, 1)
+    desc = cache_desc(k_pool, page_table, page_size)
+    _rows("page_refs", page_refs, desc.num_pages)
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=k_pool.device)
+    else:
+        _need(num_live, "num_live", torch.int32, 1)
+        _rows("num_live", num_live, 1)
+    lib = load_library()
+    need = 0
+    if workspace is None:
+        need = lib.pkv_compact_workspace_size(ctypes.byref(desc))
+    workspace = _scratch(workspace, need, k_pool.device)
+    st = lib.pkv_compact_pages(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(page_refs),
+        _ptr(num_live), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_err), _stream(stream))
+    _check("pkv_compact_pages", st)
+    return num_live

@@ -41,7 +41,10 @@ struct DeviceInfo {
 
 constexpr int kMaxDevices = 64;
 
-// SM count and architecture of `dev`, queried once per device.
+}  // namespace
+
+namespace pkv {
+
 pkv_status device_info(int* sm_count) {
   static DeviceInfo cache[kMaxDevices];
   static std::mutex mu;
@@ -68,11 +71,22 @@ pkv_status device_info(int* sm_count) {
   return PKV_OK;
 }
 
+}  // namespace pkv
+
+namespace {
+
+using pkv::check_cache;
+using pkv::device_info;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
 pkv_status cuda_status(cudaError_t e) { return pkv::record_cuda_status(e); }
+
+}  // namespace
+
+namespace pkv {
 
 pkv_status check_cache(const pkv_cache_desc* c) {
   if (c == nullptr) return PKV_ERR_ARG;
@@ -84,6 +98,10 @@ pkv_status check_cache(const pkv_cache_desc* c) {
   if (static_cast<long long>(c->max_batch) * c->max_blocks > INT_MAX) return PKV_ERR_ARG;
   return PKV_OK;
 }
+
+}  // namespace pkv
+
+namespace {
 
 bool group_ok(int num_q_heads, int num_kv_heads) {
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return false;

@@ -104,6 +104,13 @@ cudaError_t launch_append_rope(const AppendRopeParams& p, cudaStream_t stream);
 // pkv_last_cuda_error_string() and returns PKV_ERR_CUDA.
 pkv_status record_cuda_status(cudaError_t e);
 
+// PKV_OK for a geometry that the calls serve (pkv_api.cu).
+pkv_status check_cache(const pkv_cache_desc* c);
+
+// SM count of the current device, PKV_ERR_DEVICE unless it is an sm_103
+// (pkv_api.cu; queried once per device).
+pkv_status device_info(int* sm_count);
+
 // Validation and launch of pkv_prefill_attention (pkv_prefill.cu).
 pkv_status prefill_entry(const void* q, const void* k, const void* v, int num_q_heads,
                          int num_kv_heads, int head_dim, const int32_t* batch_idx,

@@ -509,5 +509,24 @@ inline bool encode_packed_map(CUtensorMap* map, const void* base, int heads, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+
+// 4-D view {64 dims, rows, 2 halves of the head dims, H_kv} of a pool; one box
+// is `box_rows` rows of one half of one head, 128-byte swizzled, so a box of
+// page k of a 128-key tile lands at rows k * box_rows.. of that half.
+inline bool encode_pool_box_map(CUtensorMap* map, const void* pool, const pkv_cache_desc* c,
+                                int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(c->num_pages) * c->page_size, 2u,
+                              static_cast<cuuint64_t>(c->num_kv_heads)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->num_kv_heads) * c->head_dim * 2,
+                                 128u, static_cast<cuuint64_t>(c->head_dim) * 2};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace prefill_host
 }  // namespace pkv

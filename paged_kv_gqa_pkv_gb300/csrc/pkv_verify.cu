@@ -1,0 +1,603 @@
+// pkv_verify.cu - pkv_verify_tree: which drafted tokens the target accepts,
+// and the token that follows them.
+//
+// At a node with target row p and draft row q the children are tried one after
+// another; each refusal replaces the residual r by max(r - R q, 0) and R by its
+// sum. Nested residuals collapse: max(max(p - a q, 0) - R q, 0) =
+// max(p - (a + R) q, 0) for R >= 0, so the whole state at a node is one scalar a
+// (a_0 = 0, R_0 = 1, a_{k+1} = a_k + R_k), and a refusal costs one pass over the
+// two rows, R = sum_v max(p - a q, 0), with nothing written. An acceptance costs
+// two numbers. Without draft rows a refusal only takes p(tok) off R.
+//
+// What bounds it: the passes' bytes (one or two rows of `vocab` values for each
+// refusal and for the draw), so a row of the call is shared by a cluster of
+// CTAs, each with a contiguous part of the vocabulary, whose sums meet in
+// distributed shared memory; with few rows it is the latency of the walk's
+// dependent steps, so every number the walk may ask for (each node's token, its
+// p and q at the parent) is gathered by one thread per node up front, and every
+// warp of every CTA then takes the same decisions from shared memory, with one
+// cluster barrier per pass and none per decision.
+//
+// Arithmetic: a drawn number next to a border has to fall on the side that exact
+// sums give, and fp32 sums of 10^5 terms move borders by more than a token's
+// probability. Doubles are slow on this GPU (two per cycle and SM), so a term
+// p - a q and a thread's running sum are kept as unevaluated pairs of floats by
+// the classical error-free sum and product (Knuth, Dekker; the product's error
+// by an FMA), about 48 bits; the few sums per warp, CTA and cluster are doubles,
+// always added in the same order. p and q are exact in fp32 whatever their type.
+#include "pkv.h"
+#include "pkv_launch.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kNodes = PKV_MAX_TREE_NODES;
+constexpr int kUnroll = 4;  // 16-byte loads per row and thread in flight
+
+struct VerifyParams {
+  const void* target;
+  const void* draft;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* tree_lens;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* path;
+  int32_t* out_tokens;
+  int32_t* n_accepted;
+  int32_t* dev_err;
+  int n_nodes;
+  int vocab;
+  int cluster;  // CTAs per row
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *(the same shared-memory location in CTA `rank` of the cluster) = v
+__device__ __forceinline__ void cluster_store(double* at, uint32_t rank, double v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
+}
+
+// Unevaluated sum of two floats.
+struct Pair {
+  float hi, lo;
+};
+
+// s = a + b, with the rounding error of s (exact whatever their magnitudes).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+
+// Negative and NaN entries count as 0.
+__device__ __forceinline__ float clean(float x) { return fmaxf(x, 0.f); }
+
+// max(p - (ah + al) q, 0)
+__device__ __forceinline__ Pair residual(float p, float q, float ah, float al) {
+  const float prod = __fmul_rn(ah, q);
+  const float perr = __fmaf_rn(ah, q, -prod);
+  const Pair d = two_sum(p, -prod);
+  const float lo = __fsub_rn(__fsub_rn(d.lo, perr), __fmul_rn(al, q));
+  const bool pos = __fadd_rn(d.hi, lo) > 0.f || p == INFINITY;  // (infinite: the sum tells)
+  return {pos ? d.hi : 0.f, pos ? lo : 0.f};
+}
+
+__device__ __forceinline__ void add(Pair& s, const Pair& x) {
+  const Pair t = two_sum(s.hi, x.hi);
+  s.hi = t.hi;
+  s.lo = __fadd_rn(s.lo, __fadd_rn(t.lo, x.lo));
+}
+
+__device__ __forceinline__ double value(const Pair& x) {
+  return static_cast<double>(x.hi) + static_cast<double>(x.lo);
+}
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kPer = 4;  // values per 16-byte granule
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = bf16lo(u[k]);
+      x[2 * k + 1] = bf16hi(u[k]);
+    }
+  }
+};
+
+// One row of `vocab` values, read in 16-byte granules from the aligned address
+// at or below its start: value v sits at index v + off of the granules, and the
+// first and last granule are read value by value where they hang over.
+template <typename T>
+struct RowView {
+  const T* base;  // 16-byte aligned
+  int off;        // values of the first granule in front of the row
+  int end;        // off + vocab
+  __device__ __forceinline__ RowView(const void* all, int64_t row, int vocab) {
+    const T* start = static_cast<const T*>(all) + row * vocab;
+    off = static_cast<int>((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
+    base = start - off;
+    end = off + vocab;
+  }
+  __device__ __forceinline__ bool inside(int g) const {
+    return g * Elem<T>::kPer >= off && (g + 1) * Elem<T>::kPer <= end;
+  }
+  __device__ __forceinline__ uint4 whole(int g) const {
+    return *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(g) * Elem<T>::kPer);
+  }
+  // values outside the row read as 0
+  __device__ __forceinline__ void values(int g, float (&x)[Elem<T>::kPer]) const {
+    if (inside(g)) {
+      Elem<T>::unpack(whole(g), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < Elem<T>::kPer; ++e) {
+        const int i = g * Elem<T>::kPer + e;
+        x[e] = i >= off && i < end ? Elem<T>::get(base + i) : 0.f;
+      }
+    }
+  }
+};
+
+struct Shared {
+  int parent[kNodes], token[kNodes];
+  float p[kNodes], q[kNodes], u[kNodes];
+  int path[kNodes];
+  int refused[kNodes];                // tokens refused at the current node (no draft rows)
+  double warp_sum[kWarps];            // of the last pass, this CTA's warps
+  double cta_sum[2][kMaxCluster];     // of the last two passes, all CTAs
+};
+
+// What a pass sums: max(p - a q, 0) with the `n_refused` tokens left out.
+struct Residual {
+  double a;
+  int n_refused;
+};
+
+template <typename T, bool kDraft>
+struct Walk {
+  const VerifyParams& p;
+  Shared& s;
+  const int64_t row0;  // this sequence's first row
+  const uint32_t rank;
+  const int lane, warp;
+  int passes = 0;
+
+  // granules [g0, g1) of the row at node c are this warp's
+  __device__ __forceinline__ void my_range(const RowView<T>& v, int& g0, int& g1) const {
+    const int total = (v.end + Elem<T>::kPer - 1) / Elem<T>::kPer;
+    const int warps = p.cluster * kWarps;
+    const int per = ((total + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t w = static_cast<int64_t>(rank) * kWarps + warp;
+    g0 = static_cast<int>(w * per < total ? w * per : total);
+    g1 = static_cast<int>((w + 1) * per < total ? (w + 1) * per : total);
+  }
+
+  // the residual's terms of one granule
+  __device__ __forceinline__ void terms(const Residual& r, float ah, float al, int g, int off,
+                                        const float (&x)[Elem<T>::kPer],
+                                        const float (&y)[Elem<T>::kPer],
+                                        Pair (&t)[Elem<T>::kPer]) const {
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kPer; ++e) {
+      if constexpr (kDraft) t[e] = residual(clean(x[e]), clean(y[e]), ah, al);
+      else t[e] = {clean(x[e]), 0.f};
+    }
+    if constexpr (!kDraft) {
+      for (int k = 0; k < r.n_refused; ++k) {
+        const int at = s.refused[k] + off - g * Elem<T>::kPer;
+#pragma unroll
+        for (int e = 0; e < Elem<T>::kPer; ++e)
+          if (at == e) t[e].hi = 0.f;
+      }
+    }
+  }
+
+  // Sum of the residual at node c over the whole vocabulary, the same double in
+  // every thread of the cluster. Every thread of the cluster calls it.
+  __device__ double sum(int c, const Residual& r) {
+    const RowView<T> pv(p.target, row0 + c, p.vocab);
+    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + c, p.vocab);
+    const bool with_q = kDraft && r.a != 0.0;
+    const float ah = static_cast<float>(r.a);
+    const float al = static_cast<float>(r.a - static_cast<double>(ah));
+    int g0, g1;
+    my_range(pv, g0, g1);
+    constexpr int E = Elem<T>::kPer;
+    Pair acc = {0.f, 0.f};
+    float y0[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y0[e] = 0.f;
+    for (int g = g0 + lane; g < g1; g += 32 * kUnroll) {
+      uint4 xw[kUnroll], yw[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = g + 32 * u;
+        if (i < g1 && pv.inside(i)) {
+          xw[u] = pv.whole(i);
+          if (with_q) yw[u] = qv.whole(i);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = g + 32 * u;
+        if (i >= g1) break;
+        float x[E], y[E];
+        if (pv.inside(i)) {
+          Elem<T>::unpack(xw[u], x);
+          if (with_q) Elem<T>::unpack(yw[u], y);
+        } else {
+          pv.values(i, x);
+          if (with_q) qv.values(i, y);
+        }
+        Pair t[E];
+        if (with_q) terms(r, ah, al, i, pv.off, x, y, t);
+        else terms(r, ah, al, i, pv.off, x, y0, t);
+#pragma unroll
+        for (int e = 0; e < E; ++e) add(acc, t[e]);
+      }
+    }
+    double w = value(acc);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    __syncthreads();  // the previous pass's warp sums have been read
+    if (lane == 0) s.warp_sum[warp] = w;
+    __syncthreads();
+    double mine = 0.0;
+    for (int k = 0; k < kWarps; ++k) mine += s.warp_sum[k];
+    double* slots = s.cta_sum[passes & 1];
+    if (threadIdx.x < static_cast<unsigned>(p.cluster)) cluster_store(&slots[rank], threadIdx.x, mine);
+    // one barrier per pass: the next pass writes the other half, and the one
+    // after that follows a barrier that every CTA reaches after these reads
+    __syncwarp();
+    cluster_sync();
+    ++passes;
+    double total = 0.0;
+    for (int k = 0; k < p.cluster; ++k) total += slots[k];
+    return total;
+  }
+
+  // The token drawn at t of the last pass's sum, by the one warp of the cluster
+  // that holds it; -1 in the other warps.
+  __device__ int draw(int c, const Residual& r, double t) const {
+    const double* slots = s.cta_sum[(passes - 1) & 1];
+    // the first CTA, then the first warp, whose running sum passes t; where
+    // rounding leaves none, the last one with any mass, and its last token
+    double base = 0.0;
+    int cta = -1, last = 0;
+    double cta_base = 0.0, last_base = 0.0;
+    for (int k = 0; k < p.cluster; ++k) {
+      if (slots[k] > 0.0) {
+        last = k;
+        last_base = base;
+      }
+      if (cta < 0 && base + slots[k] > t) {
+        cta = k;
+        cta_base = base;
+      }
+      base += slots[k];
+    }
+    if (cta < 0) {
+      cta = last;
+      cta_base = last_base;
+    }
+    if (static_cast<int>(rank) != cta) return -1;
+    base = cta_base;
+    int w = -1, last_w = 0;
+    double w_base = 0.0, last_w_base = 0.0;
+    for (int k = 0; k < kWarps; ++k) {
+      if (s.warp_sum[k] > 0.0) {
+        last_w = k;
+        last_w_base = base;
+      }
+      if (w < 0 && base + s.warp_sum[k] > t) {
+        w = k;
+        w_base = base;
+      }
+      base += s.warp_sum[k];
+    }
+    if (w < 0) {
+      w = last_w;
+      w_base = last_w_base;
+    }
+    if (warp != w) return -1;
+
+    const RowView<T> pv(p.target, row0 + c, p.vocab);
+    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + c, p.vocab);
+    const float ah = static_cast<float>(r.a);
+    const float al = static_cast<float>(r.a - static_cast<double>(ah));
+    int g0, g1;
+    my_range(pv, g0, g1);
+    constexpr int E = Elem<T>::kPer;
+    int highest = -1;  // the highest token with mass seen by this lane
+    base = w_base;
+    for (int s0 = g0; s0 < g1; s0 += 32) {
+      const int g = s0 + lane;
+      Pair tm[E];
+      Pair acc = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) tm[e] = {0.f, 0.f};
+      if (g < g1) {
+        float x[E], y[E];
+        pv.values(g, x);
+        qv.values(g, y);
+        if (!kDraft || r.a == 0.0) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] = 0.f;
+        }
+        terms(r, ah, al, g, pv.off, x, y, tm);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          add(acc, tm[e]);
+          if (value(tm[e]) > 0.0) highest = g * E + e - pv.off;
+        }
+      }
+      double incl = value(acc);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > t && value(acc) > 0.0);
+      if (past != 0u) {
+        const int owner = __ffs(past) - 1;
+        int at = -1;
+        if (lane == owner) {
+          // the same sums, value by value: the first past t, or the granule's
+          // last with mass where rounding leaves none
+          double run = base + incl - value(acc);
+          bool found = false;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const double x = value(tm[e]);
+            if (x > 0.0 && !found) {
+              at = g * E + e - pv.off;
+              run += x;
+              found = run > t;
+            }
+          }
+        }
+        return __shfl_sync(0xffffffffu, at, owner);
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) highest = max(highest, __shfl_xor_sync(0xffffffffu, highest, o));
+    return highest;
+  }
+};
+
+template <typename T, bool kDraft>
+__global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const VerifyParams p) {
+  __shared__ Shared s;
+  pdl_wait_primary();
+  const uint32_t rank = cluster_rank();
+  const int b = blockIdx.x / p.cluster;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int N = p.n_nodes;
+  const int64_t n0 = static_cast<int64_t>(b) * N;
+  int err = 0;
+  int len = p.tree_lens[b];
+  if (len < 0 || len > N) {
+    err = PKV_DEV_ERR_BAD_TREE;
+    len = 0;
+  }
+  if (len == 0) {  // the whole cluster leaves together
+    if (rank == 0) {
+      for (int i = threadIdx.x; i < N; i += kThreads) p.path[n0 + i] = p.out_tokens[n0 + i] = -1;
+      if (threadIdx.x == 0) {
+        p.n_accepted[b] = 0;
+        if (err) set_dev_err(p.dev_err, err);
+      }
+      __threadfence();
+    }
+    return;
+  }
+  if (threadIdx.x < kNodes) {
+    const int i = threadIdx.x;
+    int parent = -1, tok = 0;
+    float px = 0.f, qx = 0.f, u = 0.f;
+    if (i >= 1 && i < len) {
+      parent = p.parents[n0 + i];
+      tok = p.tokens[n0 + i];
+      u = p.u_accept[n0 + i];
+      if (parent < -1 || parent >= i || tok < 0 || tok >= p.vocab) {
+        err = PKV_DEV_ERR_BAD_TREE;
+        parent = -1;
+      }
+      if (parent >= 0) {
+        const int64_t at = (n0 + parent) * p.vocab + tok;
+        px = clean(Elem<T>::get(static_cast<const T*>(p.target) + at));
+        qx = kDraft ? clean(Elem<T>::get(static_cast<const T*>(p.draft) + at)) : 1.f;
+      }
+      if (err && rank == 0) set_dev_err(p.dev_err, err);
+    }
+    s.parent[i] = parent;
+    s.token[i] = tok;
+    s.p[i] = px;
+    s.q[i] = qx;
+    s.u[i] = u;
+  }
+  __syncthreads();
+
+  // every warp of the cluster walks alike
+  Walk<T, kDraft> walk{p, s, n0, rank, lane, warp};
+  const int par0 = s.parent[lane], par1 = s.parent[lane + 32];
+  int cur = 0, count = 1;
+  uint64_t on_path = 1;
+  Residual r = {0.0, 0};
+  double mass = 1.0;
+  bool summed = false;  // the last pass summed the residual at hand
+  while (true) {
+    uint64_t kids = static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == cur)) |
+                    static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == cur)) << 32;
+    int next = -1;
+    while (kids != 0) {
+      const int x = __ffsll(static_cast<long long>(kids)) - 1;
+      kids &= kids - 1;
+      const double px = s.p[x], qx = s.q[x];
+      double rx;
+      if constexpr (kDraft) {
+        rx = px - r.a * qx;
+        rx = rx > 0.0 ? rx : 0.0;
+      } else {
+        rx = px;
+        for (int k = 0; k < r.n_refused; ++k)
+          if (s.refused[k] == s.token[x]) rx = 0.0;
+      }
+      if (static_cast<double>(s.u[x]) * qx * mass < rx) {
+        next = x;
+        break;
+      }
+      if constexpr (kDraft) {
+        r.a += mass;
+        mass = walk.sum(cur, r);
+        summed = true;
+      } else {
+        mass = mass > rx ? mass - rx : 0.0;
+        __syncthreads();  // the list has been read by every warp
+        if (threadIdx.x == 0) s.refused[r.n_refused] = s.token[x];
+        __syncthreads();
+        ++r.n_refused;
+      }
+    }
+    if (next < 0) break;
+    cur = next;
+    ++count;
+    on_path |= 1ull << next;
+    r = {0.0, 0};
+    mass = 1.0;
+    summed = false;
+  }
+
+  double total = summed ? mass : walk.sum(cur, r);
+  if (total == 0.0 && (r.a != 0.0 || r.n_refused != 0)) {
+    r = {0.0, 0};  // nothing of the target is left: draw from all of it
+    total = walk.sum(cur, r);
+  }
+  const bool ok = total > 0.0 && total <= 1.7e308;
+  int drawn = -1;
+  if (ok) drawn = walk.draw(cur, r, static_cast<double>(p.u_sample[b]) * total);
+  if (lane == 0 && (ok ? drawn >= 0 : rank == 0 && warp == 0)) p.out_tokens[n0 + count - 1] = drawn;
+  if (rank == 0) {
+    if (threadIdx.x < kNodes && ((on_path >> threadIdx.x) & 1ull))
+      s.path[__popcll(on_path & ((1ull << threadIdx.x) - 1ull))] = threadIdx.x;
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += kThreads) {
+      p.path[n0 + i] = i < count ? s.path[i] : -1;
+      if (i != count - 1) p.out_tokens[n0 + i] = i < count - 1 ? s.token[s.path[i + 1]] : -1;
+    }
+    if (threadIdx.x == 0) {
+      p.n_accepted[b] = count;
+      if (!ok) set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PROBS);
+    }
+  }
+  // a programmatic dependent may read the results before this grid has drained
+  __threadfence();
+}
+
+// CTAs per row: a CTA reads about 60 bytes a cycle, so a long vocabulary is
+// spread over eight of them.
+int pick_cluster(int vocab) {
+  int c = 1;
+  while (c < kMaxCluster && vocab > c * 4096) c *= 2;
+  return c;
+}
+
+template <typename T, bool kDraft>
+cudaError_t launch(const VerifyParams& p, int batch, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch) * p.cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_tree_kernel<T, kDraft>, p);
+}
+
+bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_verify_tree(const void* target_probs, const void* draft_probs,
+                                      int probs_type, int vocab, const int32_t* draft_tokens,
+                                      const int32_t* parents, const int32_t* tree_lens,
+                                      const float* u_accept, const float* u_sample, int batch,
+                                      int n_nodes, int32_t* path, int32_t* tokens,
+                                      int32_t* n_accepted, int32_t* dev_err,
+                                      cudaStream_t stream) {
+  using namespace pkv;
+  if (probs_type != PKV_PROBS_FP32 && probs_type != PKV_PROBS_BF16) return PKV_ERR_ARG;
+  if (batch < 0 || batch > (1 << 24) || n_nodes < 1 || n_nodes > PKV_MAX_TREE_NODES)
+    return PKV_ERR_ARG;
+  if (vocab < 1 || vocab > (1 << 30)) return PKV_ERR_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!target_probs || !draft_tokens || !parents || !tree_lens || !u_accept || !u_sample || !path ||
+      !tokens || !n_accepted)
+    return PKV_ERR_ARG;
+  if (!aligned(target_probs, 16) || !aligned(draft_probs, 16) || !aligned(draft_tokens, 4) ||
+      !aligned(parents, 4) || !aligned(tree_lens, 4) || !aligned(u_accept, 4) ||
+      !aligned(u_sample, 4) || !aligned(path, 4) || !aligned(tokens, 4) ||
+      !aligned(n_accepted, 4) || !aligned(dev_err, 4))
+    return PKV_ERR_ALIGN;
+  int sms = 0;
+  const pkv_status st = device_info(&sms);
+  if (st != PKV_OK) return st;
+  VerifyParams p;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.tokens = draft_tokens;
+  p.parents = parents;
+  p.tree_lens = tree_lens;
+  p.u_accept = u_accept;
+  p.u_sample = u_sample;
+  p.path = path;
+  p.out_tokens = tokens;
+  p.n_accepted = n_accepted;
+  p.dev_err = dev_err;
+  p.n_nodes = n_nodes;
+  p.vocab = vocab;
+  p.cluster = pick_cluster(vocab);
+  cudaError_t e;
+  if (probs_type == PKV_PROBS_FP32)
+    e = draft_probs ? launch<float, true>(p, batch, stream) : launch<float, false>(p, batch, stream);
+  else
+    e = draft_probs ? launch<__nv_bfloat16, true>(p, batch, stream)
+                    : launch<__nv_bfloat16, false>(p, batch, stream);
+  return record_cuda_status(e);
+}
