@@ -77,6 +77,7 @@ namespace {
 
 using pkv::check_cache;
 using pkv::device_info;
+using pkv::encode_pool_map;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -109,6 +110,10 @@ bool group_ok(int num_q_heads, int num_kv_heads) {
   return g == 1 || g == 2 || g == 4 || g == 8;
 }
 
+}  // namespace
+
+namespace pkv {
+
 pkv_status encode_pool_map(CUtensorMap* map, const void* pool, const pkv_cache_desc* c) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return PKV_ERR_CUDA;
@@ -130,9 +135,6 @@ pkv_status encode_pool_map(CUtensorMap* map, const void* pool, const pkv_cache_d
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARG;
 }
 
-}  // namespace
-
-namespace pkv {
 pkv_status record_cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return PKV_OK;
   t_last_cuda_error = e;

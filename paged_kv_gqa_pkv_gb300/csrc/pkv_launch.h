@@ -111,6 +111,9 @@ pkv_status check_cache(const pkv_cache_desc* c);
 // (pkv_api.cu; queried once per device).
 pkv_status device_info(int* sm_count);
 
+// Tensor map of a pool whose boxes are one head's 16-token tiles (pkv_api.cu).
+pkv_status encode_pool_map(CUtensorMap* map, const void* pool, const pkv_cache_desc* c);
+
 // Validation and launch of pkv_prefill_attention (pkv_prefill.cu).
 pkv_status prefill_entry(const void* q, const void* k, const void* v, int num_q_heads,
                          int num_kv_heads, int head_dim, const int32_t* batch_idx,
