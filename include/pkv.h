@@ -434,7 +434,7 @@ size_t pkv_tree_workspace_size(const pkv_cache_desc* cache, int batch, int n_nod
  * bits. The K/V of a row's own nodes and context must be finite: a NaN or
  * infinity in one node's V reaches the other nodes of its row.
  * page_size must be 16, 32, 64 or a multiple of 128; scale finite and > 0.
- * batch may be any count >= 0 (above 192 rows the call runs as equal launches
+ * batch may be any count >= 0 (above 128 rows the call runs as equal launches
  * that share the workspace). workspace: at least pkv_tree_workspace_size()
  * bytes, 256-byte aligned, owned by the caller, no initialisation needed;
  * calls that share one must be stream-ordered. All tensors are device memory.
