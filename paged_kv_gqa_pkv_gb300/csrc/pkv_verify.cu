@@ -14,28 +14,28 @@
 // CTAs, each with a contiguous part of the vocabulary, whose sums meet in
 // distributed shared memory; with few rows it is the latency of the walk's
 // dependent steps, so every number the walk may ask for (each node's token, its
-// p and q at the parent) is gathered by one thread per node up front, and every
-// warp of every CTA then takes the same decisions from shared memory, with one
-// cluster barrier per pass and none per decision.
+// p and q at the parent) is gathered by one thread per node up front. The first
+// warp of every CTA then walks, all of the cluster's alike, and hands the other
+// warps the passes; a pass costs one cluster barrier, a decision none.
 //
 // Arithmetic: a drawn number next to a border has to fall on the side that exact
 // sums give, and fp32 sums of 10^5 terms move borders by more than a token's
-// probability. Doubles are slow on this GPU (two per cycle and SM), so a term
-// p - a q and a thread's running sum are kept as unevaluated pairs of floats by
-// the classical error-free sum and product (Knuth, Dekker; the product's error
-// by an FMA), about 48 bits; the few sums per warp, CTA and cluster are doubles,
-// always added in the same order. p and q are exact in fp32 whatever their type.
+// probability. A pass takes R = sum p - a sum q over the v with p > a q. Doubles are slow on this GPU (a warp's addition holds its SM's unit
+// for some sixteen cycles: every warp taking the decisions redundantly cost 9 us a
+// row), so terms and sums are unevaluated pairs of floats by the classical
+// error-free sum and product (Knuth, Dekker; the product's error by an FMA), about
+// 48 bits, added in a fixed order, two values per instruction (a pass is bound by
+// instruction issue about as much as by its bytes); doubles are left to the walking warp's few
+// decisions. p and q are exact in fp32 whatever their type.
 #include "pkv.h"
 #include "pkv_launch.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = PKV_MAX_TREE_NODES;
-constexpr int kUnroll = 4;  // 16-byte loads per row and thread in flight
 
 struct VerifyParams {
   const void* target;
@@ -63,13 +63,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// *(the same shared-memory location in CTA `rank` of the cluster) = v
-__device__ __forceinline__ void cluster_store(double* at, uint32_t rank, double v) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
-}
-
 // Unevaluated sum of two floats.
 struct Pair {
   float hi, lo;
@@ -91,8 +84,10 @@ __device__ __forceinline__ Pair residual(float p, float q, float ah, float al) {
   const float perr = __fmaf_rn(ah, q, -prod);
   const Pair d = two_sum(p, -prod);
   const float lo = __fsub_rn(__fsub_rn(d.lo, perr), __fmul_rn(al, q));
-  const bool pos = __fadd_rn(d.hi, lo) > 0.f || p == INFINITY;  // (infinite: the sum tells)
-  return {pos ? d.hi : 0.f, pos ? lo : 0.f};
+  const Pair r = two_sum(d.hi, lo);
+  const bool pos = r.hi > 0.f;
+  if (p == INFINITY) return {p, 0.f};  // (the sum tells)
+  return {pos ? r.hi : 0.f, pos ? r.lo : 0.f};
 }
 
 __device__ __forceinline__ void add(Pair& s, const Pair& x) {
@@ -100,6 +95,71 @@ __device__ __forceinline__ void add(Pair& s, const Pair& x) {
   s.hi = t.hi;
   s.lo = __fadd_rn(s.lo, __fadd_rn(t.lo, x.lo));
 }
+
+__device__ __forceinline__ Pair shfl_xor(const Pair& x, int o) {
+  return {__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+}
+
+// Sum over the warp's 32 lanes, the same bits in every lane: the two partners of
+// a step add in one order.
+__device__ __forceinline__ Pair warp_sum(Pair x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair y = shfl_xor(x, o);
+    Pair a = (lane & o) ? y : x;
+    add(a, (lane & o) ? x : y);
+    x = a;
+  }
+  return x;
+}
+
+// *(the same shared-memory location in CTA `rank` of the cluster) = v
+__device__ __forceinline__ void cluster_store(double* at, uint32_t rank, double v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
+}
+
+// Two floats per instruction.
+using Two = unsigned long long;
+__device__ __forceinline__ Two pack2(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(Two v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Two running pair sums side by side.
+struct Sum2 {
+  Two hi, lo;
+  __device__ __forceinline__ void add(Two x) {
+    const Two minus = pack2(-1.f, -1.f);
+    const Two t = add2(hi, x);
+    const Two bb = fma2(hi, minus, t);                   // t - hi, exactly rounded like it
+    const Two e1 = fma2(fma2(bb, minus, t), minus, hi);  // hi - (t - bb)
+    lo = add2(lo, add2(e1, fma2(bb, minus, x)));
+    hi = t;
+  }
+  __device__ __forceinline__ Pair total() const {
+    Pair a, b;
+    unpack2(hi, a.hi, b.hi);
+    unpack2(lo, a.lo, b.lo);
+    const Pair t = two_sum(a.hi, b.hi);
+    return {t.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), t.lo)};
+  }
+};
 
 __device__ __forceinline__ double value(const Pair& x) {
   return static_cast<double>(x.hi) + static_cast<double>(x.lo);
@@ -166,22 +226,29 @@ struct RowView {
   }
 };
 
-struct Shared {
-  int parent[kNodes], token[kNodes];
-  float p[kNodes], q[kNodes], u[kNodes];
-  int path[kNodes];
-  int refused[kNodes];                // tokens refused at the current node (no draft rows)
-  double warp_sum[kWarps];            // of the last pass, this CTA's warps
-  double cta_sum[2][kMaxCluster];     // of the last two passes, all CTAs
-};
-
-// What a pass sums: max(p - a q, 0) with the `n_refused` tokens left out.
+// What a pass sums: max(p - a q, 0) with the refused tokens left out.
 struct Residual {
   double a;
   int n_refused;
 };
 
-template <typename T, bool kDraft>
+enum : int { kSum, kDraw, kLeave };
+
+struct Shared {
+  int parent[kNodes], token[kNodes];
+  float p[kNodes], q[kNodes], u[kNodes];
+  int path[kNodes];
+  int refused[kNodes];                // tokens refused at the current node (no draft rows)
+  Pair warp_p[kMaxWarps];             // sums of p and q over the residual's tokens of the
+  Pair warp_q[kMaxWarps];             // last pass, this CTA's warps
+  double cta_sum[2][kMaxCluster];     // the residual's, of the last two passes, all CTAs
+  // the walking warp's order to the others
+  int order, node, n_refused, draw_warp, count;
+  float ah, al;
+  double a, draw_at, draw_base;
+};
+
+template <typename T, bool kDraft, int kWarps>
 struct Walk {
   const VerifyParams& p;
   Shared& s;
@@ -201,7 +268,7 @@ struct Walk {
   }
 
   // the residual's terms of one granule
-  __device__ __forceinline__ void terms(const Residual& r, float ah, float al, int g, int off,
+  __device__ __forceinline__ void terms(float ah, float al, int g, int off,
                                         const float (&x)[Elem<T>::kPer],
                                         const float (&y)[Elem<T>::kPer],
                                         Pair (&t)[Elem<T>::kPer]) const {
@@ -211,7 +278,7 @@ struct Walk {
       else t[e] = {clean(x[e]), 0.f};
     }
     if constexpr (!kDraft) {
-      for (int k = 0; k < r.n_refused; ++k) {
+      for (int k = 0; k < s.n_refused; ++k) {
         const int at = s.refused[k] + off - g * Elem<T>::kPer;
 #pragma unroll
         for (int e = 0; e < Elem<T>::kPer; ++e)
@@ -220,21 +287,18 @@ struct Walk {
     }
   }
 
-  // Sum of the residual at node c over the whole vocabulary, the same double in
-  // every thread of the cluster. Every thread of the cluster calls it.
-  __device__ double sum(int c, const Residual& r) {
-    const RowView<T> pv(p.target, row0 + c, p.vocab);
-    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + c, p.vocab);
-    const bool with_q = kDraft && r.a != 0.0;
-    const float ah = static_cast<float>(r.a);
-    const float al = static_cast<float>(r.a - static_cast<double>(ah));
+  // This warp's part of the ordered sums: p and q over the tokens with p > a q.
+  __device__ __forceinline__ void sum_part() const {
+    const RowView<T> pv(p.target, row0 + s.node, p.vocab);
+    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
+    const float ah = s.ah, al = s.al;
+    const bool with_q = kDraft && ah != 0.f;
     int g0, g1;
     my_range(pv, g0, g1);
     constexpr int E = Elem<T>::kPer;
-    Pair acc = {0.f, 0.f};
-    float y0[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) y0[e] = 0.f;
+    constexpr int kUnroll = 16 / E;  // 16-byte loads per row and thread in flight
+    Sum2 ps = {0ull, 0ull}, qs = {0ull, 0ull};
+    const Two mah = pack2(-ah, -ah), mal = pack2(-al, -al);
     for (int g = g0 + lane; g < g1; g += 32 * kUnroll) {
       uint4 xw[kUnroll], yw[kUnroll];
 #pragma unroll
@@ -248,7 +312,7 @@ struct Walk {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int i = g + 32 * u;
-        if (i >= g1) break;
+        if (i >= g1) continue;
         float x[E], y[E];
         if (pv.inside(i)) {
           Elem<T>::unpack(xw[u], x);
@@ -257,87 +321,132 @@ struct Walk {
           pv.values(i, x);
           if (with_q) qv.values(i, y);
         }
-        Pair t[E];
-        if (with_q) terms(r, ah, al, i, pv.off, x, y, t);
-        else terms(r, ah, al, i, pv.off, x, y0, t);
 #pragma unroll
-        for (int e = 0; e < E; ++e) add(acc, t[e]);
+        for (int e = 0; e < E; ++e) {
+          x[e] = clean(x[e]);
+          if (with_q) y[e] = clean(y[e]);
+        }
+        if (with_q) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            // p - a q to single rounding twice: its sign is that of the exact
+            // difference unless that is below 2^-48 of its terms
+            const Two x2 = pack2(x[e], x[e + 1]), y2 = pack2(y[e], y[e + 1]);
+            float d0, d1;
+            unpack2(fma2(mal, y2, fma2(mah, y2, x2)), d0, d1);
+            // (an infinite p tells itself by the sum)
+            ps.add(pack2(d0 > 0.f ? x[e] : 0.f, d1 > 0.f ? x[e + 1] : 0.f));
+            qs.add(pack2(d0 > 0.f ? y[e] : 0.f, d1 > 0.f ? y[e + 1] : 0.f));
+          }
+        } else {
+          if constexpr (!kDraft) {
+            for (int k = 0; k < s.n_refused; ++k) {
+              const int at = s.refused[k] + pv.off - i * E;
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if (at == e) x[e] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < E; e += 2) ps.add(pack2(x[e], x[e + 1]));
+        }
       }
     }
-    double w = value(acc);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-    __syncthreads();  // the previous pass's warp sums have been read
-    if (lane == 0) s.warp_sum[warp] = w;
+    const Pair sp = warp_sum(ps.total(), lane);
+    Pair sq = {0.f, 0.f};
+    if (with_q) sq = warp_sum(qs.total(), lane);
+    if (lane == 0) {
+      s.warp_p[warp] = sp;
+      s.warp_q[warp] = sq;
+    }
+  }
+
+  // sum p - a sum q, not below 0
+  __device__ __forceinline__ double mass_of(const Pair& sp, const Pair& sq) const {
+    const double r = value(sp) - s.a * value(sq);
+    return r < 0.0 ? 0.0 : r;
+  }
+
+  // The walking warp: sum of the residual at node c over the whole vocabulary,
+  // the same double in every lane of every CTA of the cluster.
+  __device__ double sum(int c, const Residual& r) {
+    if (lane == 0) {
+      s.order = kSum;
+      s.node = c;
+      s.n_refused = r.n_refused;
+      s.a = r.a;
+      s.ah = static_cast<float>(r.a);
+      s.al = static_cast<float>(r.a - static_cast<double>(s.ah));
+    }
     __syncthreads();
-    double mine = 0.0;
-    for (int k = 0; k < kWarps; ++k) mine += s.warp_sum[k];
+    sum_part();
+    __syncthreads();
+    Pair sp = {0.f, 0.f}, sq = {0.f, 0.f};
+    if (lane < kWarps) {
+      sp = s.warp_p[lane];
+      sq = s.warp_q[lane];
+    }
+    const double mine = mass_of(warp_sum(sp, lane), warp_sum(sq, lane));
     double* slots = s.cta_sum[passes & 1];
-    if (threadIdx.x < static_cast<unsigned>(p.cluster)) cluster_store(&slots[rank], threadIdx.x, mine);
+    if (lane < p.cluster) cluster_store(&slots[rank], lane, mine);
     // one barrier per pass: the next pass writes the other half, and the one
     // after that follows a barrier that every CTA reaches after these reads
     __syncwarp();
     cluster_sync();
     ++passes;
-    double total = 0.0;
-    for (int k = 0; k < p.cluster; ++k) total += slots[k];
-    return total;
+    double all = lane < p.cluster ? slots[lane] : 0.0;
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    return __shfl_sync(0xffffffffu, all, 0);
   }
 
-  // The token drawn at t of the last pass's sum, by the one warp of the cluster
-  // that holds it; -1 in the other warps.
-  __device__ int draw(int c, const Residual& r, double t) const {
+  // The walking warp: which CTA and warp hold the token drawn at t of the last
+  // pass's sum, and what lies in front of them: the first whose running sum passes
+  // t, or where rounding leaves none the last one with any mass.
+  __device__ __forceinline__ void place(double t) {
     const double* slots = s.cta_sum[(passes - 1) & 1];
-    // the first CTA, then the first warp, whose running sum passes t; where
-    // rounding leaves none, the last one with any mass, and its last token
     double base = 0.0;
-    int cta = -1, last = 0;
-    double cta_base = 0.0, last_base = 0.0;
-    for (int k = 0; k < p.cluster; ++k) {
-      if (slots[k] > 0.0) {
-        last = k;
-        last_base = base;
-      }
-      if (cta < 0 && base + slots[k] > t) {
-        cta = k;
-        cta_base = base;
-      }
-      base += slots[k];
+    const int cta = pick(lane < p.cluster ? slots[lane] : 0.0, t, base);
+    int w = -1;
+    if (static_cast<int>(rank) == cta)
+      w = pick(lane < kWarps ? mass_of(s.warp_p[lane], s.warp_q[lane]) : 0.0, t, base);
+    if (lane == 0) {
+      s.order = kDraw;
+      s.draw_warp = w;
+      s.draw_at = t;
+      s.draw_base = base;
     }
-    if (cta < 0) {
-      cta = last;
-      cta_base = last_base;
-    }
-    if (static_cast<int>(rank) != cta) return -1;
-    base = cta_base;
-    int w = -1, last_w = 0;
-    double w_base = 0.0, last_w_base = 0.0;
-    for (int k = 0; k < kWarps; ++k) {
-      if (s.warp_sum[k] > 0.0) {
-        last_w = k;
-        last_w_base = base;
-      }
-      if (w < 0 && base + s.warp_sum[k] > t) {
-        w = k;
-        w_base = base;
-      }
-      base += s.warp_sum[k];
-    }
-    if (w < 0) {
-      w = last_w;
-      w_base = last_w_base;
-    }
-    if (warp != w) return -1;
+  }
 
-    const RowView<T> pv(p.target, row0 + c, p.vocab);
-    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + c, p.vocab);
-    const float ah = static_cast<float>(r.a);
-    const float al = static_cast<float>(r.a - static_cast<double>(ah));
+  // Lane of the first running sum of x past t (from `base` on), else the last
+  // lane with x > 0; base becomes the sum in front of it.
+  __device__ __forceinline__ int pick(double x, double t, double& base) const {
+    double incl = x;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, lane < 16 && base + incl > t && x > 0.0);
+    const uint32_t some = __ballot_sync(0xffffffffu, lane < 16 && x > 0.0);
+    const int at = past != 0u ? __ffs(past) - 1 : 31 - __clz(some | 1u);
+    const double front = __shfl_sync(0xffffffffu, incl - x, at);
+    base += front;
+    return at;
+  }
+
+  // The ordered draw, by the one warp of the cluster that holds the token.
+  __device__ int draw() const {
+    const RowView<T> pv(p.target, row0 + s.node, p.vocab);
+    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
+    const float ah = s.ah, al = s.al;
+    const double t = s.draw_at;
     int g0, g1;
     my_range(pv, g0, g1);
     constexpr int E = Elem<T>::kPer;
     int highest = -1;  // the highest token with mass seen by this lane
-    base = w_base;
+    Pair run = {0.f, 0.f};  // what this warp has passed
+    const double base = s.draw_base;
     for (int s0 = g0; s0 < g1; s0 += 32) {
       const int g = s0 + lane;
       Pair tm[E];
@@ -347,46 +456,52 @@ struct Walk {
       if (g < g1) {
         float x[E], y[E];
         pv.values(g, x);
-        qv.values(g, y);
-        if (!kDraft || r.a == 0.0) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[e] = 0.f;
-        }
-        terms(r, ah, al, g, pv.off, x, y, tm);
+        for (int e = 0; e < E; ++e) y[e] = 0.f;
+        if (kDraft && ah != 0.f) qv.values(g, y);
+        terms(ah, al, g, pv.off, x, y, tm);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           add(acc, tm[e]);
-          if (value(tm[e]) > 0.0) highest = g * E + e - pv.off;
+          if (tm[e].hi > 0.f) highest = g * E + e - pv.off;
         }
       }
-      double incl = value(acc);
+      Pair incl = acc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        Pair v = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+        if (lane >= o) {
+          add(v, incl);
+          incl = v;
+        }
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > t && value(acc) > 0.0);
+      Pair here = run;
+      add(here, incl);
+      const uint32_t past = __ballot_sync(0xffffffffu, base + value(here) > t && acc.hi > 0.f);
       if (past != 0u) {
         const int owner = __ffs(past) - 1;
+        // what lies in front of the owner's granule
+        Pair front = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+        if (lane == 0) front = {0.f, 0.f};
         int at = -1;
         if (lane == owner) {
           // the same sums, value by value: the first past t, or the granule's
           // last with mass where rounding leaves none
-          double run = base + incl - value(acc);
+          add(run, front);
           bool found = false;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const double x = value(tm[e]);
-            if (x > 0.0 && !found) {
+            if (tm[e].hi > 0.f && !found) {
               at = g * E + e - pv.off;
-              run += x;
-              found = run > t;
+              add(run, tm[e]);
+              found = base + value(run) > t;
             }
           }
         }
         return __shfl_sync(0xffffffffu, at, owner);
       }
-      base += __shfl_sync(0xffffffffu, incl, 31);
+      const Pair whole = {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+      add(run, whole);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) highest = max(highest, __shfl_xor_sync(0xffffffffu, highest, o));
@@ -394,8 +509,10 @@ struct Walk {
   }
 };
 
-template <typename T, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const VerifyParams p) {
+template <typename T, bool kDraft, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1024 / (kWarps * 32))
+verify_tree_kernel(const VerifyParams p) {
+  constexpr int kThreads = kWarps * 32;
   __shared__ Shared s;
   pdl_wait_primary();
   const uint32_t rank = cluster_rank();
@@ -447,77 +564,99 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const VerifyPa
   }
   __syncthreads();
 
-  // every warp of the cluster walks alike
-  Walk<T, kDraft> walk{p, s, n0, rank, lane, warp};
-  const int par0 = s.parent[lane], par1 = s.parent[lane + 32];
-  int cur = 0, count = 1;
-  uint64_t on_path = 1;
-  Residual r = {0.0, 0};
-  double mass = 1.0;
-  bool summed = false;  // the last pass summed the residual at hand
-  while (true) {
-    uint64_t kids = static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == cur)) |
-                    static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == cur)) << 32;
-    int next = -1;
-    while (kids != 0) {
-      const int x = __ffsll(static_cast<long long>(kids)) - 1;
-      kids &= kids - 1;
-      const double px = s.p[x], qx = s.q[x];
-      double rx;
-      if constexpr (kDraft) {
-        rx = px - r.a * qx;
-        rx = rx > 0.0 ? rx : 0.0;
-      } else {
-        rx = px;
-        for (int k = 0; k < r.n_refused; ++k)
-          if (s.refused[k] == s.token[x]) rx = 0.0;
+  Walk<T, kDraft, kWarps> walk{p, s, n0, rank, lane, warp};
+  int count = 1;
+  bool ok = false;
+  if (warp == 0) {
+    const int par0 = s.parent[lane], par1 = s.parent[lane + 32];
+    int cur = 0;
+    uint64_t on_path = 1;
+    Residual r = {0.0, 0};
+    double mass = 1.0;
+    bool summed = false;  // the last pass summed the residual at hand
+    while (true) {
+      uint64_t kids = static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == cur)) |
+                      static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == cur)) << 32;
+      int next = -1;
+      while (kids != 0) {
+        const int x = __ffsll(static_cast<long long>(kids)) - 1;
+        kids &= kids - 1;
+        const double px = s.p[x], qx = s.q[x];
+        double rx;
+        if constexpr (kDraft) {
+          rx = px - r.a * qx;
+          rx = rx > 0.0 ? rx : 0.0;
+        } else {
+          rx = px;
+          for (int k = 0; k < r.n_refused; ++k)
+            if (s.refused[k] == s.token[x]) rx = 0.0;
+        }
+        if (static_cast<double>(s.u[x]) * qx * mass < rx) {
+          next = x;
+          break;
+        }
+        if constexpr (kDraft) {
+          r.a += mass;
+          mass = walk.sum(cur, r);
+          summed = true;
+        } else {
+          mass = mass > rx ? mass - rx : 0.0;
+          __syncwarp();
+          if (lane == 0) s.refused[r.n_refused] = s.token[x];
+          __syncwarp();
+          ++r.n_refused;
+        }
       }
-      if (static_cast<double>(s.u[x]) * qx * mass < rx) {
-        next = x;
-        break;
-      }
-      if constexpr (kDraft) {
-        r.a += mass;
-        mass = walk.sum(cur, r);
-        summed = true;
-      } else {
-        mass = mass > rx ? mass - rx : 0.0;
-        __syncthreads();  // the list has been read by every warp
-        if (threadIdx.x == 0) s.refused[r.n_refused] = s.token[x];
-        __syncthreads();
-        ++r.n_refused;
-      }
+      if (next < 0) break;
+      cur = next;
+      ++count;
+      on_path |= 1ull << next;
+      r = {0.0, 0};
+      mass = 1.0;
+      summed = false;
     }
-    if (next < 0) break;
-    cur = next;
-    ++count;
-    on_path |= 1ull << next;
-    r = {0.0, 0};
-    mass = 1.0;
-    summed = false;
-  }
-
-  double total = summed ? mass : walk.sum(cur, r);
-  if (total == 0.0 && (r.a != 0.0 || r.n_refused != 0)) {
-    r = {0.0, 0};  // nothing of the target is left: draw from all of it
-    total = walk.sum(cur, r);
-  }
-  const bool ok = total > 0.0 && total <= 1.7e308;
-  int drawn = -1;
-  if (ok) drawn = walk.draw(cur, r, static_cast<double>(p.u_sample[b]) * total);
-  if (lane == 0 && (ok ? drawn >= 0 : rank == 0 && warp == 0)) p.out_tokens[n0 + count - 1] = drawn;
-  if (rank == 0) {
-    if (threadIdx.x < kNodes && ((on_path >> threadIdx.x) & 1ull))
-      s.path[__popcll(on_path & ((1ull << threadIdx.x) - 1ull))] = threadIdx.x;
+    double total = summed ? mass : walk.sum(cur, r);
+    if (total == 0.0 && (r.a != 0.0 || r.n_refused != 0)) {
+      r = {0.0, 0};  // nothing of the target is left: draw from all of it
+      total = walk.sum(cur, r);
+    }
+    ok = total > 0.0 && total <= 1.7e308;
+    if (ok) walk.place(static_cast<double>(p.u_sample[b]) * total);
+    else if (lane == 0) s.order = kLeave;
+    if (lane == 0) s.count = count;
     __syncthreads();
-    for (int i = threadIdx.x; i < N; i += kThreads) {
-      p.path[n0 + i] = i < count ? s.path[i] : -1;
-      if (i != count - 1) p.out_tokens[n0 + i] = i < count - 1 ? s.token[s.path[i + 1]] : -1;
+    if (rank == 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        if ((on_path >> i) & 1ull) s.path[__popcll(on_path & ((1ull << i) - 1ull))] = i;
+      }
+      __syncwarp();
+      for (int i = lane; i < N; i += 32) {
+        p.path[n0 + i] = i < count ? s.path[i] : -1;
+        if (i != count - 1) p.out_tokens[n0 + i] = i < count - 1 ? s.token[s.path[i + 1]] : -1;
+      }
+      if (lane == 0) {
+        p.n_accepted[b] = count;
+        if (!ok) {
+          p.out_tokens[n0 + count - 1] = -1;
+          set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PROBS);
+        }
+      }
     }
-    if (threadIdx.x == 0) {
-      p.n_accepted[b] = count;
-      if (!ok) set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PROBS);
+  } else {
+    while (true) {
+      __syncthreads();
+      if (s.order != kSum) break;
+      walk.sum_part();
+      __syncthreads();
+      cluster_sync();
     }
+    count = s.count;
+  }
+  if (s.order == kDraw && warp == s.draw_warp) {
+    const int drawn = walk.draw();
+    if (lane == 0) p.out_tokens[n0 + count - 1] = drawn;
   }
   // a programmatic dependent may read the results before this grid has drained
   __threadfence();
@@ -531,11 +670,11 @@ int pick_cluster(int vocab) {
   return c;
 }
 
-template <typename T, bool kDraft>
+template <typename T, bool kDraft, int kWarps>
 cudaError_t launch(const VerifyParams& p, int batch, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch) * p.cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -546,7 +685,16 @@ cudaError_t launch(const VerifyParams& p, int batch, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_tree_kernel<T, kDraft>, p);
+  return cudaLaunchKernelEx(&cfg, verify_tree_kernel<T, kDraft, kWarps>, p);
+}
+
+// 16 warps a CTA while two CTAs per SM hold every row's cluster, else 8 (four CTAs
+// per SM): more warps shorten a row's pass, more CTAs keep the rows in one wave.
+template <typename T, bool kDraft>
+cudaError_t launch_for(const VerifyParams& p, int batch, int sms, cudaStream_t stream) {
+  return static_cast<int64_t>(batch) * p.cluster <= 2 * sms
+             ? launch<T, kDraft, 16>(p, batch, stream)
+             : launch<T, kDraft, 8>(p, batch, stream);
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
@@ -595,9 +743,10 @@ extern "C" pkv_status pkv_verify_tree(const void* target_probs, const void* draf
   p.cluster = pick_cluster(vocab);
   cudaError_t e;
   if (probs_type == PKV_PROBS_FP32)
-    e = draft_probs ? launch<float, true>(p, batch, stream) : launch<float, false>(p, batch, stream);
+    e = draft_probs ? launch_for<float, true>(p, batch, sms, stream)
+                    : launch_for<float, false>(p, batch, sms, stream);
   else
-    e = draft_probs ? launch<__nv_bfloat16, true>(p, batch, stream)
-                    : launch<__nv_bfloat16, false>(p, batch, stream);
+    e = draft_probs ? launch_for<__nv_bfloat16, true>(p, batch, sms, stream)
+                    : launch_for<__nv_bfloat16, false>(p, batch, sms, stream);
   return record_cuda_status(e);
 }
