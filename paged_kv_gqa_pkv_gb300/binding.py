@@ -464,27 +464,68 @@ def pkv_stage_from_host(dst: torch.Tensor, src: torch.Tensor, stream=None) -> No
     _check("pkv_stage_from_host", st)
 
 
-def _rows(name: str, t: torch.Tensor, *shape: int) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _tensor(name: str, t, dtype: torch.dtype, shape, dev: int) -> int:
+    """The address of a contiguous CUDA tensor of `dtype` and `shape` on device
+    `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {list(shape)} on "
+                     f"cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _cache_args(k_pool, v_pool, page_table) -> None:
-    _need(k_pool, "k_pool", torch.bfloat16, 3)
-    _need(v_pool, "v_pool", torch.bfloat16, 3)
+def _device_of(name: str, t, dtype: torch.dtype, ndim: int) -> int:
+    """The device that a call runs on: that of its first tensor."""
+    _need(t, name, dtype, ndim)
+    return t.get_device()
+
+
+def _cache(k_pool, v_pool, page_table, page_size: int):
+    """Device, descriptor and addresses of a call's cache."""
+    dev = _device_of("k_pool", k_pool, torch.bfloat16, 3)
+    v = _tensor("v_pool", v_pool, torch.bfloat16, k_pool.shape, dev)
     _need(page_table, "page_table", torch.int32, 2)
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must have one shape")
+    table = _tensor("page_table", page_table, torch.int32, page_table.shape, dev)
+    return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, table
 
 
-def _scratch(workspace, nbytes: int, device) -> torch.Tensor:
+def _scratch(workspace, nbytes: int, dev: int, like: torch.Tensor) -> torch.Tensor:
     """The caller's workspace, or one of the size the call needs."""
     if workspace is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or \
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=like.device)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
             not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     return workspace
+
+
+def _dev_err(t, dev: int) -> Optional[int]:
+    return None if t is None else _tensor("dev_err", t, torch.int32, t.shape, dev)
+
+
+# The handle of the current stream without the stream object around it (a few
+# microseconds less per call), where this PyTorch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(name: str, dev: int, stream, fn, *args) -> None:
+    """Calls fn(*args, stream) with `dev` current, on `stream` or the device's
+    current one."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _run(name, dev, stream, fn, *args)
+        return
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    st = fn(*args, handle)
+    if st != PKV_OK:
+        raise PkvError(name, st)
 
 
 def pkv_tree_workspace_size(k_pool, page_table, page_size: int, batch: int, n_nodes: int,
@@ -504,39 +545,29 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
     batch_idx[b], itself and its ancestors by parents [B, N]; the nodes' own
     K/V are in the pools at positions ctx_lens[b] + node (appended first).
     Returns (out [B, N, Hq, D] bf16, lse [B, N, Hq] fp32)."""
-    _cache_args(k_pool, v_pool, page_table)
+    dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     _need(q, "q", torch.bfloat16, 4)
-    for name, t, nd in (("parents", parents, 2), ("tree_lens", tree_lens, 1),
-                        ("batch_idx", batch_idx, 1), ("ctx_lens", ctx_lens, 1)):
-        _need(t, name, torch.int32, nd)
     B, N, hq, d = q.shape
-    if d != k_pool.shape[2]:
+    if d != desc.head_dim:
         raise ValueError("q and the pools must have one head dim")
-    _rows("parents", parents, B, N)
-    for name, t in (("tree_lens", tree_lens), ("batch_idx", batch_idx), ("ctx_lens", ctx_lens)):
-        _rows(name, t, B)
+    i32, nodes, rows = torch.int32, (B, N), (B,)
+    args = (_tensor("q", q, torch.bfloat16, q.shape, dev), hq,
+            _tensor("parents", parents, i32, nodes, dev),
+            _tensor("tree_lens", tree_lens, i32, rows, dev),
+            _tensor("batch_idx", batch_idx, i32, rows, dev),
+            _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N, float(scale))
     if out is None:
-        out = torch.empty((B, N, hq, d), dtype=torch.bfloat16, device=q.device)
-    else:
-        _need(out, "out", torch.bfloat16, 4)
-        _rows("out", out, B, N, hq, d)
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((B, N, hq), dtype=torch.float32, device=q.device)
-    else:
-        _need(lse, "lse", torch.float32, 3)
-        _rows("lse", lse, B, N, hq)
-    desc = cache_desc(k_pool, page_table, page_size)
     lib = load_library()
-    need = 0
-    if workspace is None:
-        need = lib.pkv_tree_workspace_size(ctypes.byref(desc), B, N, hq)
-    workspace = _scratch(workspace, need, q.device)
-    st = lib.pkv_tree_attention(
-        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(q), hq,
-        _ptr(parents), _ptr(tree_lens), _ptr(batch_idx), _ptr(ctx_lens), B, N, float(scale),
-        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(dev_err), _stream(stream))
-    _check("pkv_tree_attention", st)
+    desc_p = ctypes.byref(desc)
+    workspace = _scratch(workspace, 0 if workspace is not None else
+                         lib.pkv_tree_workspace_size(desc_p, B, N, hq), dev, q)
+    _run("pkv_tree_attention", dev, stream, lib.pkv_tree_attention, desc_p, k, v, table, *args,
+         _tensor("out", out, torch.bfloat16, q.shape, dev),
+         _tensor("lse", lse, torch.float32, (B, N, hq), dev), workspace.data_ptr(),
+         workspace.nbytes, _dev_err(dev_err, dev))
     return out, lse
 
 
@@ -551,36 +582,30 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
     [B, N] and u_sample [B]; draft_probs is like target_probs, or None for
     guessed tokens. Returns (path [B, N], tokens [B, N], n_accepted [B])
     int32: the accepted nodes, their tokens and the next one."""
-    if not isinstance(target_probs, torch.Tensor) or target_probs.dtype not in _PROBS_TYPES:
+    kind = target_probs.dtype if isinstance(target_probs, torch.Tensor) else None
+    if kind not in _PROBS_TYPES:
         raise ValueError("target_probs must be an fp32 or bf16 tensor")
-    kind = target_probs.dtype
-    _need(target_probs, "target_probs", kind, 3)
+    dev = _device_of("target_probs", target_probs, kind, 3)
     B, N, V = target_probs.shape
-    if draft_probs is not None:
-        _need(draft_probs, "draft_probs", kind, 3)
-        _rows("draft_probs", draft_probs, B, N, V)
-    for name, t, dt, shape in (("draft_tokens", draft_tokens, torch.int32, (B, N)),
-                               ("parents", parents, torch.int32, (B, N)),
-                               ("tree_lens", tree_lens, torch.int32, (B,)),
-                               ("u_accept", u_accept, torch.float32, (B, N)),
-                               ("u_sample", u_sample, torch.float32, (B,))):
-        _need(t, name, dt, len(shape))
-        _rows(name, t, *shape)
-    outs = []
-    for name, t, shape in (("path", path, (B, N)), ("tokens", tokens, (B, N)),
-                           ("n_accepted", n_accepted, (B,))):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=target_probs.device)
-        else:
-            _need(t, name, torch.int32, len(shape))
-            _rows(name, t, *shape)
-        outs.append(t)
-    st = load_library().pkv_verify_tree(
-        _ptr(target_probs), _ptr(draft_probs), _PROBS_TYPES[kind], V, _ptr(draft_tokens),
-        _ptr(parents), _ptr(tree_lens), _ptr(u_accept), _ptr(u_sample), B, N, _ptr(outs[0]),
-        _ptr(outs[1]), _ptr(outs[2]), _ptr(dev_err), _stream(stream))
-    _check("pkv_verify_tree", st)
-    return tuple(outs)
+    i32, nodes, rows = torch.int32, (B, N), (B,)
+    args = (target_probs.data_ptr(),
+            None if draft_probs is None else
+            _tensor("draft_probs", draft_probs, kind, target_probs.shape, dev),
+            _PROBS_TYPES[kind], V, _tensor("draft_tokens", draft_tokens, i32, nodes, dev),
+            _tensor("parents", parents, i32, nodes, dev),
+            _tensor("tree_lens", tree_lens, i32, rows, dev),
+            _tensor("u_accept", u_accept, torch.float32, nodes, dev),
+            _tensor("u_sample", u_sample, torch.float32, rows, dev), B, N)
+    if path is None:
+        path = torch.empty(nodes, dtype=i32, device=target_probs.device)
+    if tokens is None:
+        tokens = torch.empty(nodes, dtype=i32, device=target_probs.device)
+    if n_accepted is None:
+        n_accepted = torch.empty(rows, dtype=i32, device=target_probs.device)
+    _run("pkv_verify_tree", dev, stream, load_library().pkv_verify_tree, *args,
+         _tensor("path", path, i32, nodes, dev), _tensor("tokens", tokens, i32, nodes, dev),
+         _tensor("n_accepted", n_accepted, i32, rows, dev), _dev_err(dev_err, dev))
+    return path, tokens, n_accepted
 
 
 def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx_lens,
@@ -589,24 +614,18 @@ def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx
     positions ctx_lens[b] + node to ctx_lens[b], ctx_lens[b] + 1, ... in
     place. Returns new_lens [B] = ctx_lens + n_accepted (``new_lens`` may be
     ctx_lens itself)."""
-    _cache_args(k_pool, v_pool, page_table)
+    dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     _need(path, "path", torch.int32, 2)
     B, N = path.shape
-    for name, t in (("n_accepted", n_accepted), ("batch_idx", batch_idx),
-                    ("ctx_lens", ctx_lens)):
-        _need(t, name, torch.int32, 1)
-        _rows(name, t, B)
+    i32, rows = torch.int32, (B,)
+    args = (_tensor("path", path, i32, (B, N), dev),
+            _tensor("n_accepted", n_accepted, i32, rows, dev),
+            _tensor("batch_idx", batch_idx, i32, rows, dev),
+            _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=path.device)
-    else:
-        _need(new_lens, "new_lens", torch.int32, 1)
-        _rows("new_lens", new_lens, B)
-    desc = cache_desc(k_pool, page_table, page_size)
-    st = load_library().pkv_commit_path(
-        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(path),
-        _ptr(n_accepted), _ptr(batch_idx), _ptr(ctx_lens), B, N, _ptr(new_lens), _ptr(dev_err),
-        _stream(stream))
-    _check("pkv_commit_path", st)
+        new_lens = torch.empty(rows, dtype=i32, device=path.device)
+    _run("pkv_commit_path", dev, stream, load_library().pkv_commit_path, ctypes.byref(desc), k, v,
+         table, *args, _tensor("new_lens", new_lens, i32, rows, dev), _dev_err(dev_err, dev))
     return new_lens
 
 
@@ -625,25 +644,21 @@ def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots
     dst_slots[i] gets the first keep_lens[i] tokens of slot src_slots[i] (pages
     shared) and pages of its own for the positions up to new_lens[i].
     page_refs [num_pages] counts the table entries that use each page (0: free)."""
-    _cache_args(k_pool, v_pool, page_table)
-    _need(page_refs, "page_refs", torch.int32, 1)
+    dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     _need(dst_slots, "dst_slots", torch.int32, 1)
-    n = dst_slots.numel()
-    for name, t in (("src_slots", src_slots), ("keep_lens", keep_lens), ("new_lens", new_lens)):
-        _need(t, name, torch.int32, 1)
-        _rows(name, t, n)
-    desc = cache_desc(k_pool, page_table, page_size)
-    _rows("page_refs", page_refs, desc.num_pages)
+    n = dst_slots.shape[0]
+    i32, rows = torch.int32, (n,)
+    args = (_tensor("page_refs", page_refs, i32, (desc.num_pages,), dev),
+            _tensor("dst_slots", dst_slots, i32, rows, dev),
+            _tensor("src_slots", src_slots, i32, rows, dev),
+            _tensor("keep_lens", keep_lens, i32, rows, dev),
+            _tensor("new_lens", new_lens, i32, rows, dev), n)
     lib = load_library()
-    need = 0
-    if workspace is None:
-        need = lib.pkv_update_workspace_size(ctypes.byref(desc), n)
-    workspace = _scratch(workspace, need, k_pool.device)
-    st = lib.pkv_update_pages(
-        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(page_refs),
-        _ptr(dst_slots), _ptr(src_slots), _ptr(keep_lens), _ptr(new_lens), n, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream))
-    _check("pkv_update_pages", st)
+    desc_p = ctypes.byref(desc)
+    workspace = _scratch(workspace, 0 if workspace is not None else
+                         lib.pkv_update_workspace_size(desc_p, n), dev, k_pool)
+    _run("pkv_update_pages", dev, stream, lib.pkv_update_pages, desc_p, k, v, table, *args,
+         workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
 
 
 def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
@@ -658,23 +673,15 @@ def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num
                       workspace=None, dev_err=None, stream=None):
     """Moves the live pages to the low end of the pool (K/V rows, table
     entries and counts), in place. Returns num_live [1], how many there are."""
-    _cache_args(k_pool, v_pool, page_table)
-    _need(page_refs, "page_refs", torch.int32, 1)
-    desc = cache_desc(k_pool, page_table, page_size)
-    _rows("page_refs", page_refs, desc.num_pages)
+    dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
+    refs = _tensor("page_refs", page_refs, torch.int32, (desc.num_pages,), dev)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=k_pool.device)
-    else:
-        _need(num_live, "num_live", torch.int32, 1)
-        _rows("num_live", num_live, 1)
+        num_live = torch.empty(1, dtype=torch.int32, device=page_refs.device)
     lib = load_library()
-    need = 0
-    if workspace is None:
-        need = lib.pkv_compact_workspace_size(ctypes.byref(desc))
-    workspace = _scratch(workspace, need, k_pool.device)
-    st = lib.pkv_compact_pages(
-        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(page_refs),
-        _ptr(num_live), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(dev_err), _stream(stream))
-    _check("pkv_compact_pages", st)
+    desc_p = ctypes.byref(desc)
+    workspace = _scratch(workspace, 0 if workspace is not None else
+                         lib.pkv_compact_workspace_size(desc_p), dev, k_pool)
+    _run("pkv_compact_pages", dev, stream, lib.pkv_compact_pages, desc_p, k, v, table, refs,
+         _tensor("num_live", num_live, torch.int32, (1,), dev), workspace.data_ptr(),
+         workspace.nbytes, _dev_err(dev_err, dev))
     return num_live

@@ -161,6 +161,12 @@ struct Sum2 {
   }
 };
 
+// a > b, as the sums they stand for.
+__device__ __forceinline__ bool above(const Pair& a, const Pair& b) {
+  const Pair x = two_sum(a.hi, a.lo);
+  return x.hi > b.hi || (x.hi == b.hi && x.lo > b.lo);
+}
+
 __device__ __forceinline__ double value(const Pair& x) {
   return static_cast<double>(x.hi) + static_cast<double>(x.lo);
 }
@@ -244,8 +250,10 @@ struct Shared {
   double cta_sum[2][kMaxCluster];     // the residual's, of the last two passes, all CTAs
   // the walking warp's order to the others
   int order, node, n_refused, draw_warp, count;
+  int first[kMaxWarps], last[kMaxWarps];  // of the draw, lanes per warp
   float ah, al;
-  double a, draw_at, draw_base;
+  double a;
+  Pair draw_at;  // how far into the draw's warp
 };
 
 template <typename T, bool kDraft, int kWarps>
@@ -257,12 +265,12 @@ struct Walk {
   const int lane, warp;
   int passes = 0;
 
-  // granules [g0, g1) of the row at node c are this warp's
-  __device__ __forceinline__ void my_range(const RowView<T>& v, int& g0, int& g1) const {
+  // granules [g0, g1) of a row are warp wp's of this CTA
+  __device__ __forceinline__ void range_of(const RowView<T>& v, int wp, int& g0, int& g1) const {
     const int total = (v.end + Elem<T>::kPer - 1) / Elem<T>::kPer;
     const int warps = p.cluster * kWarps;
     const int per = ((total + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t w = static_cast<int64_t>(rank) * kWarps + warp;
+    const int64_t w = static_cast<int64_t>(rank) * kWarps + wp;
     g0 = static_cast<int>(w * per < total ? w * per : total);
     g1 = static_cast<int>((w + 1) * per < total ? (w + 1) * per : total);
   }
@@ -294,7 +302,7 @@ struct Walk {
     const float ah = s.ah, al = s.al;
     const bool with_q = kDraft && ah != 0.f;
     int g0, g1;
-    my_range(pv, g0, g1);
+    range_of(pv, warp, g0, g1);
     constexpr int E = Elem<T>::kPer;
     constexpr int kUnroll = 16 / E;  // 16-byte loads per row and thread in flight
     Sum2 ps = {0ull, 0ull}, qs = {0ull, 0ull};
@@ -413,8 +421,9 @@ struct Walk {
     if (lane == 0) {
       s.order = kDraw;
       s.draw_warp = w;
-      s.draw_at = t;
-      s.draw_base = base;
+      const double at = t - base;
+      s.draw_at.hi = static_cast<float>(at);
+      s.draw_at.lo = static_cast<float>(at - static_cast<double>(s.draw_at.hi));
     }
   }
 
@@ -435,77 +444,95 @@ struct Walk {
     return at;
   }
 
-  // The ordered draw, by the one warp of the cluster that holds the token.
-  __device__ int draw() const {
+  // The ordered draw, by all threads of the CTA that holds the token, over the
+  // granules of the warp that held it in the pass: each thread sums a few of them,
+  // the running sums pick the thread, and that one picks the token. (One warp
+  // alone took 10 us for its 300 granules.) Returns the token in the thread that
+  // picked it, -1 in the others.
+  __device__ int draw() {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
     const float ah = s.ah, al = s.al;
-    const double t = s.draw_at;
+    const Pair t = s.draw_at;
     int g0, g1;
-    my_range(pv, g0, g1);
+    range_of(pv, s.draw_warp, g0, g1);
     constexpr int E = Elem<T>::kPer;
-    int highest = -1;  // the highest token with mass seen by this lane
-    Pair run = {0.f, 0.f};  // what this warp has passed
-    const double base = s.draw_base;
-    for (int s0 = g0; s0 < g1; s0 += 32) {
-      const int g = s0 + lane;
+    const int per = (g1 - g0 + kWarps * 32 - 1) / (kWarps * 32);
+    const int a0 = min(g0 + (32 * warp + lane) * per, g1), a1 = min(a0 + per, g1);
+    auto granule = [&](int g, Pair (&tm)[E]) {
+      float x[E], y[E];
+      pv.values(g, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = 0.f;
+      if (kDraft && ah != 0.f) qv.values(g, y);
+      terms(ah, al, g, pv.off, x, y, tm);
+    };
+    Pair acc = {0.f, 0.f};
+    for (int g = a0; g < a1; ++g) {
       Pair tm[E];
-      Pair acc = {0.f, 0.f};
+      granule(g, tm);
 #pragma unroll
-      for (int e = 0; e < E; ++e) tm[e] = {0.f, 0.f};
-      if (g < g1) {
-        float x[E], y[E];
-        pv.values(g, x);
+      for (int e = 0; e < E; ++e) add(acc, tm[e]);
+    }
+    Pair incl = acc;
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = 0.f;
-        if (kDraft && ah != 0.f) qv.values(g, y);
-        terms(ah, al, g, pv.off, x, y, tm);
+    for (int o = 1; o < 32; o <<= 1) {
+      Pair v = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+      if (lane >= o) {
+        add(v, incl);
+        incl = v;
+      }
+    }
+    if (lane == 31) s.warp_p[warp] = incl;
+    __syncthreads();
+    // what lies in front of this warp, then of this thread
+    Pair front = lane < kWarps ? s.warp_p[lane] : Pair{0.f, 0.f};
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+      Pair v = {__shfl_up_sync(0xffffffffu, front.hi, o), __shfl_up_sync(0xffffffffu, front.lo, o)};
+      if (lane >= o) {
+        add(v, front);
+        front = v;
+      }
+    }
+    front = {__shfl_sync(0xffffffffu, front.hi, max(warp - 1, 0)),
+             __shfl_sync(0xffffffffu, front.lo, max(warp - 1, 0))};
+    if (warp == 0) front = {0.f, 0.f};
+    Pair here = front;
+    add(here, incl);
+    const uint32_t past = __ballot_sync(0xffffffffu, above(here, t) && acc.hi > 0.f);
+    const uint32_t some = __ballot_sync(0xffffffffu, acc.hi > 0.f);
+    if (lane == 0) {
+      s.first[warp] = past != 0u ? __ffs(past) - 1 : -1;
+      s.last[warp] = some != 0u ? 31 - __clz(some) : -1;
+    }
+    __syncthreads();
+    // the first thread whose running sum passes t, else the last with any mass
+    const int f = lane < kWarps ? s.first[lane] : -1, e = lane < kWarps ? s.last[lane] : -1;
+    const uint32_t fs = __ballot_sync(0xffffffffu, f >= 0), es = __ballot_sync(0xffffffffu, e >= 0);
+    const int w = fs != 0u ? __ffs(fs) - 1 : 31 - __clz(es | 1u);
+    const int l = __shfl_sync(0xffffffffu, fs != 0u ? f : e, w);
+    const Pair before = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    int at = -1;
+    if (warp == w && lane == l) {
+      // the same sums, value by value: the first past t, or the last with mass
+      // where rounding leaves none
+      if (lane > 0) add(front, before);
+      bool found = false;
+      for (int g = a0; g < a1 && !found; ++g) {
+        Pair tm[E];
+        granule(g, tm);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          add(acc, tm[e]);
-          if (tm[e].hi > 0.f) highest = g * E + e - pv.off;
-        }
-      }
-      Pair incl = acc;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        Pair v = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
-        if (lane >= o) {
-          add(v, incl);
-          incl = v;
-        }
-      }
-      Pair here = run;
-      add(here, incl);
-      const uint32_t past = __ballot_sync(0xffffffffu, base + value(here) > t && acc.hi > 0.f);
-      if (past != 0u) {
-        const int owner = __ffs(past) - 1;
-        // what lies in front of the owner's granule
-        Pair front = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-        if (lane == 0) front = {0.f, 0.f};
-        int at = -1;
-        if (lane == owner) {
-          // the same sums, value by value: the first past t, or the granule's
-          // last with mass where rounding leaves none
-          add(run, front);
-          bool found = false;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if (tm[e].hi > 0.f && !found) {
-              at = g * E + e - pv.off;
-              add(run, tm[e]);
-              found = base + value(run) > t;
-            }
+          if (tm[e].hi > 0.f && !found) {
+            at = g * E + e - pv.off;
+            add(front, tm[e]);
+            found = above(front, t);
           }
         }
-        return __shfl_sync(0xffffffffu, at, owner);
       }
-      const Pair whole = {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-      add(run, whole);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) highest = max(highest, __shfl_xor_sync(0xffffffffu, highest, o));
-    return highest;
+    return at;
   }
 };
 
@@ -520,7 +547,15 @@ verify_tree_kernel(const VerifyParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int N = p.n_nodes;
   const int64_t n0 = static_cast<int64_t>(b) * N;
+  // the trees' numbers, in flight together with the tree's size
   int err = 0;
+  int parent = -1, tok = 0;
+  float u = 0.f;
+  if (threadIdx.x >= 1 && static_cast<int>(threadIdx.x) < N) {
+    parent = p.parents[n0 + threadIdx.x];
+    tok = p.tokens[n0 + threadIdx.x];
+    u = p.u_accept[n0 + threadIdx.x];
+  }
   int len = p.tree_lens[b];
   if (len < 0 || len > N) {
     err = PKV_DEV_ERR_BAD_TREE;
@@ -539,12 +574,10 @@ verify_tree_kernel(const VerifyParams p) {
   }
   if (threadIdx.x < kNodes) {
     const int i = threadIdx.x;
-    int parent = -1, tok = 0;
-    float px = 0.f, qx = 0.f, u = 0.f;
-    if (i >= 1 && i < len) {
-      parent = p.parents[n0 + i];
-      tok = p.tokens[n0 + i];
-      u = p.u_accept[n0 + i];
+    float px = 0.f, qx = 0.f;
+    if (i < 1 || i >= len) {
+      parent = -1;
+    } else {
       if (parent < -1 || parent >= i || tok < 0 || tok >= p.vocab) {
         err = PKV_DEV_ERR_BAD_TREE;
         parent = -1;
@@ -581,17 +614,26 @@ verify_tree_kernel(const VerifyParams p) {
       while (kids != 0) {
         const int x = __ffsll(static_cast<long long>(kids)) - 1;
         kids &= kids - 1;
-        const double px = s.p[x], qx = s.q[x];
         double rx;
-        if constexpr (kDraft) {
-          rx = px - r.a * qx;
-          rx = rx > 0.0 ? rx : 0.0;
+        bool take;
+        if (r.a == 0.0 && r.n_refused == 0) {
+          // a node's first child, R = 1: u q against p, exactly and without doubles
+          const float prod = __fmul_rn(s.u[x], s.q[x]);
+          const float rest = __fmaf_rn(s.u[x], s.q[x], -prod);
+          take = prod < s.p[x] || (prod == s.p[x] && rest < 0.f);
+          rx = s.p[x];
         } else {
-          rx = px;
-          for (int k = 0; k < r.n_refused; ++k)
-            if (s.refused[k] == s.token[x]) rx = 0.0;
+          rx = s.p[x];
+          if constexpr (kDraft) {
+            rx -= r.a * static_cast<double>(s.q[x]);
+            rx = rx > 0.0 ? rx : 0.0;
+          } else {
+            for (int k = 0; k < r.n_refused; ++k)
+              if (s.refused[k] == s.token[x]) rx = 0.0;
+          }
+          take = static_cast<double>(s.u[x]) * static_cast<double>(s.q[x]) * mass < rx;
         }
-        if (static_cast<double>(s.u[x]) * qx * mass < rx) {
+        if (take) {
           next = x;
           break;
         }
@@ -654,9 +696,9 @@ verify_tree_kernel(const VerifyParams p) {
     }
     count = s.count;
   }
-  if (s.order == kDraw && warp == s.draw_warp) {
+  if (s.order == kDraw && s.draw_warp >= 0) {  // (the same in the whole CTA)
     const int drawn = walk.draw();
-    if (lane == 0) p.out_tokens[n0 + count - 1] = drawn;
+    if (drawn >= 0) p.out_tokens[n0 + count - 1] = drawn;
   }
   // a programmatic dependent may read the results before this grid has drained
   __threadfence();
