@@ -563,9 +563,10 @@ size_t pkv_update_workspace_size(const pkv_cache_desc* cache, int n);
  * page in use with a count below 1), PKV_DEV_ERR_NO_PAGES (a row that needs
  * pages where the needs of the rows up to it exceed the free ones). Entries of
  * the destination outside [1, num_pages) count as unreserved.
- * page_table, page_refs, k_pool and v_pool are updated in place. workspace: at
- * least pkv_update_workspace_size() bytes, 256-byte aligned, no initialisation
- * needed; calls that share one must be stream-ordered.
+ * page_size x num_kv_heads must be below 2^25. page_table, page_refs, k_pool and
+ * v_pool are updated in place. workspace: at least pkv_update_workspace_size()
+ * bytes, 256-byte aligned, no initialisation needed; calls that share one must
+ * be stream-ordered.
  */
 pkv_status pkv_update_pages(const pkv_cache_desc* cache, void* k_pool, void* v_pool,
                             int32_t* page_table, int32_t* page_refs, const int32_t* dst_slots,

@@ -14,8 +14,8 @@
 // k-th free page of the pool by a binary search, so a pool of any size is read
 // once, in parallel, and no CTA waits for another.
 //
-// What bounds them: K/V rows are moved by 16-byte loads and stores with eight
-// loads in flight per thread (the copy's bandwidth where much is moved), and
+// What bounds them: K/V rows are moved by 16-byte loads and stores with eight loads
+// in flight per thread (the copy's bandwidth where much is moved), and
 // two launches' latency where little is.
 #include <climits>
 
@@ -29,7 +29,7 @@ constexpr int kPlanThreads = 256;
 constexpr int kMaxChunks = 1024;
 constexpr int kChunkPages = 4096;  // smallest chunk: 16 counts per thread
 
-constexpr int kInFlight = 8;  // 16-byte loads per thread before the first store
+constexpr int kInFlight = 4;  // 16-byte loads per thread and pool before the first store
 
 struct PagesParams {
   void* pool[2];  // K, V
@@ -155,24 +155,29 @@ __device__ __forceinline__ int kth_free(const PagesParams& p, const int* prefix,
 }
 
 // Copies `vecs` 16-byte vectors of both pools, from `src` to `dst` (vector
-// offsets), by the part `part` of `parts` CTAs.
-__device__ __forceinline__ void copy_rows(const PagesParams& p, int64_t src, int64_t dst,
-                                          int64_t vecs, int part, int parts) {
-  const int64_t step = static_cast<int64_t>(parts) * blockDim.x;
+// offsets), by the part `part` of `parts` CTAs; kInFlight loads of each pool go out
+// before the first store.
+__device__ __forceinline__ void copy_rows(const PagesParams& p, int64_t src, int64_t dst, int vecs,
+                                          int part, int parts) {
+  const int step = parts * kPlanThreads;
+  const uint4* kf = static_cast<const uint4*>(p.pool[0]) + src;
+  const uint4* vf = static_cast<const uint4*>(p.pool[1]) + src;
+  uint4* kt = static_cast<uint4*>(p.pool[0]) + dst;
+  uint4* vt = static_cast<uint4*>(p.pool[1]) + dst;
+  for (int i = part * kPlanThreads + threadIdx.x; i < vecs; i += step * kInFlight) {
+    uint4 k[kInFlight], v[kInFlight];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const uint4* from = static_cast<const uint4*>(p.pool[t]) + src;
-    uint4* to = static_cast<uint4*>(p.pool[t]) + dst;
-    for (int64_t i = static_cast<int64_t>(part) * blockDim.x + threadIdx.x; i < vecs;
-         i += step * kInFlight) {
-      uint4 v[kInFlight];
+    for (int u = 0; u < kInFlight; ++u)
+      if (i + u * step < vecs) {
+        k[u] = kf[i + u * step];
+        v[u] = vf[i + u * step];
+      }
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
-        if (i + u * step < vecs) v[u] = from[i + u * step];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
-        if (i + u * step < vecs) to[i + u * step] = v[u];
-    }
+    for (int u = 0; u < kInFlight; ++u)
+      if (i + u * step < vecs) {
+        kt[i + u * step] = k[u];
+        vt[i + u * step] = v[u];
+      }
   }
 }
 
@@ -277,25 +282,24 @@ __global__ void __launch_bounds__(kPlanThreads) update_plan_kernel(const PagesPa
 
 // grid (n, parts): every CTA of a row copies its part of the partly kept page;
 // part 0 also rewrites the row's table entries and counts.
-__global__ void __launch_bounds__(kPlanThreads) update_apply_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kPlanThreads, 3) update_apply_kernel(const PagesParams p) {
   __shared__ int scratch[kPlanThreads / 32];
   __shared__ int prefix[kMaxChunks + 1];
   pdl_wait_primary();
+  // everything that the row's place depends on, in flight at once
   const int i = blockIdx.x;
-  const int need = p.need[i];
-  if (need < 0) return;
-  const int tail = p.tail[i];
-  if (blockIdx.y > 0 && tail < 0) return;
-  scan_chunks(p, prefix, scratch);
+  const int need = p.need[i], tail = p.tail[i];
+  const Row r = load_row(p, i);
   int mine = 0;
   for (int k = threadIdx.x; k < i; k += kPlanThreads) mine += max(p.need[k], 0);
+  if (need < 0 || (blockIdx.y > 0 && tail < 0)) return;
+  scan_chunks(p, prefix, scratch);
   int before;  // fresh pages of the rows above
   block_excl(mine, scratch, before);
   if (need > 0 && static_cast<int64_t>(before) + need > prefix[p.n_chunks]) {
     if (blockIdx.y == 0 && threadIdx.x == 0) set_dev_err(p.dev_err, PKV_DEV_ERR_NO_PAGES);
     return;
   }
-  const Row r = load_row(p, i);
   if (blockIdx.y == 0) {
     int32_t* row = p.page_table + static_cast<int64_t>(r.d) * p.max_blocks;
     const int32_t* from = p.page_table + static_cast<int64_t>(r.s) * p.max_blocks;
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kPlanThreads) update_apply_kernel(const PagesP
     const int to = kth_free(p, prefix, before);
     const int64_t page_vecs = static_cast<int64_t>(p.page_size) * p.row_vecs;
     copy_rows(p, tail * page_vecs, to * page_vecs,
-              static_cast<int64_t>(r.keep % p.page_size) * p.row_vecs, blockIdx.y, gridDim.y);
+              (r.keep % p.page_size) * p.row_vecs, blockIdx.y, gridDim.y);
   }
 }
 
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesP
   plan_chunk<true>(p, blockIdx.x, scratch);
 }
 
-constexpr int kPieceVecs = 2 * kPlanThreads * kInFlight;  // 64 KB of each pool per piece
+constexpr int kPieceVecs = 4096;  // 64 KB of each pool per piece
 
 // Everything is read from the plan's lists, so the counts may be rewritten while
 // other CTAs still look pages up.
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_apply_kernel(const Pages
         p.live_list[static_cast<int64_t>(c) * p.chunk_pages + (stay + k - live_prefix(c))];
     const int to = kth_free(p, prefix, k);
     const int64_t v0 = static_cast<int64_t>(piece) * kPieceVecs;
-    const int64_t nv = page_vecs - v0 < kPieceVecs ? page_vecs - v0 : kPieceVecs;
+    const int nv = static_cast<int>(page_vecs - v0 < kPieceVecs ? page_vecs - v0 : kPieceVecs);
     copy_rows(p, from * page_vecs + v0, to * page_vecs + v0, nv, 0, 1);
     if (piece == 0 && threadIdx.x == 0) {
       p.refs[to] = p.refs[from];
@@ -426,9 +430,10 @@ struct CommitParams {
 };
 
 constexpr int kCommitThreads = 256;
+constexpr int kCommitInFlight = 16;
 
 // One CTA per row; a thread owns one 16-byte column of the slot's K or V rows
-// and moves the path's rows in ascending order, kInFlight at a time: all of a
+// and moves the path's rows in ascending order, kCommitInFlight at a time: all of a
 // group's loads precede its stores. In place this is safe: with path strictly
 // increasing, path[j] >= j, so row ctx + i is never the source of a later j.
 __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const CommitParams p) {
@@ -477,13 +482,13 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const Commi
   for (int c = threadIdx.x; c < 2 * p.row_vecs; c += kCommitThreads) {
     const bool k_side = c < p.row_vecs;
     uint4* pool = static_cast<uint4*>(k_side ? p.pool[0] : p.pool[1]) + (k_side ? c : c - p.row_vecs);
-    for (int k0 = 0; k0 < n; k0 += kInFlight) {
-      uint4 v[kInFlight];
+    for (int k0 = 0; k0 < n; k0 += kCommitInFlight) {
+      uint4 v[kCommitInFlight];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
+      for (int u = 0; u < kCommitInFlight; ++u)
         if (k0 + u < n && s_src[k0 + u] != s_dst[k0 + u]) v[u] = pool[s_src[k0 + u] * p.row_vecs];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
+      for (int u = 0; u < kCommitInFlight; ++u)
         if (k0 + u < n && s_src[k0 + u] != s_dst[k0 + u]) pool[s_dst[k0 + u] * p.row_vecs] = v[u];
     }
   }
@@ -579,7 +584,9 @@ pkv_status pkv_update_pages(const pkv_cache_desc* cache, void* k_pool, void* v_p
   using namespace pkv;
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
-  if (n < 0) return PKV_ERR_ARG;
+  // (a page's 16-byte vectors are counted in 32 bits)
+  if (n < 0 || static_cast<int64_t>(cache->page_size) * cache->num_kv_heads > (INT_MAX >> 6))
+    return PKV_ERR_ARG;
   if (n == 0) return PKV_OK;
   if (!k_pool || !v_pool || !page_table || !page_refs || !dst_slots || !src_slots || !keep_lens ||
       !new_lens)
@@ -609,10 +616,13 @@ pkv_status pkv_update_pages(const pkv_cache_desc* cache, void* k_pool, void* v_p
   cudaError_t e = launch_kernel(update_plan_kernel, dim3(n + l.n_chunks), dim3(kPlanThreads), 0,
                                 stream, /*programmatic=*/true, p);
   if (e != cudaSuccess) return record_cuda_status(e);
-  // parts per row: one CTA for each 32 KB of a page of one pool, at most 8
+  // parts per row: one CTA for each 16 KB of a page of one pool, as long as all rows'
+  // parts are one wave (three CTAs per SM); at most 16
   const int64_t page_vecs = static_cast<int64_t>(p.page_size) * p.row_vecs;
-  const int64_t want = (page_vecs + kPlanThreads * kInFlight - 1) / (kPlanThreads * kInFlight);
-  const unsigned parts = static_cast<unsigned>(want < 8 ? want : 8);
+  int64_t parts64 = (page_vecs + kPlanThreads * kInFlight - 1) / (kPlanThreads * kInFlight);
+  const int64_t wave = 3 * static_cast<int64_t>(sms) / n;
+  if (parts64 > wave) parts64 = wave;
+  const unsigned parts = static_cast<unsigned>(parts64 < 1 ? 1 : parts64 > 16 ? 16 : parts64);
   e = launch_kernel(update_apply_kernel, dim3(n, parts), dim3(kPlanThreads), 0, stream,
                     /*programmatic=*/true, p);
   return record_cuda_status(e);
