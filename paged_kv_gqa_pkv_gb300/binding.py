@@ -23,6 +23,7 @@ Functions keep the names of the C entry points: ``pkv_append``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -510,6 +511,18 @@ def _dev_err(t, dev: int) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _on_its_stream(call):
+    """With ``stream=`` given, makes it the current one for the call, so that
+    outputs and workspaces allocated here belong to the stream that uses them."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return run
+
+
 def _run(name: str, dev: int, stream, fn, *args) -> None:
     """Calls fn(*args, stream) with `dev` current, on `stream` or the device's
     current one."""
@@ -518,6 +531,8 @@ def _run(name: str, dev: int, stream, fn, *args) -> None:
             _run(name, dev, stream, fn, *args)
         return
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
     elif _raw_stream is not None:
         handle = _raw_stream(dev)
@@ -537,6 +552,7 @@ def pkv_tree_workspace_size(k_pool, page_table, page_size: int, batch: int, n_no
     return int(n)
 
 
+@_on_its_stream
 def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_idx, ctx_lens,
                        page_size: int, scale: float, out=None, lse=None, workspace=None,
                        dev_err=None, stream=None):
@@ -574,6 +590,7 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
 _PROBS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
+@_on_its_stream
 def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_sample,
                     draft_probs=None, path=None, tokens=None, n_accepted=None, dev_err=None,
                     stream=None):
@@ -608,6 +625,7 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
     return path, tokens, n_accepted
 
 
+@_on_its_stream
 def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx_lens,
                     page_size: int, new_lens=None, dev_err=None, stream=None):
     """Moves the K/V rows of the accepted nodes path[b, :n_accepted[b]] from
@@ -637,6 +655,7 @@ def pkv_update_workspace_size(k_pool, page_table, page_size: int, n: int) -> int
     return int(size)
 
 
+@_on_its_stream
 def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots, keep_lens,
                      new_lens, page_size: int, workspace=None, dev_err=None,
                      stream=None) -> None:
@@ -669,6 +688,7 @@ def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
     return int(size)
 
 
+@_on_its_stream
 def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num_live=None,
                       workspace=None, dev_err=None, stream=None):
     """Moves the live pages to the low end of the pool (K/V rows, table

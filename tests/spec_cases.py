@@ -119,3 +119,110 @@ def pages_state(seed, lens, ps, hkv, pages, cols, slots=None, share=()):
             refs[e] += 1
     k, v = pool_bits(rng, pages * ps, hkv)
     return SimpleNamespace(k=k, v=v, table=table, refs=refs, ps=ps)
+
+
+class Mirror:
+    """A cache on the GPU and the oracle's copy of it, driven by the same
+    calls. ``equal`` compares every byte of pools, table, counts and lengths."""
+
+    def __init__(self, seed, lens, ps, hkv, pages, cols, slots):
+        from paged_kv_gqa_pkv_gb300 import binding
+        self.b, self.ps = binding, ps
+        self.host = pages_state(seed, lens, ps, hkv, pages, cols, slots=slots)
+        rng = np.random.default_rng(seed + 1)
+        shape = self.host.k.shape
+        self.host.k, self.host.v = (bf16_bits(torch.from_numpy(
+            rng.standard_normal(shape).astype(np.float32)).bfloat16()) for _ in range(2))
+        self.lens = np.zeros(slots, dtype=np.int32)
+        self.lens[1:len(lens) + 1] = lens
+        h = self.host
+        self.k, self.v = from_bits(h.k).cuda(), from_bits(h.v).cuda()
+        self.table, self.refs = torch.from_numpy(h.table.copy()).cuda(), torch.from_numpy(h.refs).cuda()
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def i32(self, x):
+        return torch.from_numpy(np.array(x, dtype=np.int32)).cuda()
+
+    def update(self, dst, src, keep, new):
+        h = self.host
+        self.b.pkv_update_pages(self.k, self.v, self.table, self.refs, self.i32(dst), self.i32(src),
+                                self.i32(keep), self.i32(new), self.ps, dev_err=self.err)
+        h.k, h.v, h.table, h.refs, err = spec.update_pages(h.k, h.v, h.table, h.refs, dst, src, keep,
+                                                           new, self.ps)
+        assert err == 0
+
+    def append(self, k_new, v_new, slots, pos):
+        import oracle.paged_attention as orc
+        h = self.host
+        self.b.pkv_append(self.k, self.v, self.table, k_new.cuda(), v_new.cuda(), self.i32(slots),
+                          self.i32(pos), self.ps, dev_err=self.err)
+        h.k, h.v, bad = orc.append(h.k, h.v, h.table, bf16_bits(k_new), bf16_bits(v_new),
+                                   np.array(slots), np.array(pos), self.ps)
+        assert not bad
+
+    def compact(self):
+        h = self.host
+        n = self.b.pkv_compact_pages(self.k, self.v, self.table, self.refs, self.ps,
+                                     dev_err=self.err)
+        h.k, h.v, h.table, h.refs, want, err = spec.compact_pages(h.k, h.v, h.table, h.refs, self.ps)
+        assert err == 0 and int(n.item()) == want
+        return want
+
+    def equal(self):
+        torch.cuda.synchronize()
+        h = self.host
+        assert int(self.err.item()) == 0
+        assert np.array_equal(self.table.cpu().numpy(), h.table)
+        assert np.array_equal(self.refs.cpu().numpy(), h.refs)
+        assert np.array_equal(bf16_bits(self.k.cpu()), h.k)
+        assert np.array_equal(bf16_bits(self.v.cpu()), h.v)
+
+
+def draft_step(m, rng, slots, N, hq, V, shape="random"):
+    """One step of drafting on the mirror: pages for N nodes, their K/V, tree
+    attention, verification against probabilities made from the attention's
+    (rounded) output, the accepted path, and the rest given back. Each result
+    is compared with the oracle's. Returns the attention's largest error."""
+    from tests.parity import assert_attention_close
+    B, hkv = len(slots), m.k.shape[1]
+    ctx = m.lens[slots].copy()
+    m.update(slots, slots, ctx, ctx + N)
+    parents = rand_parents(rng, B, N, shape)
+    tree = rng.integers(1, N + 1, B).astype(np.int32)
+    rows = [(b, a) for b in range(B) for a in range(tree[b])]
+    new = lambda: torch.from_numpy(rng.standard_normal(  # noqa: E731
+        (len(rows), hkv, 128)).astype(np.float32)).bfloat16()
+    m.append(new(), new(), [slots[b] for b, _ in rows], [ctx[b] + a for b, a in rows])
+    q = torch.from_numpy(rng.standard_normal((B, N, hq, 128)).astype(np.float32)).bfloat16()
+    i32 = m.i32
+    par, ln, sl, cx = i32(parents), i32(tree), i32(slots), i32(ctx)
+    scale = 1 / math.sqrt(128)
+    out, lse = m.b.pkv_tree_attention(m.k, m.v, m.table, q.cuda(), par, ln, sl, cx, m.ps, scale,
+                                      dev_err=m.err)
+    ro, rl, err, _ = spec.tree_attention(bf16_bits(q), m.host.k, m.host.v, m.host.table, parents,
+                                         tree, slots, ctx, m.ps, scale)
+    assert err == 0
+    worst = assert_attention_close(out.cpu(), lse.cpu(), ro, rl, tag="step")[0]
+    # the same bits go to both sides from here
+    head = torch.from_numpy(rng.standard_normal((hq * 128, V)).astype(np.float32) * 0.05).cuda()
+    target = torch.softmax(out.float().view(B, N, -1) @ head, -1)
+    draft = torch.softmax(torch.log(target) +
+                          torch.from_numpy(rng.standard_normal((B, N, V)).astype(np.float32)).cuda(),
+                          -1)
+    tokens = torch.from_numpy(rng.integers(0, V, (B, N)).astype(np.int32)).cuda()
+    u, us = (torch.from_numpy(rng.random(s).astype(np.float32)).cuda() for s in ((B, N), (B,)))
+    path, toks, n = m.b.pkv_verify_tree(target, tokens, par, ln, u, us, draft_probs=draft,
+                                        dev_err=m.err)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    want = spec.verify_tree(f(target), f(draft), tokens.cpu().numpy(), parents, tree,
+                            f(u), f(us))
+    for g, w in zip((path, toks, n), want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    lens = m.b.pkv_commit_path(m.k, m.v, m.table, path, n, sl, cx, m.ps, dev_err=m.err)
+    h = m.host
+    h.k, h.v, new_lens, err = spec.commit_path(h.k, h.v, h.table, want[0], want[2], slots, ctx, m.ps)
+    assert err == 0 and np.array_equal(lens.cpu().numpy(), new_lens)
+    m.lens[slots] = new_lens
+    m.update(slots, slots, new_lens, new_lens)   # pages past the accepted tokens go back
+    m.equal()
+    return worst

@@ -1,0 +1,278 @@
+"""The drafted-token and page operators as a serving loop uses them: steps of
+drafting with forks, freed users and compaction between them, beside the other
+operators of the cache; the loop captured once and replayed; calls on two
+streams; rows of other users and page 0 left as they were. Whole numbers,
+tables and pools have to equal the oracle's; attention keeps the tolerances of
+the other attention tests."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged_attention as orc
+import oracle.speculative as spec
+from paged_kv_gqa_pkv_gb300 import binding
+from paged_kv_gqa_pkv_gb300.graphs import DecodeGraphs
+from paged_kv_gqa_pkv_gb300.workloads import bf16_bits
+from tests import spec_cases as S
+from tests.parity import assert_attention_close
+
+pytestmark = pytest.mark.gpu
+
+
+def decode_close(m, rng, slots, hq):
+    """One token of decode on each slot, by the framework's own decode."""
+    q = torch.from_numpy(rng.standard_normal((len(slots), hq, 128)).astype(np.float32)).bfloat16()
+    scale = 1 / math.sqrt(128)
+    out, lse = binding.pkv_decode_attention(m.k, m.v, m.table, q.cuda(), m.i32(slots),
+                                            m.i32(m.lens[slots]), m.ps, scale, dev_err=m.err)
+    ro, rl, bad = orc.decode_attention(bf16_bits(q), m.host.k, m.host.v, m.host.table,
+                                       np.array(slots), m.lens[slots], m.ps, scale)
+    assert not bad
+    assert_attention_close(out.cpu(), lse.cpu(), ro, rl, tag="decode")
+
+
+@pytest.mark.parametrize("ps,N", [(16, 8), (64, 40)])
+def test_a_loop_of_steps(ps, N):
+    rng = np.random.default_rng(ps)
+    m = S.Mirror(1, [70, 33, 129, 1], ps, 2, 160, -(-800 // ps), slots=9)
+    slots = [1, 2, 3, 4]
+    for step in range(6):
+        S.draft_step(m, rng, slots, N, hq=8, V=97, shape=["random", "chain", "star"][step % 3])
+        if step == 1:      # two users branch off user 2, mid-page
+            keep = int(m.lens[2])
+            m.update([5, 6], [2, 2], [keep, keep - 3], [keep, keep])
+            m.lens[5], m.lens[6] = keep, keep - 3
+            slots = [1, 2, 3, 4, 5, 6]
+        if step == 3:      # one user leaves, the pool is packed
+            m.update([3], [0], [0], [0])
+            slots = [1, 2, 4, 5, 6]
+            live = m.compact()
+            assert live == int((m.host.refs > 0).sum())
+        decode_close(m, rng, slots, 8)
+    m.equal()
+
+
+def test_steps_between_captured_decode_steps():
+    """The table that captured decode steps hold is updated by the page
+    operators between replays."""
+    rng = np.random.default_rng(5)
+    m = S.Mirror(2, [60, 20], 16, 2, 60, 12, slots=5)
+    scale = 1 / math.sqrt(128)
+    g = DecodeGraphs(m.k, m.v, m.table, 16, 8, scale, buckets=(2, 4))
+    slots = [1, 2]
+    for step in range(4):
+        S.draft_step(m, rng, slots, 6, hq=8, V=50)
+        if step == 1:
+            m.update([3], [1], [int(m.lens[1])], [int(m.lens[1])])
+            m.lens[3] = m.lens[1]
+            slots = [1, 2, 3]
+        if step == 2:
+            m.compact()
+        ctx = m.lens[slots].copy()
+        m.update(slots, slots, ctx, ctx + 1)
+        B = len(slots)
+        t = lambda *s: torch.from_numpy(  # noqa: E731
+            rng.standard_normal(s).astype(np.float32)).bfloat16()
+        q, kn, vn = t(B, 8, 128), t(B, 2, 128), t(B, 2, 128)
+        out, lse = g.step(q.cuda(), kn.cuda(), vn.cuda(), m.i32(slots), m.i32(ctx),
+                          m.i32(ctx + 1))[:2]
+        h = m.host
+        h.k, h.v, bad = orc.append(h.k, h.v, h.table, bf16_bits(kn), bf16_bits(vn),
+                                   np.array(slots), ctx, 16)
+        m.lens[slots] += 1
+        ro, rl, bad2 = orc.decode_attention(bf16_bits(q), h.k, h.v, h.table, np.array(slots),
+                                            ctx + 1, 16, scale)
+        assert not bad and not bad2
+        assert_attention_close(out.cpu()[:B], lse.cpu()[:B], ro, rl, tag=f"replay {step}")
+        m.equal()
+
+
+def test_a_step_captured_and_replayed():
+    """Reserve, append, attend, verify, commit and truncate in one graph whose
+    lengths live on the device; five replays against the oracle."""
+    rng = np.random.default_rng(9)
+    m = S.Mirror(3, [40, 90, 16], 16, 2, 60, 14, slots=4)
+    slots, N, hq, V, B = [1, 2, 3], 7, 8, 61, 3
+    scale = 1 / math.sqrt(128)
+    h = m.host
+    parents = S.rand_parents(rng, B, N)
+    sl, par = m.i32(slots), m.i32(parents)
+    ctx = m.i32(m.lens[slots])
+    lens = m.i32([N] * B)
+    f32 = dict(dtype=torch.float32, device="cuda")
+    q = torch.zeros((B, N, hq, 128), dtype=torch.bfloat16, device="cuda")
+    kn, vn = (torch.zeros((B * N, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    target = torch.zeros((B, N, V), **f32)
+    tok = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+    u, us = torch.zeros((B, N), **f32), torch.zeros(B, **f32)
+    out, lse = torch.empty_like(q), torch.empty((B, N, hq), **f32)
+    path, toks = torch.empty_like(tok), torch.empty_like(tok)
+    n = torch.empty(B, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(binding.pkv_update_workspace_size(m.k, m.table, 16, B),
+                         binding.pkv_tree_workspace_size(m.k, m.table, 16, B, N, hq)),
+                     dtype=torch.uint8, device="cuda")   # one for all: the calls are in order
+    row_slots = sl.repeat_interleave(N)
+    node = torch.arange(N, dtype=torch.int32, device="cuda").repeat(B)
+
+    def step():
+        top = ctx + N
+        binding.pkv_update_pages(m.k, m.v, m.table, m.refs, sl, sl, ctx, top, 16, workspace=ws,
+                                 dev_err=m.err)
+        binding.pkv_append(m.k, m.v, m.table, kn, vn, row_slots, ctx.repeat_interleave(N) + node,
+                           16, dev_err=m.err)
+        binding.pkv_tree_attention(m.k, m.v, m.table, q, par, lens, sl, ctx, 16, scale, out=out,
+                                   lse=lse, workspace=ws, dev_err=m.err)
+        binding.pkv_verify_tree(target, tok, par, lens, u, us, path=path, tokens=toks,
+                                n_accepted=n, dev_err=m.err)
+        binding.pkv_commit_path(m.k, m.v, m.table, path, n, sl, ctx, 16, new_lens=ctx,
+                                dev_err=m.err)
+        binding.pkv_update_pages(m.k, m.v, m.table, m.refs, sl, sl, ctx, ctx, 16, workspace=ws,
+                                 dev_err=m.err)
+
+    keep = [t.clone() for t in (m.k, m.v, m.table, m.refs, ctx)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                      # a warm-up; its state is put back
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t, old in zip((m.k, m.v, m.table, m.refs, ctx), keep):
+        t.copy_(old)
+    m.err.zero_()
+    for replay in range(5):
+        g = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+        q.copy_(torch.from_numpy(g(B, N, hq, 128)))
+        kn.copy_(torch.from_numpy(g(B * N, 2, 128)))
+        vn.copy_(torch.from_numpy(g(B * N, 2, 128)))
+        target.copy_(torch.softmax(torch.from_numpy(g(B, N, V)), -1))
+        tok.copy_(torch.from_numpy(rng.integers(0, V, (B, N)).astype(np.int32)))
+        u.copy_(torch.from_numpy(rng.random((B, N)).astype(np.float32) * 0.1))
+        us.copy_(torch.from_numpy(rng.random(B).astype(np.float32)))
+        old = ctx.cpu().numpy()
+        graph.replay()
+        torch.cuda.synchronize()
+        h.k, h.v, h.table, h.refs, e0 = spec.update_pages(h.k, h.v, h.table, h.refs, slots, slots,
+                                                          old, old + N, 16)
+        h.k, h.v, bad = orc.append(h.k, h.v, h.table, bf16_bits(kn.cpu()), bf16_bits(vn.cpu()),
+                                   row_slots.cpu().numpy(), np.repeat(old, N) + node.cpu().numpy(),
+                                   16)
+        ro, rl, e1, _ = spec.tree_attention(bf16_bits(q.cpu()), h.k, h.v, h.table, parents,
+                                            np.full(B, N), slots, old, 16, scale)
+        assert_attention_close(out.cpu(), lse.cpu(), ro, rl, tag=f"replay {replay}")
+        wp, wt, wn, e2 = spec.verify_tree(target.double().cpu().numpy(), None, tok.cpu().numpy(),
+                                          parents, np.full(B, N), u.double().cpu().numpy(),
+                                          us.double().cpu().numpy())
+        assert np.array_equal(path.cpu().numpy(), wp) and np.array_equal(toks.cpu().numpy(), wt)
+        h.k, h.v, new, e3 = spec.commit_path(h.k, h.v, h.table, wp, wn, slots, old, 16)
+        h.k, h.v, h.table, h.refs, e4 = spec.update_pages(h.k, h.v, h.table, h.refs, slots, slots,
+                                                          new, new, 16)
+        assert not bad and not (e0 | e1 | e2 | e3 | e4)
+        assert np.array_equal(ctx.cpu().numpy(), new)
+        m.equal()
+
+
+def test_two_streams_with_their_own_workspaces():
+    """Two independent caches worked on at once give the bits that each gives
+    alone."""
+    cases = [S.tree_case(1, [3000, 700], [30, 64], 64, hq=8, hkv=2, ps=64),
+             S.tree_case(2, [500] * 12, [8] * 12, 8, hq=8, hkv=2, ps=16)]
+    ver = [S.verify_case(3, 6, 20, 5000), S.verify_case(4, 2, 64, 9000, kind=torch.bfloat16)]
+    to = lambda a: (a if isinstance(a, torch.Tensor) else torch.from_numpy(a)).cuda()  # noqa: E731
+    ta = [[to(x) for x in (c.k, c.v, c.table, c.q, c.parents, c.lens, c.slots, c.ctx)] +
+          [c.ps, c.scale] for c in cases]
+    va = [([to(x) for x in (c.target, c.tokens, c.parents, c.lens, c.u, c.us)], to(c.draft))
+          for c in ver]
+    alone = [binding.pkv_tree_attention(*a) for a in ta] + \
+            [binding.pkv_verify_tree(*a, draft_probs=d) for a, d in va]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, binding.pkv_tree_attention(*ta[i])))
+                got.append((2 + i, binding.pkv_verify_tree(*va[i][0], draft_probs=va[i][1])))
+    torch.cuda.synchronize()
+    for which, r in got:
+        for x, y in zip(r, alone[which]):
+            assert torch.equal(x, y)
+
+
+def test_a_stream_given_by_name():
+    c = S.tree_case(21, [300, 80], [16, 9], 16)
+    to = lambda a: (a if isinstance(a, torch.Tensor) else torch.from_numpy(a)).cuda()  # noqa: E731
+    args = [to(x) for x in (c.k, c.v, c.table, c.q, c.parents, c.lens, c.slots, c.ctx)] + \
+        [c.ps, c.scale]
+    want = binding.pkv_tree_attention(*args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out, lse = (torch.empty_like(x) for x in want)
+    ws = torch.empty(binding.pkv_tree_workspace_size(args[0], args[2], c.ps, 2, 16, 8),
+                     dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    binding.pkv_tree_attention(*args, out=out, lse=lse, workspace=ws, stream=s)
+    # without buffers of its own: they come from the named stream's memory, so
+    # nothing that the current stream does meanwhile can reuse them
+    more = []
+    for _ in range(20):
+        more.append(binding.pkv_tree_attention(*args, stream=s))
+        torch.full((ws.numel(),), 0xFF, dtype=torch.uint8, device="cuda")
+    s.synchronize()
+    for o, l in [(out, lse)] + more:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+def test_a_context_past_the_reserved_pages_and_a_padded_batch():
+    """Rows of padding name arbitrary lengths and trees and touch nothing."""
+    c = S.tree_case(22, [100, 64, 30], [8, 8, 8], 8, pad=(1,))
+    c.ctx[1], c.lens[1] = -7, 99
+    c.parents[1] = 50
+    to = lambda a: (a if isinstance(a, torch.Tensor) else torch.from_numpy(a)).cuda()  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = binding.pkv_tree_attention(*[to(x) for x in (c.k, c.v, c.table, c.q, c.parents,
+                                                            c.lens, c.slots, c.ctx)], c.ps,
+                                          c.scale, dev_err=err)
+    ro, rl, e, skip = S.tree_oracle(c)
+    assert e == int(err.item()) == 0 and not skip
+    assert_attention_close(out.cpu(), lse.cpu(), ro, rl)
+
+
+def test_verification_of_rows_past_32_bits():
+    """Probabilities whose offset in elements passes 2^31: the last rows."""
+    V, N, B = 1 << 20, 64, 33            # 33 * 64 * 2^20 = 2^31 + 2^26 elements of bf16
+    t = torch.zeros((B, N, V), dtype=torch.bfloat16, device="cuda")
+    t[:, :, 7] = 0.25
+    t[:, :, V - 1] = 0.75
+    tok = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+    tok[:, 1:] = V - 1
+    parents = torch.from_numpy(S.rand_parents(np.random.default_rng(0), B, N, "chain")).cuda()
+    lens = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    u = torch.full((B, N), 0.5, device="cuda")
+    u[:, 40] = 0.9                       # node 40 is refused: 0.9 > 0.75
+    path, toks, n = binding.pkv_verify_tree(t, tok, parents, lens, u,
+                                            torch.full((B,), 0.5, device="cuda"))
+    # nodes 0..39 accepted; without the refused token only token 7 is left
+    assert n.cpu().tolist() == [40] * B
+    assert torch.equal(path[:, :40].cpu(), torch.arange(40).int().expand(B, 40))
+    assert (toks[:, :39] == V - 1).all() and (toks[:, 39] == 7).all()
+
+
+@pytest.mark.parametrize("how", ["small", "misaligned", "device", "type"])
+def test_refused_workspaces_and_outputs(how):
+    m = S.Mirror(4, [30], 16, 1, 8, 4, slots=3)
+    one = m.i32([1])
+    n = binding.pkv_update_workspace_size(m.k, m.table, 16, 1)
+    ws = {"small": torch.empty(n - 1, dtype=torch.uint8, device="cuda"),
+          "misaligned": torch.empty(n + 64, dtype=torch.uint8, device="cuda")[64:],
+          "device": torch.empty(n, dtype=torch.uint8),
+          "type": torch.empty(n, dtype=torch.uint8, device="cuda")}[how]
+    refs = m.refs.long() if how == "type" else m.refs
+    with pytest.raises((ValueError, binding.PkvError)):
+        binding.pkv_update_pages(m.k, m.v, m.table, refs, one, one, m.i32([30]), m.i32([40]), 16,
+                                 workspace=ws)
+    m.equal()
