@@ -477,8 +477,8 @@ pkv_status pkv_tree_attention(const pkv_cache_desc* cache, const void* k_pool,
  * r(v) > 0 and sum_{w <= v} r(w) > u_sample[b] * sum_w r(w), or the highest v
  * with r(v) > 0 where rounding leaves none; from p where r has no mass. (The
  * accepted tokens and the next one are then distributed as the target's.)
- * Decisions and sums are held to about 2^-45 of their terms, so that they do
- * not depend on an order of summation in fp32.
+ * Sums are held to about 2^-40 and decisions to 2^-45 of their terms, so that
+ * they do not depend on an order of summation in fp32.
  *
  * path: int32 [batch, n_nodes], the accepted nodes (0 first), -1 behind them;
  * n_accepted: int32 [batch], their number (>= 1); tokens: int32 [batch,

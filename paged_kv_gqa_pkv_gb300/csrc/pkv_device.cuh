@@ -119,6 +119,16 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                : "memory");
 }
 
+// Closes the calling thread's group of cp.async copies; waits until at most kLeft
+// of its groups are in flight.
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // The calling thread's earlier cp.async copies arrive on `bar` once they have
 // completed. The barrier's pending count rises now (no .noinc), so a phase
 // armed after this call cannot complete before those copies land.

@@ -27,6 +27,8 @@
 // 48 bits, added in a fixed order, two values per instruction (a pass is bound by
 // instruction issue about as much as by its bytes); doubles are left to the walking warp's few
 // decisions. p and q are exact in fp32 whatever their type.
+#include <atomic>
+
 #include "pkv.h"
 #include "pkv_launch.h"
 
@@ -36,6 +38,7 @@ namespace {
 constexpr int kMaxWarps = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = PKV_MAX_TREE_NODES;
+constexpr int kDepth = 6;  // granules of each row in flight per thread
 
 struct VerifyParams {
   const void* target;
@@ -100,11 +103,12 @@ __device__ __forceinline__ Pair shfl_xor(const Pair& x, int o) {
   return {__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
 }
 
-// Sum over the warp's 32 lanes, the same bits in every lane: the two partners of
-// a step add in one order.
+// Sum over each kLanes lanes of the warp, the same bits in all of them: the two
+// partners of a step add in one order.
+template <int kLanes = 32>
 __device__ __forceinline__ Pair warp_sum(Pair x, int lane) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < kLanes; o <<= 1) {
     const Pair y = shfl_xor(x, o);
     Pair a = (lane & o) ? y : x;
     add(a, (lane & o) ? x : y);
@@ -141,25 +145,38 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
   return r;
 }
 
-// Two running pair sums side by side.
+// Two running pair sums side by side of x m for m of 0 or 1. They start from kBase,
+// so that no summand of a probability vector passes the running sum and the
+// error of each addition is the short form's three operations; values from 2 kBase
+// on (of rows that sum to more than 1) are summed to fp32 accuracy.
 struct Sum2 {
+  static constexpr float kBase = 1.f;
   Two hi, lo;
-  __device__ __forceinline__ void add(Two x) {
-    const Two minus = pack2(-1.f, -1.f);
-    const Two t = add2(hi, x);
-    const Two bb = fma2(hi, minus, t);                   // t - hi, exactly rounded like it
-    const Two e1 = fma2(fma2(bb, minus, t), minus, hi);  // hi - (t - bb)
-    lo = add2(lo, add2(e1, fma2(bb, minus, x)));
+  __device__ __forceinline__ void clear() {
+    hi = pack2(kBase, kBase);
+    lo = 0ull;
+  }
+  __device__ __forceinline__ void add(Two x, Two m) {
+    const Two t = fma2(x, m, hi);
+    const Two back = fma2(t, pack2(-1.f, -1.f), hi);  // hi - t, exact
+    lo = add2(lo, fma2(x, m, back));
     hi = t;
   }
   __device__ __forceinline__ Pair total() const {
     Pair a, b;
     unpack2(hi, a.hi, b.hi);
     unpack2(lo, a.lo, b.lo);
-    const Pair t = two_sum(a.hi, b.hi);
-    return {t.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), t.lo)};
+    const Pair t = two_sum(__fsub_rn(a.hi, kBase), __fsub_rn(b.hi, kBase));
+    return two_sum(t.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), t.lo));
   }
 };
+
+// 1 where d > 0, else 0 (NaN: 0)
+__device__ __forceinline__ float positive(float d) {
+  float m;
+  asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(m) : "f"(d), "f"(0.f));
+  return m;
+}
 
 // a > b, as the sums they stand for.
 __device__ __forceinline__ bool above(const Pair& a, const Pair& b) {
@@ -177,6 +194,16 @@ template <>
 struct Elem<float> {
   static constexpr int kPer = 4;  // values per 16-byte granule
   static __device__ __forceinline__ float get(const float* p) { return *p; }
+  // the granule with negative and NaN entries as 0, and with kFinite infinity as the
+  // largest finite value
+  template <bool kFinite>
+  static __device__ __forceinline__ uint4 clean4(const uint4& w) {
+    const auto f = [](uint32_t u) {
+      const float x = fmaxf(__uint_as_float(u), 0.f);
+      return __float_as_uint(kFinite ? fminf(x, 3.402823466e38f) : x);
+    };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+  }
   static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
     x[0] = __uint_as_float(w.x);
     x[1] = __uint_as_float(w.y);
@@ -188,6 +215,16 @@ template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int kPer = 8;
   static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  template <bool kFinite>
+  static __device__ __forceinline__ uint4 clean4(const uint4& w) {
+    const auto f = [](uint32_t u) {
+      uint32_t r;
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0u));
+      if (kFinite) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x7F7F7F7Fu));
+      return r;
+    };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+  }
   static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -212,8 +249,12 @@ struct RowView {
     base = start - off;
     end = off + vocab;
   }
+  // granules, and those that lie inside the row: [first_whole, end_whole)
+  __device__ __forceinline__ int granules() const { return (end + Elem<T>::kPer - 1) / Elem<T>::kPer; }
+  __device__ __forceinline__ int first_whole() const { return off > 0 ? 1 : 0; }
+  __device__ __forceinline__ int end_whole() const { return end / Elem<T>::kPer; }
   __device__ __forceinline__ bool inside(int g) const {
-    return g * Elem<T>::kPer >= off && (g + 1) * Elem<T>::kPer <= end;
+    return g >= first_whole() && g < end_whole();
   }
   __device__ __forceinline__ uint4 whole(int g) const {
     return *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(g) * Elem<T>::kPer);
@@ -263,11 +304,13 @@ struct Walk {
   const int64_t row0;  // this sequence's first row
   const uint32_t rank;
   const int lane, warp;
+  uint4* ring;  // this thread's slots: [kDepth][p, q], kThreads apart
   int passes = 0;
+  static constexpr int kThreads = kWarps * 32;
 
   // granules [g0, g1) of a row are warp wp's of this CTA
   __device__ __forceinline__ void range_of(const RowView<T>& v, int wp, int& g0, int& g1) const {
-    const int total = (v.end + Elem<T>::kPer - 1) / Elem<T>::kPer;
+    const int total = v.granules();
     const int warps = p.cluster * kWarps;
     const int per = ((total + warps - 1) / warps + 31) / 32 * 32;
     const int64_t w = static_cast<int64_t>(rank) * kWarps + wp;
@@ -296,6 +339,9 @@ struct Walk {
   }
 
   // This warp's part of the ordered sums: p and q over the tokens with p > a q.
+  // A thread's granules come through kDepth slots of its own in shared memory, so
+  // that a row's pass waits for memory about once (with four loads in flight
+  // per thread a pass of few rows took 6.5 us for 76 KB per CTA, all of it latency).
   __device__ __forceinline__ void sum_part() const {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
@@ -304,62 +350,83 @@ struct Walk {
     int g0, g1;
     range_of(pv, warp, g0, g1);
     constexpr int E = Elem<T>::kPer;
-    constexpr int kUnroll = 16 / E;  // 16-byte loads per row and thread in flight
-    Sum2 ps = {0ull, 0ull}, qs = {0ull, 0ull};
+    Sum2 ps, qs;
+    ps.clear();
+    qs.clear();
     const Two mah = pack2(-ah, -ah), mal = pack2(-al, -al);
-    for (int g = g0 + lane; g < g1; g += 32 * kUnroll) {
-      uint4 xw[kUnroll], yw[kUnroll];
+    auto take = [&](int i, const float(&x)[E], const float(&y)[E]) {
+      if (with_q) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = g + 32 * u;
-        if (i < g1 && pv.inside(i)) {
-          xw[u] = pv.whole(i);
-          if (with_q) yw[u] = qv.whole(i);
+        for (int e = 0; e < E; e += 2) {
+          // p - a q to single rounding twice: its sign is that of the exact
+          // difference unless that is below 2^-48 of its terms
+          const Two x2 = pack2(x[e], x[e + 1]), y2 = pack2(y[e], y[e + 1]);
+          float d0, d1;
+          unpack2(fma2(mal, y2, fma2(mah, y2, x2)), d0, d1);
+          const Two m = pack2(positive(d0), positive(d1));
+          ps.add(x2, m);  // (an infinite p tells itself by the sum)
+          qs.add(y2, m);
         }
+      } else {
+        float z[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) z[e] = 1.f;
+        if constexpr (!kDraft) {
+          for (int k = 0; k < s.n_refused; ++k) {
+            const int at = s.refused[k] + pv.off - i * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (at == e) z[e] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) ps.add(pack2(x[e], x[e + 1]), pack2(z[e], z[e + 1]));
       }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = g + 32 * u;
-        if (i >= g1) continue;
+    };
+    // the granules that hang over the row's ends, value by value
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int i = k == 0 ? 0 : pv.granules() - 1;
+      if (lane == 0 && i >= g0 && i < g1 && !pv.inside(i) && (k == 0 || i > 0)) {
         float x[E], y[E];
-        if (pv.inside(i)) {
-          Elem<T>::unpack(xw[u], x);
-          if (with_q) Elem<T>::unpack(yw[u], y);
-        } else {
-          pv.values(i, x);
-          if (with_q) qv.values(i, y);
-        }
+        pv.values(i, x);
+        if (with_q) qv.values(i, y);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           x[e] = clean(x[e]);
-          if (with_q) y[e] = clean(y[e]);
+          y[e] = with_q ? fminf(clean(y[e]), 3.402823466e38f) : 0.f;
         }
-        if (with_q) {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            // p - a q to single rounding twice: its sign is that of the exact
-            // difference unless that is below 2^-48 of its terms
-            const Two x2 = pack2(x[e], x[e + 1]), y2 = pack2(y[e], y[e + 1]);
-            float d0, d1;
-            unpack2(fma2(mal, y2, fma2(mah, y2, x2)), d0, d1);
-            // (an infinite p tells itself by the sum)
-            ps.add(pack2(d0 > 0.f ? x[e] : 0.f, d1 > 0.f ? x[e + 1] : 0.f));
-            qs.add(pack2(d0 > 0.f ? y[e] : 0.f, d1 > 0.f ? y[e + 1] : 0.f));
-          }
-        } else {
-          if constexpr (!kDraft) {
-            for (int k = 0; k < s.n_refused; ++k) {
-              const int at = s.refused[k] + pv.off - i * E;
-#pragma unroll
-              for (int e = 0; e < E; ++e)
-                if (at == e) x[e] = 0.f;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < E; e += 2) ps.add(pack2(x[e], x[e + 1]));
-        }
+        take(i, x, y);
       }
     }
+    g0 = max(g0, pv.first_whole());
+    g1 = min(g1, pv.end_whole());
+    const uint4* from_p = reinterpret_cast<const uint4*>(pv.base) + lane;
+    const uint4* from_q = reinterpret_cast<const uint4*>(qv.base) + lane;
+    auto fetch = [&](int g, int slot) {
+      if (g + lane < g1) {
+        cp_async16(ring + (2 * slot) * kThreads, from_p + g);
+        if (with_q) cp_async16(ring + (2 * slot + 1) * kThreads, from_q + g);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) fetch(g0 + 32 * k, k);
+    int slot = 0;
+    for (int g = g0; g < g1; g += 32) {
+      cp_async_wait<kDepth - 1>();
+      if (g + lane < g1) {
+        float x[E], y[E];
+        // (0 x infinity is not 0: q is made finite)
+        const uint4 yw = with_q ? ring[(2 * slot + 1) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+        Elem<T>::unpack(Elem<T>::template clean4<false>(ring[(2 * slot) * kThreads]), x);
+        Elem<T>::unpack(Elem<T>::template clean4<true>(yw), y);
+        take(g + lane, x, y);
+      }
+      fetch(g + 32 * kDepth, slot);  // (the slot's values have been used)
+      slot = slot + 1 < kDepth ? slot + 1 : 0;
+    }
+    cp_async_wait<0>();
     const Pair sp = warp_sum(ps.total(), lane);
     Pair sq = {0.f, 0.f};
     if (with_q) sq = warp_sum(qs.total(), lane);
@@ -389,12 +456,9 @@ struct Walk {
     __syncthreads();
     sum_part();
     __syncthreads();
-    Pair sp = {0.f, 0.f}, sq = {0.f, 0.f};
-    if (lane < kWarps) {
-      sp = s.warp_p[lane];
-      sq = s.warp_q[lane];
-    }
-    const double mine = mass_of(warp_sum(sp, lane), warp_sum(sq, lane));
+    // (every kWarps lanes add the same numbers in the same order)
+    const double mine = mass_of(warp_sum<kWarps>(s.warp_p[lane % kWarps], lane),
+                                warp_sum<kWarps>(s.warp_q[lane % kWarps], lane));
     double* slots = s.cta_sum[passes & 1];
     if (lane < p.cluster) cluster_store(&slots[rank], lane, mine);
     // one barrier per pass: the next pass writes the other half, and the one
@@ -459,20 +523,32 @@ struct Walk {
     constexpr int E = Elem<T>::kPer;
     const int per = (g1 - g0 + kWarps * 32 - 1) / (kWarps * 32);
     const int a0 = min(g0 + (32 * warp + lane) * per, g1), a1 = min(a0 + per, g1);
-    auto granule = [&](int g, Pair (&tm)[E]) {
+    const bool with_q = kDraft && ah != 0.f;
+    // a granule that lies inside the row comes as it was loaded, in xw and yw
+    auto granule = [&](int g, const uint4& xw, const uint4& yw, Pair (&tm)[E]) {
       float x[E], y[E];
-      pv.values(g, x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = 0.f;
-      if (kDraft && ah != 0.f) qv.values(g, y);
+      Elem<T>::unpack(xw, x);
+      Elem<T>::unpack(yw, y);
+      if (!pv.inside(g)) {
+        pv.values(g, x);
+        if (with_q) qv.values(g, y);
+      }
       terms(ah, al, g, pv.off, x, y, tm);
     };
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    auto raw_p = [&](int g) { return g < a1 && pv.inside(g) ? pv.whole(g) : none; };
+    auto raw_q = [&](int g) { return with_q && g < a1 && qv.inside(g) ? qv.whole(g) : none; };
     Pair acc = {0.f, 0.f};
-    for (int g = a0; g < a1; ++g) {
-      Pair tm[E];
-      granule(g, tm);
+    for (int g = a0; g < a1; g += 2) {
+      const uint4 xw[2] = {raw_p(g), raw_p(g + 1)}, yw[2] = {raw_q(g), raw_q(g + 1)};
 #pragma unroll
-      for (int e = 0; e < E; ++e) add(acc, tm[e]);
+      for (int k = 0; k < 2; ++k) {
+        if (g + k >= a1) break;
+        Pair tm[E];
+        granule(g + k, xw[k], yw[k], tm);
+#pragma unroll
+        for (int e = 0; e < E; ++e) add(acc, tm[e]);
+      }
     }
     Pair incl = acc;
 #pragma unroll
@@ -521,7 +597,7 @@ struct Walk {
       bool found = false;
       for (int g = a0; g < a1 && !found; ++g) {
         Pair tm[E];
-        granule(g, tm);
+        granule(g, raw_p(g), raw_q(g), tm);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           if (tm[e].hi > 0.f && !found) {
@@ -541,6 +617,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1024 / (kWarps * 32))
 verify_tree_kernel(const VerifyParams p) {
   constexpr int kThreads = kWarps * 32;
   __shared__ Shared s;
+  extern __shared__ __align__(16) uint4 ring[];
   pdl_wait_primary();
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / p.cluster;
@@ -597,7 +674,7 @@ verify_tree_kernel(const VerifyParams p) {
   }
   __syncthreads();
 
-  Walk<T, kDraft, kWarps> walk{p, s, n0, rank, lane, warp};
+  Walk<T, kDraft, kWarps> walk{p, s, n0, rank, lane, warp, ring + threadIdx.x};
   int count = 1;
   bool ok = false;
   if (warp == 0) {
@@ -713,10 +790,21 @@ int pick_cluster(int vocab) {
 }
 
 template <typename T, bool kDraft, int kWarps>
-cudaError_t launch(const VerifyParams& p, int batch, cudaStream_t stream) {
+cudaError_t launch(const VerifyParams& p, int batch, int dev, cudaStream_t stream) {
+  constexpr int kRingBytes = kDepth * 2 * kWarps * 32 * 16;
+  // the shared-memory opt-in, once per device; host threads may race to set it
+  static std::atomic<bool> attr_set[64] = {};
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(verify_tree_kernel<T, kDraft, kWarps>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRingBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch) * p.cluster);
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -733,10 +821,10 @@ cudaError_t launch(const VerifyParams& p, int batch, cudaStream_t stream) {
 // 16 warps a CTA while two CTAs per SM hold every row's cluster, else 8 (four CTAs
 // per SM): more warps shorten a row's pass, more CTAs keep the rows in one wave.
 template <typename T, bool kDraft>
-cudaError_t launch_for(const VerifyParams& p, int batch, int sms, cudaStream_t stream) {
+cudaError_t launch_for(const VerifyParams& p, int batch, int sms, int dev, cudaStream_t stream) {
   return static_cast<int64_t>(batch) * p.cluster <= 2 * sms
-             ? launch<T, kDraft, 16>(p, batch, stream)
-             : launch<T, kDraft, 8>(p, batch, stream);
+             ? launch<T, kDraft, 16>(p, batch, dev, stream)
+             : launch<T, kDraft, 8>(p, batch, dev, stream);
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
@@ -768,6 +856,8 @@ extern "C" pkv_status pkv_verify_tree(const void* target_probs, const void* draf
   int sms = 0;
   const pkv_status st = device_info(&sms);
   if (st != PKV_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_DEVICE;
   VerifyParams p;
   p.target = target_probs;
   p.draft = draft_probs;
@@ -785,10 +875,10 @@ extern "C" pkv_status pkv_verify_tree(const void* target_probs, const void* draf
   p.cluster = pick_cluster(vocab);
   cudaError_t e;
   if (probs_type == PKV_PROBS_FP32)
-    e = draft_probs ? launch_for<float, true>(p, batch, sms, stream)
-                    : launch_for<float, false>(p, batch, sms, stream);
+    e = draft_probs ? launch_for<float, true>(p, batch, sms, dev, stream)
+                    : launch_for<float, false>(p, batch, sms, dev, stream);
   else
-    e = draft_probs ? launch_for<__nv_bfloat16, true>(p, batch, sms, stream)
-                    : launch_for<__nv_bfloat16, false>(p, batch, sms, stream);
+    e = draft_probs ? launch_for<__nv_bfloat16, true>(p, batch, sms, dev, stream)
+                    : launch_for<__nv_bfloat16, false>(p, batch, sms, dev, stream);
   return record_cuda_status(e);
 }
