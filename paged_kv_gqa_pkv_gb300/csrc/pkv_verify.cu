@@ -25,8 +25,8 @@
 // row), so terms and sums are unevaluated pairs of floats by the classical
 // error-free sum and product (Knuth, Dekker; the product's error by an FMA), about
 // 48 bits, added in a fixed order, two values per instruction (a pass is bound by
-// instruction issue about as much as by its bytes); doubles are left to the walking warp's few
-// decisions. p and q are exact in fp32 whatever their type.
+// instruction issue about as much as by its bytes). p and q are exact in fp32
+// whatever their type.
 #include <atomic>
 
 #include "pkv.h"
@@ -117,11 +117,44 @@ __device__ __forceinline__ Pair warp_sum(Pair x, int lane) {
   return x;
 }
 
+// Inclusive running sums over the lanes, for lanes below kLanes.
+template <int kLanes>
+__device__ __forceinline__ Pair scan(Pair x, int lane) {
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+    Pair y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+    if (lane >= o) {
+      add(y, x);
+      x = y;
+    }
+  }
+  return x;
+}
+
+__device__ __forceinline__ Pair shfl(const Pair& x, int from) {
+  return {__shfl_sync(0xffffffffu, x.hi, from), __shfl_sync(0xffffffffu, x.lo, from)};
+}
+
+__device__ __forceinline__ Pair times(const Pair& a, const Pair& b) {
+  const float prod = __fmul_rn(a.hi, b.hi);
+  float err = __fmaf_rn(a.hi, b.hi, -prod);
+  err = __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, err));
+  return two_sum(prod, err);
+}
+
+// max(a - b, 0); NaN stays
+__device__ __forceinline__ Pair minus(const Pair& a, const Pair& b) {
+  const Pair d = two_sum(a.hi, -b.hi);
+  const Pair r = two_sum(d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo)));
+  return r.hi < 0.f ? Pair{0.f, 0.f} : r;
+}
+
 // *(the same shared-memory location in CTA `rank` of the cluster) = v
-__device__ __forceinline__ void cluster_store(double* at, uint32_t rank, double v) {
+__device__ __forceinline__ void cluster_store(Pair* at, uint32_t rank, const Pair& v) {
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.hi), "f"(v.lo)
+               : "memory");
 }
 
 // Two floats per instruction.
@@ -182,10 +215,6 @@ __device__ __forceinline__ float positive(float d) {
 __device__ __forceinline__ bool above(const Pair& a, const Pair& b) {
   const Pair x = two_sum(a.hi, a.lo);
   return x.hi > b.hi || (x.hi == b.hi && x.lo > b.lo);
-}
-
-__device__ __forceinline__ double value(const Pair& x) {
-  return static_cast<double>(x.hi) + static_cast<double>(x.lo);
 }
 
 template <typename T>
@@ -275,7 +304,7 @@ struct RowView {
 
 // What a pass sums: max(p - a q, 0) with the refused tokens left out.
 struct Residual {
-  double a;
+  Pair a;
   int n_refused;
 };
 
@@ -288,12 +317,11 @@ struct Shared {
   int refused[kNodes];                // tokens refused at the current node (no draft rows)
   Pair warp_p[kMaxWarps];             // sums of p and q over the residual's tokens of the
   Pair warp_q[kMaxWarps];             // last pass, this CTA's warps
-  double cta_sum[2][kMaxCluster];     // the residual's, of the last two passes, all CTAs
+  Pair cta_sum[2][kMaxCluster];       // the residual's, of the last two passes, all CTAs
   // the walking warp's order to the others
   int order, node, n_refused, draw_warp, count;
   int first[kMaxWarps], last[kMaxWarps];  // of the draw, lanes per warp
-  float ah, al;
-  double a;
+  Pair a;
   Pair draw_at;  // how far into the draw's warp
 };
 
@@ -338,23 +366,20 @@ struct Walk {
     }
   }
 
-  // This warp's part of the ordered sums: p and q over the tokens with p > a q.
-  // A thread's granules come through kDepth slots of its own in shared memory, so
-  // that a row's pass waits for memory about once (with four loads in flight
-  // per thread a pass of few rows took 6.5 us for 76 KB per CTA, all of it latency).
-  __device__ __forceinline__ void sum_part() const {
-    const RowView<T> pv(p.target, row0 + s.node, p.vocab);
-    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
-    const float ah = s.ah, al = s.al;
-    const bool with_q = kDraft && ah != 0.f;
-    int g0, g1;
-    range_of(pv, warp, g0, g1);
-    constexpr int E = Elem<T>::kPer;
+  // Sums of p and q over the tokens with p > a q, a granule at a time.
+  struct Sums {
+    static constexpr int E = Elem<T>::kPer;
     Sum2 ps, qs;
-    ps.clear();
-    qs.clear();
-    const Two mah = pack2(-ah, -ah), mal = pack2(-al, -al);
-    auto take = [&](int i, const float(&x)[E], const float(&y)[E]) {
+    Two mah, mal;
+    bool with_q;
+    __device__ __forceinline__ Sums(const Pair& a, bool with)
+        : mah(pack2(-a.hi, -a.hi)), mal(pack2(-a.lo, -a.lo)), with_q(with) {
+      ps.clear();
+      qs.clear();
+    }
+    // x, y: cleaned p and q of the tokens from `first` on
+    __device__ __forceinline__ void take(const Shared& s, int first, const float (&x)[E],
+                                         const float (&y)[E]) {
       if (with_q) {
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
@@ -373,7 +398,7 @@ struct Walk {
         for (int e = 0; e < E; ++e) z[e] = 1.f;
         if constexpr (!kDraft) {
           for (int k = 0; k < s.n_refused; ++k) {
-            const int at = s.refused[k] + pv.off - i * E;
+            const int at = s.refused[k] - first;
 #pragma unroll
             for (int e = 0; e < E; ++e)
               if (at == e) z[e] = 0.f;
@@ -382,7 +407,22 @@ struct Walk {
 #pragma unroll
         for (int e = 0; e < E; e += 2) ps.add(pack2(x[e], x[e + 1]), pack2(z[e], z[e + 1]));
       }
-    };
+    }
+  };
+
+  // This warp's part of the ordered sums: p and q over the tokens with p > a q.
+  // A thread's granules come through kDepth slots of its own in shared memory, so
+  // that a row's pass waits for memory about once (with four loads in flight
+  // per thread a pass of few rows took 6.5 us for 76 KB per CTA, all of it latency).
+  __device__ __forceinline__ void sum_part() const {
+    const RowView<T> pv(p.target, row0 + s.node, p.vocab);
+    const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
+    const float ah = s.a.hi, al = s.a.lo;
+    const bool with_q = kDraft && ah != 0.f;
+    int g0, g1;
+    range_of(pv, warp, g0, g1);
+    constexpr int E = Elem<T>::kPer;
+    Sums acc(s.a, with_q);
     // the granules that hang over the row's ends, value by value
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
@@ -396,7 +436,7 @@ struct Walk {
           x[e] = clean(x[e]);
           y[e] = with_q ? fminf(clean(y[e]), 3.402823466e38f) : 0.f;
         }
-        take(i, x, y);
+        acc.take(s, i * E - pv.off, x, y);
       }
     }
     g0 = max(g0, pv.first_whole());
@@ -421,90 +461,79 @@ struct Walk {
         const uint4 yw = with_q ? ring[(2 * slot + 1) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
         Elem<T>::unpack(Elem<T>::template clean4<false>(ring[(2 * slot) * kThreads]), x);
         Elem<T>::unpack(Elem<T>::template clean4<true>(yw), y);
-        take(g + lane, x, y);
+        acc.take(s, (g + lane) * E - pv.off, x, y);
       }
       fetch(g + 32 * kDepth, slot);  // (the slot's values have been used)
       slot = slot + 1 < kDepth ? slot + 1 : 0;
     }
     cp_async_wait<0>();
-    const Pair sp = warp_sum(ps.total(), lane);
+    const Pair sp = warp_sum(acc.ps.total(), lane);
     Pair sq = {0.f, 0.f};
-    if (with_q) sq = warp_sum(qs.total(), lane);
+    if (with_q) sq = warp_sum(acc.qs.total(), lane);
     if (lane == 0) {
       s.warp_p[warp] = sp;
       s.warp_q[warp] = sq;
     }
   }
 
-  // sum p - a sum q, not below 0
-  __device__ __forceinline__ double mass_of(const Pair& sp, const Pair& sq) const {
-    const double r = value(sp) - s.a * value(sq);
-    return r < 0.0 ? 0.0 : r;
-  }
-
   // The walking warp: sum of the residual at node c over the whole vocabulary,
-  // the same double in every lane of every CTA of the cluster.
-  __device__ double sum(int c, const Residual& r) {
+  // the same bits in every lane of every CTA of the cluster.
+  __device__ Pair sum(int c, const Residual& r) {
     if (lane == 0) {
       s.order = kSum;
       s.node = c;
       s.n_refused = r.n_refused;
       s.a = r.a;
-      s.ah = static_cast<float>(r.a);
-      s.al = static_cast<float>(r.a - static_cast<double>(s.ah));
     }
     __syncthreads();
     sum_part();
     __syncthreads();
     // (every kWarps lanes add the same numbers in the same order)
-    const double mine = mass_of(warp_sum<kWarps>(s.warp_p[lane % kWarps], lane),
-                                warp_sum<kWarps>(s.warp_q[lane % kWarps], lane));
-    double* slots = s.cta_sum[passes & 1];
+    const Pair mine = minus(warp_sum<kWarps>(s.warp_p[lane % kWarps], lane),
+                            times(r.a, warp_sum<kWarps>(s.warp_q[lane % kWarps], lane)));
+    Pair* slots = s.cta_sum[passes & 1];
     if (lane < p.cluster) cluster_store(&slots[rank], lane, mine);
     // one barrier per pass: the next pass writes the other half, and the one
     // after that follows a barrier that every CTA reaches after these reads
     __syncwarp();
     cluster_sync();
     ++passes;
-    double all = lane < p.cluster ? slots[lane] : 0.0;
-#pragma unroll
-    for (int o = 1; o < kMaxCluster; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    return __shfl_sync(0xffffffffu, all, 0);
+    const int at = lane % kMaxCluster;
+    return warp_sum<kMaxCluster>(at < p.cluster ? slots[at] : Pair{0.f, 0.f}, lane);
   }
 
   // The walking warp: which CTA and warp hold the token drawn at t of the last
   // pass's sum, and what lies in front of them: the first whose running sum passes
   // t, or where rounding leaves none the last one with any mass.
-  __device__ __forceinline__ void place(double t) {
-    const double* slots = s.cta_sum[(passes - 1) & 1];
-    double base = 0.0;
-    const int cta = pick(lane < p.cluster ? slots[lane] : 0.0, t, base);
+  __device__ __forceinline__ void place(const Pair& t, const Residual& r) {
+    const Pair none = {0.f, 0.f};
+    const Pair of_cta = lane < p.cluster ? s.cta_sum[(passes - 1) & 1][lane] : none;
+    const Pair of_warp =
+        lane < kWarps ? minus(s.warp_p[lane], times(r.a, s.warp_q[lane])) : none;
+    const Pair ctas = scan<kMaxCluster>(of_cta, lane), warps = scan<kMaxWarps>(of_warp, lane);
+    Pair base = none;
+    const int cta = pick(of_cta.hi > 0.f, ctas, t, base);
     int w = -1;
+    // (a sum above 0 has a token with p > a q in it, whatever its parts round to)
     if (static_cast<int>(rank) == cta)
-      w = pick(lane < kWarps ? mass_of(s.warp_p[lane], s.warp_q[lane]) : 0.0, t, base);
+      w = pick(lane < kWarps && s.warp_p[lane].hi > 0.f, warps, t, base);
     if (lane == 0) {
       s.order = kDraw;
       s.draw_warp = w;
-      const double at = t - base;
-      s.draw_at.hi = static_cast<float>(at);
-      s.draw_at.lo = static_cast<float>(at - static_cast<double>(s.draw_at.hi));
+      s.draw_at = minus(t, base);
     }
   }
 
-  // Lane of the first running sum of x past t (from `base` on), else the last
-  // lane with x > 0; base becomes the sum in front of it.
-  __device__ __forceinline__ int pick(double x, double t, double& base) const {
-    double incl = x;
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, lane < 16 && base + incl > t && x > 0.0);
-    const uint32_t some = __ballot_sync(0xffffffffu, lane < 16 && x > 0.0);
+  // Lane of the first running sum past t (from `base` on), else the last lane that
+  // has any token of the residual; base becomes the sum in front of it.
+  __device__ __forceinline__ int pick(bool has, const Pair& incl, const Pair& t,
+                                      Pair& base) const {
+    Pair here = base;
+    add(here, incl);
+    const uint32_t past = __ballot_sync(0xffffffffu, has && above(here, t));
+    const uint32_t some = __ballot_sync(0xffffffffu, has);
     const int at = past != 0u ? __ffs(past) - 1 : 31 - __clz(some | 1u);
-    const double front = __shfl_sync(0xffffffffu, incl - x, at);
-    base += front;
+    if (at > 0) add(base, shfl(incl, at - 1));
     return at;
   }
 
@@ -516,7 +545,7 @@ struct Walk {
   __device__ int draw() {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
-    const float ah = s.ah, al = s.al;
+    const float ah = s.a.hi, al = s.a.lo;
     const Pair t = s.draw_at;
     int g0, g1;
     range_of(pv, s.draw_warp, g0, g1);
@@ -525,59 +554,47 @@ struct Walk {
     const int a0 = min(g0 + (32 * warp + lane) * per, g1), a1 = min(a0 + per, g1);
     const bool with_q = kDraft && ah != 0.f;
     // a granule that lies inside the row comes as it was loaded, in xw and yw
-    auto granule = [&](int g, const uint4& xw, const uint4& yw, Pair (&tm)[E]) {
-      float x[E], y[E];
+    auto cleaned = [&](int g, const uint4& xw, const uint4& yw, float (&x)[E], float (&y)[E]) {
       Elem<T>::unpack(xw, x);
       Elem<T>::unpack(yw, y);
       if (!pv.inside(g)) {
         pv.values(g, x);
         if (with_q) qv.values(g, y);
       }
-      terms(ah, al, g, pv.off, x, y, tm);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] = clean(x[e]);
+        y[e] = fminf(clean(y[e]), 3.402823466e38f);
+      }
     };
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     auto raw_p = [&](int g) { return g < a1 && pv.inside(g) ? pv.whole(g) : none; };
     auto raw_q = [&](int g) { return with_q && g < a1 && qv.inside(g) ? qv.whole(g) : none; };
-    Pair acc = {0.f, 0.f};
+    Sums sums(s.a, with_q);
     for (int g = a0; g < a1; g += 2) {
       const uint4 xw[2] = {raw_p(g), raw_p(g + 1)}, yw[2] = {raw_q(g), raw_q(g + 1)};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (g + k >= a1) break;
-        Pair tm[E];
-        granule(g + k, xw[k], yw[k], tm);
-#pragma unroll
-        for (int e = 0; e < E; ++e) add(acc, tm[e]);
+        float x[E], y[E];
+        cleaned(g + k, xw[k], yw[k], x, y);
+        sums.take(s, (g + k) * E - pv.off, x, y);
       }
     }
-    Pair incl = acc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      Pair v = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
-      if (lane >= o) {
-        add(v, incl);
-        incl = v;
-      }
-    }
+    const Pair all_p = sums.ps.total();
+    const bool has = all_p.hi > 0.f;
+    const Pair acc = minus(all_p, times(s.a, sums.qs.total()));
+    const Pair incl = scan<32>(acc, lane);
     if (lane == 31) s.warp_p[warp] = incl;
     __syncthreads();
     // what lies in front of this warp, then of this thread
-    Pair front = lane < kWarps ? s.warp_p[lane] : Pair{0.f, 0.f};
-#pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) {
-      Pair v = {__shfl_up_sync(0xffffffffu, front.hi, o), __shfl_up_sync(0xffffffffu, front.lo, o)};
-      if (lane >= o) {
-        add(v, front);
-        front = v;
-      }
-    }
-    front = {__shfl_sync(0xffffffffu, front.hi, max(warp - 1, 0)),
-             __shfl_sync(0xffffffffu, front.lo, max(warp - 1, 0))};
+    const Pair warps = scan<kMaxWarps>(lane < kWarps ? s.warp_p[lane] : Pair{0.f, 0.f}, lane);
+    Pair front = shfl(warps, max(warp - 1, 0));
     if (warp == 0) front = {0.f, 0.f};
     Pair here = front;
     add(here, incl);
-    const uint32_t past = __ballot_sync(0xffffffffu, above(here, t) && acc.hi > 0.f);
-    const uint32_t some = __ballot_sync(0xffffffffu, acc.hi > 0.f);
+    const uint32_t past = __ballot_sync(0xffffffffu, has && above(here, t));
+    const uint32_t some = __ballot_sync(0xffffffffu, has);
     if (lane == 0) {
       s.first[warp] = past != 0u ? __ffs(past) - 1 : -1;
       s.last[warp] = some != 0u ? 31 - __clz(some) : -1;
@@ -596,11 +613,14 @@ struct Walk {
       if (lane > 0) add(front, before);
       bool found = false;
       for (int g = a0; g < a1 && !found; ++g) {
+        float x[E], y[E];
         Pair tm[E];
-        granule(g, raw_p(g), raw_q(g), tm);
+        cleaned(g, raw_p(g), raw_q(g), x, y);
+        terms(ah, al, g, pv.off, x, y, tm);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (tm[e].hi > 0.f && !found) {
+          const bool in = with_q ? fmaf(-al, y[e], fmaf(-ah, y[e], x[e])) > 0.f : tm[e].hi > 0.f;
+          if (in && !found) {
             at = g * E + e - pv.off;
             add(front, tm[e]);
             found = above(front, t);
@@ -674,6 +694,7 @@ verify_tree_kernel(const VerifyParams p) {
   }
   __syncthreads();
 
+  const float u_sample = p.u_sample[b];
   Walk<T, kDraft, kWarps> walk{p, s, n0, rank, lane, warp, ring + threadIdx.x};
   int count = 1;
   bool ok = false;
@@ -681,8 +702,8 @@ verify_tree_kernel(const VerifyParams p) {
     const int par0 = s.parent[lane], par1 = s.parent[lane + 32];
     int cur = 0;
     uint64_t on_path = 1;
-    Residual r = {0.0, 0};
-    double mass = 1.0;
+    Residual r = {{0.f, 0.f}, 0};
+    Pair mass = {1.f, 0.f};
     bool summed = false;  // the last pass summed the residual at hand
     while (true) {
       uint64_t kids = static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == cur)) |
@@ -691,35 +712,33 @@ verify_tree_kernel(const VerifyParams p) {
       while (kids != 0) {
         const int x = __ffsll(static_cast<long long>(kids)) - 1;
         kids &= kids - 1;
-        double rx;
+        Pair rx = {s.p[x], 0.f};
         bool take;
-        if (r.a == 0.0 && r.n_refused == 0) {
-          // a node's first child, R = 1: u q against p, exactly and without doubles
+        if (r.a.hi == 0.f && r.n_refused == 0) {
+          // a node's first child, R = 1: u q against p, exactly
           const float prod = __fmul_rn(s.u[x], s.q[x]);
           const float rest = __fmaf_rn(s.u[x], s.q[x], -prod);
           take = prod < s.p[x] || (prod == s.p[x] && rest < 0.f);
-          rx = s.p[x];
         } else {
-          rx = s.p[x];
           if constexpr (kDraft) {
-            rx -= r.a * static_cast<double>(s.q[x]);
-            rx = rx > 0.0 ? rx : 0.0;
+            rx = residual(s.p[x], s.q[x], r.a.hi, r.a.lo);
           } else {
             for (int k = 0; k < r.n_refused; ++k)
-              if (s.refused[k] == s.token[x]) rx = 0.0;
+              if (s.refused[k] == s.token[x]) rx.hi = 0.f;
           }
-          take = static_cast<double>(s.u[x]) * static_cast<double>(s.q[x]) * mass < rx;
+          take = above(rx, times(times({s.u[x], 0.f}, {s.q[x], 0.f}), mass));
         }
         if (take) {
           next = x;
           break;
         }
         if constexpr (kDraft) {
-          r.a += mass;
+          add(r.a, mass);
+          r.a = two_sum(r.a.hi, r.a.lo);
           mass = walk.sum(cur, r);
           summed = true;
         } else {
-          mass = mass > rx ? mass - rx : 0.0;
+          mass = minus(mass, rx);
           __syncwarp();
           if (lane == 0) s.refused[r.n_refused] = s.token[x];
           __syncwarp();
@@ -730,17 +749,17 @@ verify_tree_kernel(const VerifyParams p) {
       cur = next;
       ++count;
       on_path |= 1ull << next;
-      r = {0.0, 0};
-      mass = 1.0;
+      r = {{0.f, 0.f}, 0};
+      mass = {1.f, 0.f};
       summed = false;
     }
-    double total = summed ? mass : walk.sum(cur, r);
-    if (total == 0.0 && (r.a != 0.0 || r.n_refused != 0)) {
-      r = {0.0, 0};  // nothing of the target is left: draw from all of it
+    Pair total = summed ? mass : walk.sum(cur, r);
+    if (total.hi == 0.f && (r.a.hi != 0.f || r.n_refused != 0)) {
+      r = {{0.f, 0.f}, 0};  // nothing of the target is left: draw from all of it
       total = walk.sum(cur, r);
     }
-    ok = total > 0.0 && total <= 1.7e308;
-    if (ok) walk.place(static_cast<double>(p.u_sample[b]) * total);
+    ok = total.hi > 0.f && total.hi <= 3.402823466e38f;
+    if (ok) walk.place(times({u_sample, 0.f}, total), r);
     else if (lane == 0) s.order = kLeave;
     if (lane == 0) s.count = count;
     __syncthreads();
