@@ -9,8 +9,11 @@ namespace tree {
 
 namespace {
 constexpr int kMergeThreads = 256;
-constexpr int kMergeCols = 8;          // head dims per merge thread
-constexpr int kMergeUnroll = 4;        // partials in flight per merge thread
+constexpr int kMergeUnroll = 2;        // partials in flight per merge thread
+
+// Head dims per merge thread: column-major partials are read by single floats, and 16
+// dims make whole sectors of the output.
+constexpr int merge_cols(bool row_major) { return row_major ? 8 : 16; }
 }  // namespace
 
 // Joins the partials of items cut by range borders, and writes the rows of
@@ -21,7 +24,8 @@ constexpr int kMergeUnroll = 4;        // partials in flight per merge thread
 // neighbouring addresses: along the head dims where a partial's O is row-major
 // (kRowMajor, the streaming kernel's), along the rows where it is column-major.
 template <bool kRowMajor>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const TreeParams p) {
+  constexpr int kMergeCols = merge_cols(kRowMajor);
   __shared__ float s_part[kMergeThreads][kMergeCols + 2];
   pdl_wait_primary();
   const int tid = threadIdx.x;
@@ -33,6 +37,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
   constexpr int kVecs = kHeadDim / kMergeCols;
   const int rows = min(p.rows - rb * kMaxRows, p.slot_rows);  // of this item
   const int units = rows * kVecs;
+  const int live = p.tree_lens[b] << p.group_shift;  // rows of the sequence's tree
   int w0 = 0, w1 = 0, first_slot = 0;
   if (tiles > 0) {
     const int64_t total = static_cast<int64_t>(p.prefix[p.batch]) * p.items_per_row;
@@ -46,7 +51,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
     first_slot = u == w0 * per ? 0 : 1;  // later ranges hold the item in their first slot
   }
   const int share = tid % split;
-  const int64_t floats = slot_floats(p.slot_rows);
+  const int stride = kRowMajor ? p.slot_rows : kMaxRows;  // rows of a partial
+  const int64_t floats = slot_floats(stride);
   for (int block = blockIdx.y; block * per_block < units; block += gridDim.y) {
     const int unit = block * per_block + tid / split;
     const bool mine = unit < units;
@@ -57,7 +63,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
     float acc[kMergeCols];
 #pragma unroll
     for (int e = 0; e < kMergeCols; ++e) acc[e] = 0.f;
-    if (mine && tiles > 0) {
+    if (mine && tiles > 0 && r < live) {
       for (int w = w0 + share; w <= w1; w += kMergeUnroll * split) {
         float m[kMergeUnroll], l[kMergeUnroll], o[kMergeUnroll][kMergeCols];
 #pragma unroll
@@ -68,8 +74,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
           if (v <= w1) {
             const float* s =
                 p.partials + (2 * static_cast<int64_t>(v) + (v == w0 ? first_slot : 0)) * floats;
-            m[k] = __ldcg(s + static_cast<int64_t>(kHeadDim) * p.slot_rows + prow);
-            l[k] = __ldcg(s + static_cast<int64_t>(kHeadDim + 1) * p.slot_rows + prow);
+            m[k] = __ldcg(s + kHeadDim * stride + prow);
+            l[k] = __ldcg(s + (kHeadDim + 1) * stride + prow);
             if constexpr (kRowMajor) {
               const float4* o4 =
                   reinterpret_cast<const float4*>(s + static_cast<int64_t>(prow) * kHeadDim + col);
@@ -77,9 +83,10 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
               o[k][0] = x.x, o[k][1] = x.y, o[k][2] = x.z, o[k][3] = x.w;
               o[k][4] = y.x, o[k][5] = y.y, o[k][6] = y.z, o[k][7] = y.w;
             } else {
+              const float* at = s + col * kMaxRows + prow;
 #pragma unroll
               for (int e = 0; e < kMergeCols; ++e)
-                o[k][e] = __ldcg(s + static_cast<int64_t>(col + e) * p.slot_rows + prow);
+                o[k][e] = __ldcg(at + e * kMaxRows);
             }
           }
         }
@@ -132,12 +139,15 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
       const float inv = has ? 1.f / L : 0.f;
       const int64_t orow = (static_cast<int64_t>(b) * p.n_nodes + r / p.group) * p.num_q_heads +
                            kvh * p.group + r % p.group;
-      uint4 w;
-      w.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-      w.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-      w.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-      w.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHeadDim + col) = w;
+#pragma unroll
+      for (int e = 0; e < kMergeCols; e += 8) {
+        uint4 w;
+        w.x = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        w.y = pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv);
+        w.z = pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv);
+        w.w = pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHeadDim + col + e) = w;
+      }
       if (col == 0) p.lse[orow] = has ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
   }
@@ -194,7 +204,7 @@ TreeLayout tree_layout(int rows, int workers) {
   TreeLayout l;
   l.off_partials = ((kTreeMaxBatch + 1) * 4 + 255) / 256 * 256;
   const size_t part = 2 * static_cast<size_t>(workers) *
-                      static_cast<size_t>(slot_floats(rows < kMaxRows ? rows : kMaxRows)) * 4;
+                      static_cast<size_t>(slot_floats(slot_rows(rows))) * 4;
   l.total = l.off_partials + (part + 255) / 256 * 256;
   return l;
 }
@@ -218,9 +228,10 @@ cudaError_t launch_merge(const TreeParams& p, int sms, cudaStream_t stream) {
   // about 16 CTAs per SM in all, and no more per item than it has blocks of units
   const int items = p.batch * p.items_per_row;
   const int per_block = kMergeThreads / p.merge_split;
-  const int blocks = (p.slot_rows * (kHeadDim / kMergeCols) + per_block - 1) / per_block;
+  const bool wide = p.rows > kBM;
+  const int blocks = (p.slot_rows * (kHeadDim / merge_cols(!wide)) + per_block - 1) / per_block;
   const int want = (16 * sms + items - 1) / items;
-  return launch_kernel(p.rows > kBM ? tree_merge_kernel<false> : tree_merge_kernel<true>,
+  return launch_kernel(wide ? tree_merge_kernel<false> : tree_merge_kernel<true>,
                        dim3(items, blocks < want ? blocks : want), dim3(kMergeThreads), 0, stream,
                        /*programmatic=*/true, p);
 }
@@ -295,7 +306,7 @@ extern "C" pkv_status pkv_tree_attention(
   p.max_batch = cache->max_batch;
   p.max_blocks = cache->max_blocks;
   p.box_rows = cache->page_size < kBN ? cache->page_size : kBN;
-  p.slot_rows = p.rows < kMaxRows ? p.rows : kMaxRows;
+  p.slot_rows = slot_rows(p.rows);
   p.qscale = scale * 1.4426950408889634f;
   p.page_table = page_table;
   p.dev_err = dev_err;

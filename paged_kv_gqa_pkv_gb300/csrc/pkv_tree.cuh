@@ -63,12 +63,15 @@ struct TreeParams {
   int box_rows;      // rows of one K/V box: min(page_size, 128)
   int workers;       // ranges of the tile list (CTAs, chains or warps)
   int min_tiles;     // shortest range of a worker
-  int slot_rows;     // rows of a partial slot: min(rows, kMaxRows)
+  int slot_rows;     // rows of a partial slot
   int merge_split;   // merge threads that share an item's partials (a power of two)
   float qscale;      // scale * log2(e)
 };
 
-// A partial slot: O [rows][128], then m and l [rows], 16-byte aligned.
+// A partial slot: O [rows][128], or [128][rows] in the wide form, then m and l [rows],
+// 16-byte aligned. The wide form's has kMaxRows rows whatever an item's: with its
+// columns a constant apart the merge spends one instruction per load.
+__host__ __device__ constexpr int slot_rows(int rows) { return rows > kBM ? kMaxRows : rows; }
 __host__ __device__ inline int64_t slot_floats(int rows) {
   return static_cast<int64_t>(rows) * kHeadDim + (2 * rows + 3) / 4 * 4;
 }

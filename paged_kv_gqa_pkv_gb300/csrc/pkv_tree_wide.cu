@@ -60,6 +60,26 @@ __device__ __forceinline__ uint32_t visible_word(int w, int off, uint64_t anc) {
   return 0xffffffffu;
 }
 
+// w[q]: 16-byte piece q of this lane's row. Afterwards w[k] is piece lane % 4 of the row
+// of lane k of this lane's four, so that four lanes write 64 consecutive bytes of a
+// row (a store of 32 rows' pieces takes the memory pipe eight times as long).
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int o) {  // the lane with bit o keeps b and gets the other's
+    const bool up = lane & o;
+    uint4 s = up ? a : b;
+    s.x = __shfl_xor_sync(0xffffffffu, s.x, o);
+    s.y = __shfl_xor_sync(0xffffffffu, s.y, o);
+    s.z = __shfl_xor_sync(0xffffffffu, s.z, o);
+    s.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+    if (up) a = s;
+    else b = s;
+  };
+  swap(w[0], w[1], 1);
+  swap(w[2], w[3], 1);
+  swap(w[0], w[2], 2);
+  swap(w[1], w[3], 2);
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(WideCfg::kThreads, 1)
@@ -245,7 +265,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       const int r = rb * kMaxRows + prow;      // of the sequence
       const bool mine = r < p.rows;
       const int node = r >> p.group_shift;
-      const bool warp_live = __any_sync(0xffffffffu, mine);
       if (sg.b != word_b) {
         bool bad;
         ancestor_words(p.parents + static_cast<int64_t>(sg.b) * p.n_nodes, p.tree_lens[sg.b], lane,
@@ -256,6 +275,9 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       const uint64_t w0 = __shfl_sync(0xffffffffu, word[0], node & 31);
       const uint64_t w1 = __shfl_sync(0xffffffffu, word[1], node & 31);
       const uint64_t anc = mine ? (node < 32 ? w0 : w1) : 0ull;
+      // a warp whose rows are all past the tree leaves its S as P: the products keep
+      // rows apart, and nothing of these is used
+      const bool warp_live = __any_sync(0xffffffffu, anc != 0);
       float m_run = kNoMax;  // running maximum, log2 units
       float l_run = 0.f;
       bool ok = true;
@@ -356,47 +378,55 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       const bool live = mine && anc != 0;
       const bool has = live && ok && l_run != 0.f;  // (a NaN among the scores stays one)
       const float inv = has ? 1.f / l_run : 0.f;
-      const int64_t orow = (static_cast<int64_t>(sg.b) * p.n_nodes + node) * p.num_q_heads +
-                           kvh * p.group + (r & (p.group - 1));
+      const int64_t row00 = static_cast<int64_t>(sg.b) * p.n_nodes * p.num_q_heads + kvh * p.group;
+      auto row_of = [&](int x) -> int64_t {  // of the output
+        return row00 + (x >> p.group_shift) * p.num_q_heads + (x & (p.group - 1));
+      };
       float* slot = p.partials +
                     (2 * static_cast<int64_t>(blockIdx.x) + (first_of_range ? 0 : 1)) *
-                        slot_floats(p.slot_rows);
-      if (warp_live && ok) {
+                        slot_floats(kMaxRows);
+      if (ok && (warp_live || whole)) {
 #pragma unroll 1
         for (int c = 0; c < kHeadDim; c += 32) {
           uint32_t o[32];
           tmem_ld32(t_o + c, o);
           tmem_wait_ld();
-          if (mine && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                                  orow * kHeadDim + c);
+          if (whole) {
+            uint4 w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              w[q] = make_uint4(0u, 0u, 0u, 0u);
               if (has) {
                 const int e = 8 * q;
-                w.x = pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                w[q].x = pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                w[q].y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                w[q].z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                w[q].w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
               }
-              dst[q] = w;
+            }
+            transpose4(w, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rk = r - (lane & 3) + k;
+              if (rk < p.rows)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                          row_of(rk) * kHeadDim + c + 8 * (lane & 3)) = w[k];
             }
           } else if (live) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              slot[static_cast<int64_t>(c + e) * p.slot_rows + prow] = __uint_as_float(o[e]);
+              slot[(c + e) * kMaxRows + prow] = __uint_as_float(o[e]);
           }
           __syncwarp();  // the next TMEM load is warp-collective
         }
-        if (mine) {
-          if (whole) {
-            p.lse[orow] = has ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-          } else {
-            float* ml = slot + static_cast<int64_t>(kHeadDim) * p.slot_rows;
-            ml[prow] = has ? m_run : -INFINITY;
-            ml[p.slot_rows + prow] = has ? l_run : 0.f;
-          }
+      }
+      if (ok && mine) {
+        if (whole) {
+          p.lse[row_of(r)] = has ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* ml = slot + kHeadDim * kMaxRows;
+          ml[prow] = has ? m_run : -INFINITY;
+          ml[kMaxRows + prow] = has ? l_run : 0.f;
         }
       }
       tc_fence_before();

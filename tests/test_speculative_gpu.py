@@ -90,6 +90,23 @@ def test_tree_long_context_is_split(N, group):
     check_tree(S.tree_case(6, [5000, 3333], [N, N - 3], N, hq=2 * group, hkv=2, ps=128))
 
 
+@pytest.mark.parametrize("N,group", [(8, 1), (8, 4), (16, 4), (32, 4), (64, 4), (64, 8)])
+def test_tree_rows_without_keys_of_a_split_item(N, group):
+    """Nodes behind an invalid parent and trees much smaller than N, in items that
+    are cut over many CTAs, with NaN in the workspace."""
+    c = S.tree_case(13, [4000, 2500, 3000], [N, N, max(1, N // 8)], N, hq=2 * group, hkv=2, ps=128)
+    half = max(1, N // 4)
+    c.parents[0, half] = half                      # names itself
+    c.parents[0, half + 1:2 * half] = np.arange(half, 2 * half - 1)
+    c.parents[0, 2 * half:] = 0
+    k, t = dev(c.k), dev(c.table)
+    n = binding.pkv_tree_workspace_size(k, t, c.ps, 3, N, 2 * group)
+    out, lse, err = run_tree(c, workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+    ro, rl, rerr, skip = S.tree_oracle(c)
+    assert err == rerr == spec.BAD_TREE and not skip
+    assert_attention_close(out, lse, ro, rl)
+
+
 def test_tree_many_rows():
     """More batch rows than one launch takes, ragged."""
     rng = np.random.default_rng(7)
