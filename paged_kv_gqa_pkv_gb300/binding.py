@@ -492,6 +492,14 @@ def _cache(k_pool, v_pool, page_table, page_size: int):
     return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, table
 
 
+def _result(name: str, t, dtype: torch.dtype, shape, dev: int, like: torch.Tensor):
+    """The caller's output tensor, or a new one, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _tensor(name, t, dtype, shape, dev)
+
+
 def _scratch(workspace, nbytes: int, dev: int, like: torch.Tensor) -> torch.Tensor:
     """The caller's workspace, or one of the size the call needs."""
     if workspace is None:
@@ -572,18 +580,14 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N, float(scale))
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, N, hq), dtype=torch.float32, device=q.device)
+    out, out_p = _result("out", out, torch.bfloat16, q.shape, dev, q)
+    lse, lse_p = _result("lse", lse, torch.float32, (B, N, hq), dev, q)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     workspace = _scratch(workspace, 0 if workspace is not None else
                          lib.pkv_tree_workspace_size(desc_p, B, N, hq), dev, q)
     _run("pkv_tree_attention", dev, stream, lib.pkv_tree_attention, desc_p, k, v, table, *args,
-         _tensor("out", out, torch.bfloat16, q.shape, dev),
-         _tensor("lse", lse, torch.float32, (B, N, hq), dev), workspace.data_ptr(),
-         workspace.nbytes, _dev_err(dev_err, dev))
+         out_p, lse_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
     return out, lse
 
 
@@ -613,15 +617,11 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("u_accept", u_accept, torch.float32, nodes, dev),
             _tensor("u_sample", u_sample, torch.float32, rows, dev), B, N)
-    if path is None:
-        path = torch.empty(nodes, dtype=i32, device=target_probs.device)
-    if tokens is None:
-        tokens = torch.empty(nodes, dtype=i32, device=target_probs.device)
-    if n_accepted is None:
-        n_accepted = torch.empty(rows, dtype=i32, device=target_probs.device)
-    _run("pkv_verify_tree", dev, stream, load_library().pkv_verify_tree, *args,
-         _tensor("path", path, i32, nodes, dev), _tensor("tokens", tokens, i32, nodes, dev),
-         _tensor("n_accepted", n_accepted, i32, rows, dev), _dev_err(dev_err, dev))
+    path, path_p = _result("path", path, i32, nodes, dev, target_probs)
+    tokens, tokens_p = _result("tokens", tokens, i32, nodes, dev, target_probs)
+    n_accepted, n_p = _result("n_accepted", n_accepted, i32, rows, dev, target_probs)
+    _run("pkv_verify_tree", dev, stream, load_library().pkv_verify_tree, *args, path_p, tokens_p,
+         n_p, _dev_err(dev_err, dev))
     return path, tokens, n_accepted
 
 
@@ -640,10 +640,9 @@ def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx
             _tensor("n_accepted", n_accepted, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N)
-    if new_lens is None:
-        new_lens = torch.empty(rows, dtype=i32, device=path.device)
+    new_lens, new_p = _result("new_lens", new_lens, i32, rows, dev, path)
     _run("pkv_commit_path", dev, stream, load_library().pkv_commit_path, ctypes.byref(desc), k, v,
-         table, *args, _tensor("new_lens", new_lens, i32, rows, dev), _dev_err(dev_err, dev))
+         table, *args, new_p, _dev_err(dev_err, dev))
     return new_lens
 
 
@@ -695,13 +694,11 @@ def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num
     entries and counts), in place. Returns num_live [1], how many there are."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     refs = _tensor("page_refs", page_refs, torch.int32, (desc.num_pages,), dev)
-    if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=page_refs.device)
+    num_live, live_p = _result("num_live", num_live, torch.int32, (1,), dev, page_refs)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     workspace = _scratch(workspace, 0 if workspace is not None else
                          lib.pkv_compact_workspace_size(desc_p), dev, k_pool)
     _run("pkv_compact_pages", dev, stream, lib.pkv_compact_pages, desc_p, k, v, table, refs,
-         _tensor("num_live", num_live, torch.int32, (1,), dev), workspace.data_ptr(),
-         workspace.nbytes, _dev_err(dev_err, dev))
+         live_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
     return num_live

@@ -108,15 +108,16 @@ __device__ __forceinline__ void close_segment(Segment& s, int64_t left) {
   s.t1 = left < s.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.tiles;
 }
 
-// The segment that starts at tile u of the list (below u_end).
+// The segment that starts at tile u of the list (below u_end). Warp-collective: the
+// rows that end at or before u are counted 32 at a time (a binary search's dependent
+// reads took half a microsecond of every worker's start).
 __device__ __forceinline__ Segment first_segment(const int32_t* prefix, int batch, int ipr,
                                                  int64_t u, int64_t u_end) {
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(prefix[mid + 1]) * ipr > u) hi = mid;
-    else lo = mid + 1;
-  }
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int k = 0; k < batch; k += 32)
+    lo += __popc(__ballot_sync(0xffffffffu, k + lane < batch &&
+                                                static_cast<int64_t>(prefix[k + lane + 1]) * ipr <= u));
   Segment s;
   s.b = lo;
   s.tiles = prefix[lo + 1] - prefix[lo];
