@@ -324,44 +324,43 @@ __device__ __forceinline__ void produce(const TreeParams& p, const CUtensorMap& 
       const int c = i / tpc;
       const int have = (c & 1) ? rows[1] : rows[0];
       const int lane0 = (i - c * tpc) * nsub;
-      int at[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(0xffffffffu, have, (lane0 + k) & 31);
+      const uint32_t s = L % kRing;
       bool good = true;
       if (lane == 0) {
-        const uint32_t s = L % kRing;
-        if (L >= kRing && !wait_or_abort(&ring_empty[s], ((L / kRing) - 1) & 1, s_abort)) {
-          good = false;
-        } else {
-          uint8_t* dst = ring + s * kTileBytes;
-          mbar_arrive_expect_tx(&ring_full[s], kTileBytes);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k < nsub) {
-              tma_load_4d_hint(dst + k * R * 128, map, &ring_full[s], 0, at[k], 0, kvh, pol);
-              tma_load_4d_hint(dst + kHalf + k * R * 128, map, &ring_full[s], 0, at[k], 1, kvh,
-                               pol);
-            }
-          }
-        }
+        good = L < kRing || wait_or_abort(&ring_empty[s], ((L / kRing) - 1) & 1, s_abort);
+        if (good) mbar_arrive_expect_tx(&ring_full[s], kTileBytes);
       }
       good = __shfl_sync(0xffffffffu, good, 0);
-      if (good) ++L;
-      return good;
+      if (!good) return false;
+      uint8_t* dst = ring + s * kTileBytes;
+#pragma unroll 1
+      for (int k = 0; k < nsub; ++k) {
+        const int at = __shfl_sync(0xffffffffu, have, (lane0 + k) & 31);
+        if (lane == 0) {
+          tma_load_4d_hint(dst + k * R * 128, map, &ring_full[s], 0, at, 0, kvh, pol);
+          tma_load_4d_hint(dst + kHalf + k * R * 128, map, &ring_full[s], 0, at, 1, kvh, pol);
+        }
+      }
+      ++L;
+      return true;
     };
     // ring order = the issuers' order: K_0, then K_{i+1} (if any) and V_i; Q
-    // goes out behind the first K tile, whose place is free earlier
-    bool ok = load(&kmap, 0) && load_q();
-    for (int i = 0; ok && i < n; ++i) {
-      if (i > 0 && i % tpc == 0) {
-        // V enters chunk c: chunk c - 1 is done with, c + 1 takes its place
+    // goes out behind the first K tile, whose place is free earlier. (One copy of
+    // the code for all of them: the kernels' loops have to fit the instruction cache.)
+    bool ok = true;
+    for (int k = 0; ok && k < 2 * n; ++k) {
+      const bool is_k = k == 0 || ((k & 1) && k + 1 < 2 * n);
+      const int i = is_k ? (k + 1) >> 1 : k + 1 < 2 * n ? (k >> 1) - 1 : n - 1;
+      // the tile before the first V of chunk c: chunk c - 1 is done with after it, and
+      // its place goes to chunk c + 1 when V enters chunk c
+      if (!is_k && i > 0 && i % tpc == 0) {
         const int c = i / tpc;
         const int more = (c + 1) * tpc < n ? chunk_rows(sg, c + 1) : 0;
         if (c & 1) rows[0] = more;
         else rows[1] = more;
       }
-      if (i + 1 < n) ok = load(&kmap, i + 1);
-      ok = ok && load(&vmap, i);
+      ok = load(is_k ? &kmap : &vmap, i);
+      if (k == 0) ok = ok && load_q();
     }
     sg = nx;
     if (!ok && lane == 0) *s_abort = 1;

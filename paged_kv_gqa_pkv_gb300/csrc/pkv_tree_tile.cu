@@ -13,14 +13,17 @@
 // barrier that carries that question. P is at most 2^kRescaleThreshold, and its
 // rounding to bf16 is relative, so nothing is lost by a maximum that lags.
 //
-// Bound by the K/V stream where contexts are long (8 x 32768 keys: 166 us at 32 rows, 172
-// us at 128, 94 / 91 % of the copy bandwidth); where they are short by the ends of
-// segments, ~5 us each, in which a warpgroup joins its sums, writes its rows and takes
-// the next first maximum (64 sequences x 8 kv heads of ~768 keys: 55 us at 32 rows, 92
-// us at 128). Up to 64 rows a CTA is two workers, so that one's segment ends fall into
-// the other's tiles.
-#include <type_traits>
-
+// Bound by the K/V stream where contexts are long (8 x 32768 keys: 163 us at 32 rows, 169
+// us at 128, 96 / 93 % of the copy bandwidth); where they are short by the ends of
+// segments, in which a warpgroup joins its sums, writes its rows and takes the next
+// first maximum (64 sequences x 8 kv heads of ~768 keys: 44 us at 32 rows, 68 us at
+// 128). Up to 64 rows a CTA is two workers, so that one's segment ends fall into the
+// other's tiles.
+//
+// Every step stands in the code once, rolled into loops: five roles share an SM's
+// instruction cache, and what is fetched anew waits behind the K/V stream. With
+// first steps and second attempts written out, warps had no instruction for a third of
+// their stalls, and the short contexts took 54 and 81 us, the long ones 169 and 176.
 #include "pkv_tree.cuh"
 
 namespace pkv {
@@ -270,15 +273,11 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
       };
       bool ok = true;
       if constexpr (!kSingle) {
-        if (warp == 2)
-          for (int i = 0; ok && i < n; ++i) ok = issue_s(i);
-        else
-          for (int i = 0; ok && i < n; ++i) ok = issue_o(i);
+        for (int i = 0; ok && i < n; ++i) ok = warp == 2 ? issue_s(i) : issue_o(i);
       } else {
-        ok = issue_s(0);
-        for (int i = 0; ok && i < n; ++i) {
+        for (int i = -1; ok && i < n; ++i) {
           if (i + 1 < n) ok = issue_s(i + 1);
-          ok = ok && issue_o(i);
+          if (i >= 0) ok = ok && issue_o(i);
         }
       }
       base += 2 * n;
@@ -356,18 +355,19 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
           tmem_ld_frag<kNX>(t_s + (16u << 16), x[1]);
           tmem_wait_ld();
           if (off < kBN) {
-            // this lane's keys are 32 quad + g + 8 j: bit 8 j of a row's word shifted
-            // down by k0 = their distance from the tree (context below it: ones)
-            const int k0 = 32 * quad + g - off;
+            // this lane's keys are 32 quad + g + 8 j: bits 8 j of a row's word (with 32
+            // ones below it: the context) from bit `from` on
+            const int from = max(32 * quad + g - off + 32, 0);
+            const int part = from >> 5, sh = from & 31;
 #pragma unroll
             for (int c = 0; c < kNX; ++c)
 #pragma unroll
               for (int d = 0; d < 2; ++d) {
                 const uint64_t w = column_word(8 * c + 2 * t + d);
-                uint32_t v;
-                if (k0 >= 0) v = k0 < 64 ? static_cast<uint32_t>(w >> k0) : 0u;
-                else v = k0 > -32 ? (static_cast<uint32_t>(w) << -k0) | ((1u << -k0) - 1u) : ~0u;
-                if (w == 0) v = 0;
+                const uint32_t w0 = static_cast<uint32_t>(w), w1 = static_cast<uint32_t>(w >> 32);
+                const uint32_t a = part == 0 ? ~0u : part == 1 ? w0 : part == 2 ? w1 : 0u;
+                const uint32_t b = part == 0 ? w0 : part == 1 ? w1 : 0u;
+                const uint32_t v = (w0 | w1) != 0u ? __funnelshift_r(a, b, sh) : 0u;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                   if (!((v >> (8 * j)) & 1u)) x[j >> 1][4 * c + 2 * (j & 1) + d] = -INFINITY;
@@ -392,75 +392,83 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           return top > kRescaleThreshold;
         };
-        load();
-        if (i == 0 || named_bar_or(bar, kGroupThreads, shift())) {
-          // ---- the rows' maxima of this tile, then the new running ones ----
-          if (i > 0) load();  // (S has not been given back yet)
-          // P's place is free once the chain's last product has read it (and
-          // the last segment's numbers have been read from it); O is at rest
-          if (tc > 0) failed |= !wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
-          tc_fence_after();
-          // the scratch is these rows' place in P: [4 warps][kCols], the factors
-          float* scratch = reinterpret_cast<float*>(sMine);
-          float* factor = scratch + 4 * kCols;
+        for (bool slow = i == 0;; slow = true) {
+          load();  // (S has not been given back yet)
+          if (slow) {
+            // ---- the rows' maxima of this tile, then the new running ones ----
+            // P's place is free once the chain's last product has read it (and
+            // the last segment's numbers have been read from it); O is at rest
+            if (tc > 0) failed |= !wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
+            tc_fence_after();
+            // the scratch is these rows' place in P: [4 warps][kCols], the factors
+            float* scratch = reinterpret_cast<float*>(sMine);
+            float* factor = scratch + 4 * kCols;
+            float mx[kNX][2];
 #pragma unroll
-          for (int c = 0; c < kNX; ++c) {
-            float mx[2];
+            for (int c = 0; c < kNX; ++c)
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              mx[d] = fmaxf(fmaxf(x[0][4 * c + d], x[0][4 * c + 2 + d]),
-                            fmaxf(x[1][4 * c + d], x[1][4 * c + 2 + d])) * p.qscale;
+              for (int d = 0; d < 2; ++d)
+                mx[c][d] = fmaxf(fmaxf(x[0][4 * c + d], x[0][4 * c + 2 + d]),
+                                 fmaxf(x[1][4 * c + d], x[1][4 * c + 2 + d])) * p.qscale;
+            // (shuffles stay in program order: all columns' of a step side by side)
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1)
-                mx[d] = fmaxf(mx[d], __shfl_xor_sync(0xffffffffu, mx[d], o));
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+              for (int c = 0; c < kNX; ++c)
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                  mx[c][d] = fmaxf(mx[c][d], __shfl_xor_sync(0xffffffffu, mx[c][d], o));
+            if (g == 0) {
+#pragma unroll
+              for (int c = 0; c < kNX; ++c)
+                *reinterpret_cast<float2*>(scratch + quad * kCols + 8 * c + 2 * t) =
+                    make_float2(mx[c][0], mx[c][1]);
             }
-            if (g == 0)
-              *reinterpret_cast<float2*>(scratch + quad * kCols + 8 * c + 2 * t) =
-                  make_float2(mx[0], mx[1]);
-          }
-          named_bar_sync(bar, kGroupThreads);
+            named_bar_sync(bar, kGroupThreads);
 #pragma unroll
-          for (int c = 0; c < kNX; ++c) {
-            float2 mx = make_float2(-INFINITY, -INFINITY);
+            for (int c = 0; c < kNX; ++c) {
+              float2 all = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(scratch + w * kCols + 8 * c + 2 * t);
-              mx.x = fmaxf(mx.x, v.x);
-              mx.y = fmaxf(mx.y, v.y);
-            }
-            if (i == 0) {  // nothing to rescale yet
-              m_run[c][0] = fmaxf(mx.x, kNoMax);
-              m_run[c][1] = fmaxf(mx.y, kNoMax);
-              continue;
-            }
-            float f[2];
+              for (int w = 0; w < 4; ++w) {
+                const float2 v = *reinterpret_cast<const float2*>(scratch + w * kCols + 8 * c + 2 * t);
+                all.x = fmaxf(all.x, v.x);
+                all.y = fmaxf(all.y, v.y);
+              }
+              if (i == 0) {  // nothing to rescale yet
+                m_run[c][0] = fmaxf(all.x, kNoMax);
+                m_run[c][1] = fmaxf(all.y, kNoMax);
+                continue;
+              }
+              float f[2];
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const float old = m_run[c][d], top = d ? mx.y : mx.x;
-              const bool grow = top > old + kRescaleThreshold || (old == kNoMax && top > old);
-              f[d] = grow ? (old == kNoMax ? 0.f : ex2(old - top)) : 1.f;
-              if (grow) m_run[c][d] = top;
-              l_run[c][d] *= f[d];
+              for (int d = 0; d < 2; ++d) {
+                const float old = m_run[c][d], top = d ? all.y : all.x;
+                const bool grow = top > old + kRescaleThreshold || (old == kNoMax && top > old);
+                f[d] = grow ? (old == kNoMax ? 0.f : ex2(old - top)) : 1.f;
+                if (grow) m_run[c][d] = top;
+                l_run[c][d] *= f[d];
+              }
+              if (quad == 0 && g == 0)
+                *reinterpret_cast<float2*>(factor + 8 * c + 2 * t) = make_float2(f[0], f[1]);
             }
-            if (i > 0 && quad == 0 && g == 0)
-              *reinterpret_cast<float2*>(factor + 8 * c + 2 * t) = make_float2(f[0], f[1]);
-          }
-          named_bar_sync(bar, kGroupThreads);  // (and the scratch has been read)
-          if (i > 0) {
+            named_bar_sync(bar, kGroupThreads);  // (and the scratch has been read)
+            if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(t_o + c, o);
-              tmem_wait_ld();
+              for (int c = 0; c < kCols; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(t_o + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * factor[c + e]);
-              tmem_st16(t_o + c, o);
+                for (int e = 0; e < 16; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * factor[c + e]);
+                tmem_st16(t_o + c, o);
+              }
+              tmem_wait_st();
+              named_bar_sync(bar, kGroupThreads);  // the factors have been read
             }
-            tmem_wait_st();
-            named_bar_sync(bar, kGroupThreads);  // the factors have been read
           }
-          shift();
+          const bool over = shift();
+          if (slow || !named_bar_or(bar, kGroupThreads, over)) break;
         }
         tc_fence_before();
         mbar_arrive(s_free);
@@ -492,6 +500,14 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
       }
 
       // ---- the segment's end: O / l and the LSE, or a partial ----
+      // this warp's sums, while the last product runs
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int c = 0; c < kNX; ++c)
+#pragma unroll
+          for (int d = 0; d < 2; ++d)
+            l_run[c][d] += __shfl_xor_sync(0xffffffffu, l_run[c][d], o);
       failed |= !wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
       tc_fence_after();
       // in P's place: l [4 warps][kCols], m [kCols]; then per row the
@@ -499,24 +515,16 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
       float* xl = reinterpret_cast<float*>(sMine);
       float* fac = xl + 5 * kCols;
       int* place = reinterpret_cast<int*>(fac + kCols);
+      if (g == 0) {
 #pragma unroll
-      for (int c = 0; c < kNX; ++c) {
+        for (int c = 0; c < kNX; ++c) {
           const int col = 8 * c + 2 * t;
-          float l[2];
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            l[d] = l_run[c][d];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[d] += __shfl_xor_sync(0xffffffffu, l[d], o);
-            if (column_word(col + d) == 0) l[d] = 0.f;  // no live row
-          }
-          if (g == 0) {
-            *reinterpret_cast<float2*>(xl + quad * kCols + col) = make_float2(l[0], l[1]);
-            if (quad == 0)
-              *reinterpret_cast<float2*>(xl + 4 * kCols + col) =
-                  make_float2(m_run[c][0], m_run[c][1]);
-          }
+          *reinterpret_cast<float2*>(xl + quad * kCols + col) =
+              make_float2(l_run[c][0], l_run[c][1]);
+          if (quad == 0)
+            *reinterpret_cast<float2*>(xl + 4 * kCols + col) = make_float2(m_run[c][0], m_run[c][1]);
         }
+      }
       named_bar_sync(bar, kGroupThreads);
       float* slot = p.partials +
                     (2 * static_cast<int64_t>(worker) + (first_of_range ? 0 : 1)) *
@@ -527,7 +535,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
         const float l = (xl[tid] + xl[kCols + tid]) + (xl[2 * kCols + tid] + xl[3 * kCols + tid]);
         const float m = xl[4 * kCols + tid];
         const bool in = r < p.rows && !failed;
-        const bool has = in && l != 0.f;  // (a NaN among the scores stays one)
+        // a live row with keys (a NaN among the scores stays one)
+        const bool has = in && column_word(tid) != 0 && l != 0.f;
         fac[tid] = has ? (whole ? 1.f / l : 1.f) : 0.f;
         const int rel = (r >> p.group_shift) * p.num_q_heads + (r & (p.group - 1));
         place[tid] = in ? (whole ? rel : col0 + tid) : -1;
