@@ -210,13 +210,13 @@ TreeLayout tree_layout(int rows, int workers) {
 }
 
 // The form that serves `rows` query rows per item and `items` items: the streaming
-// one up to 16 rows of many items, the tile form up to 128 rows (two workers per CTA up
+// one up to 8 rows of many items, the tile form up to 128 rows (two workers per CTA up
 // to 64), the wide one above. Both sides of each border are measured at the head of
 // the forms' files.
 enum class Form { kStream, kSingle, kShared, kWide };
 
 Form pick_form(int rows, int64_t items, int sms) {
-  if (rows <= 16 && items >= sms) return Form::kStream;
+  if (rows <= 8 && items >= sms) return Form::kStream;
   return rows <= 64 ? Form::kSingle : rows <= 128 ? Form::kShared : Form::kWide;
 }
 

@@ -1,15 +1,15 @@
-// pkv_tree_stream.cu - tree attention of up to 16 query rows of many items, with
+// pkv_tree_stream.cu - tree attention of up to 8 query rows of many items, with
 // warp-level MMAs.
 //
 // The products are warp-level MMAs in the decode's transposed form, with the rows as
-// their columns (eight at a time): S^T[16 keys x 8 NB rows] = K Q^T, O^T[128 x 8 NB] +=
-// V^T P^T, and a row's whole softmax stays in a warp's registers. Each warp streams
-// its range of 16-key tiles through a ring of TMA stages of its own, so eight ranges
-// per SM hide one another's segment ends, where the warpgroup forms wait. Bound by the
-// K/V stream; with more rows by the warp-level MMAs (about 140 TFLOP/s here), with few
-// items by their many partials. Measured, 64 sequences x 8 kv heads of ~768 keys: 39 /
-// 41 / 55 us at 8 / 16 / 32 rows against 52 / 52 / 55 us in the tile form; 8 sequences,
-// 16 rows: 25 against 18.5 us.
+// their columns: S^T[16 keys x 8 rows] = K Q^T, O^T[128 x 8] += V^T P^T, and a row's whole
+// softmax stays in a warp's registers. Each warp streams its range of 16-key tiles
+// through a ring of TMA stages of its own, so eight ranges per SM hide one another's
+// segment ends, where the warpgroup forms wait. Bound by the K/V stream; with few items by
+// their many partials. Measured against the tile form, 8 kv heads, 8 rows: 64 sequences
+// of ~768 keys 39.1 / 41.6 us, of ~200 keys 19.6 / 23.6 us, 256 of ~768 keys 138 / 146 us,
+// 32 of ~12000 keys 230 / 226 us. At 16 rows (two column blocks) the tile form was
+// the faster: 43.3 / 42.2, 24.4 / 24.0, 146 / 147 and 238 / 227 us.
 #include "pkv_tree.cuh"
 
 namespace pkv {
@@ -22,9 +22,8 @@ constexpr int kStreamStages = 2;          // per warp
 constexpr int kStreamHalf = kStreamTile * 128;
 constexpr int kStreamStage = 4 * kStreamHalf;  // K and V of one tile: 8 KB
 
-template <int NB>
 struct StreamCfg {
-  static constexpr int kQRows = 16;  // two blocks of eight are read at a time
+  static constexpr int kQRows = 8;
   static constexpr int kQHalf = kQRows * 128;
   static constexpr int kOffQ = kStreamWarps * kStreamStages * kStreamStage;
   static constexpr int kOffAnc = kOffQ + kStreamWarps * 2 * kQHalf;    // uint64 [warps][64]
@@ -33,17 +32,16 @@ struct StreamCfg {
   static constexpr int kOffScan = kOffBar + kStreamWarps * kBars * 8;
   static constexpr int kOffPrefix = kOffScan + kStreamWarps * 4;
   static constexpr int kSmemBytes = kOffPrefix + (kTreeMaxBatch + 1) * 4 + 1024;
-  static_assert(NB <= 2 && kSmemBytes <= kMaxDynSmem, "rows and shared memory of one warp");
+  static_assert(kSmemBytes <= kMaxDynSmem, "rows and shared memory of one warp");
 };
 
 }  // namespace
 
-template <int NB>
 __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
-  using C = StreamCfg<NB>;
+  using C = StreamCfg;
   constexpr int S = kStreamStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -174,17 +172,14 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
       __syncwarp();
       word_b = sg.b;
     }
-    float acc[NB][8][4];
-    float m_run[NB][2], l_run[NB][2];
+    float acc[8][4];
+    float m_run[2], l_run[2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nb][mt][e] = 0.f;
-      m_run[nb][0] = m_run[nb][1] = -INFINITY;
-      l_run[nb][0] = l_run[nb][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
+    m_run[0] = m_run[1] = -INFINITY;
+    l_run[0] = l_run[1] = 0.f;
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(q_full, si & 1))) {
       bail = true;
       break;
@@ -198,20 +193,21 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
       const uint32_t sK = smem_u32(stages + s * kStreamStage);
       const uint32_t sV = sK + 2 * kStreamHalf;
 
-      // ---- S^T = K Q^T: 16 keys x 8 NB rows ----
-      float sc[NB][4];
+      // ---- S^T = K Q^T: 16 keys x 8 rows ----
+      float sc[4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int e = 0; e < 4; ++e) sc[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nb][e] = 0.f;
+      for (int kq = 0; kq < 4; ++kq) {  // 32 dims: two K-steps
+        uint32_t qf[4];
+        ldsm_x4(sqa + swzq(mrow, 4 * kq + mtx), qf[0], qf[1], qf[2], qf[3]);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint32_t kf[4];
-        ldsm_x4(sK + swz16((mtx & 1) * 8 + mrow, 2 * kk + (mtx >> 1)), kf[0], kf[1], kf[2], kf[3]);
-        uint32_t q0, q1, q2, q3;
-        ldsm_x4(sqa + swzq((mtx >> 1) * 8 + mrow, 2 * kk + (mtx & 1)), q0, q1, q2, q3);
-        mma_16816(sc[0], kf[0], kf[1], kf[2], kf[3], q0, q1);
-        if constexpr (NB > 1) mma_16816(sc[1], kf[0], kf[1], kf[2], kf[3], q2, q3);
+        for (int e = 0; e < 2; ++e) {
+          uint32_t kf[4];
+          ldsm_x4(sK + swz16((mtx & 1) * 8 + mrow, 4 * kq + 2 * e + (mtx >> 1)), kf[0], kf[1], kf[2],
+                  kf[3]);
+          mma_16816(sc, kf[0], kf[1], kf[2], kf[3], qf[2 * e], qf[2 * e + 1]);
+        }
       }
       // ---- V's fragments, then the stage goes back ----
       uint32_t vf[8][4];
@@ -226,21 +222,17 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
 
       // ---- masks ----
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nb][e] *= p.qscale;
+      for (int e = 0; e < 4; ++e) sc[e] *= p.qscale;
       if (key0 + kStreamTile > ctx) {
         const int r0 = key0 + g - ctx, r1 = r0 + 8;  // node of this lane's keys (< 0: context)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t a = anc[((nb * 8 + 2 * t + h) >> p.group_shift) & 63];
-            const bool v0 = r0 < 0 ? a != 0 : (r0 < 64 && ((a >> r0) & 1ull));
-            const bool v1 = r1 < 0 ? a != 0 : (r1 < 64 && ((a >> r1) & 1ull));
-            if (!v0) sc[nb][h] = -INFINITY;
-            if (!v1) sc[nb][2 + h] = -INFINITY;
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t a = anc[((2 * t + h) >> p.group_shift) & 63];
+          const bool v0 = r0 < 0 ? a != 0 : (r0 < 64 && ((a >> r0) & 1ull));
+          const bool v1 = r1 < 0 ? a != 0 : (r1 < 64 && ((a >> r1) & 1ull));
+          if (!v0) sc[h] = -INFINITY;
+          if (!v1) sc[2 + h] = -INFINITY;
+        }
         // V of keys past the last node: stale slots may hold any bits
         const int valid = ctx + len - key0;
         auto keep = [&](int key) -> uint32_t {  // two keys of one register
@@ -260,51 +252,44 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
       // ---- online softmax (log2 units); a row's maximum moves only when it
       // grows by more than kRescaleThreshold ----
       bool moved = false;
-      float alpha[NB][2];
-      uint32_t pb[NB][2];
+      float alpha[2];
+      uint32_t pb[2];
+      float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float mx0 = fmaxf(sc[nb][0], sc[nb][2]), mx1 = fmaxf(sc[nb][1], sc[nb][3]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-        }
-        const float mx[2] = {mx0, mx1};
-        float base[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float old = m_run[nb][h];
-          const bool grow = old == -INFINITY ? mx[h] != -INFINITY : mx[h] - old > kRescaleThreshold;
-          if (grow) m_run[nb][h] = mx[h];
-          alpha[nb][h] = grow ? ex2(old - mx[h]) : 1.f;
-          moved |= grow && old != -INFINITY;
-          base[h] = m_run[nb][h] == -INFINITY ? 0.f : m_run[nb][h];
-        }
-        const float p0 = ex2(sc[nb][0] - base[0]), p1 = ex2(sc[nb][1] - base[1]);
-        const float p2 = ex2(sc[nb][2] - base[0]), p3 = ex2(sc[nb][3] - base[1]);
-        l_run[nb][0] = l_run[nb][0] * alpha[nb][0] + (p0 + p2);
-        l_run[nb][1] = l_run[nb][1] * alpha[nb][1] + (p1 + p3);
-        pb[nb][0] = movmatrix_trans(pack_bf16x2(p0, p1));
-        pb[nb][1] = movmatrix_trans(pack_bf16x2(p2, p3));
+      for (int o = 4; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
       }
+      const float mx[2] = {mx0, mx1};
+      float base[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float old = m_run[h];
+        const bool grow = old == -INFINITY ? mx[h] != -INFINITY : mx[h] - old > kRescaleThreshold;
+        if (grow) m_run[h] = mx[h];
+        alpha[h] = grow ? ex2(old - mx[h]) : 1.f;
+        moved |= grow && old != -INFINITY;
+        base[h] = m_run[h] == -INFINITY ? 0.f : m_run[h];
+      }
+      const float p0 = ex2(sc[0] - base[0]), p1 = ex2(sc[1] - base[1]);
+      const float p2 = ex2(sc[2] - base[0]), p3 = ex2(sc[3] - base[1]);
+      l_run[0] = l_run[0] * alpha[0] + (p0 + p2);
+      l_run[1] = l_run[1] * alpha[1] + (p1 + p3);
+      pb[0] = movmatrix_trans(pack_bf16x2(p0, p1));
+      pb[1] = movmatrix_trans(pack_bf16x2(p2, p3));
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            acc[nb][mt][0] *= alpha[nb][0];
-            acc[nb][mt][1] *= alpha[nb][1];
-            acc[nb][mt][2] *= alpha[nb][0];
-            acc[nb][mt][3] *= alpha[nb][1];
-          }
+        for (int mt = 0; mt < 8; ++mt) {
+          acc[mt][0] *= alpha[0];
+          acc[mt][1] *= alpha[1];
+          acc[mt][2] *= alpha[0];
+          acc[mt][3] *= alpha[1];
+        }
       }
       // ---- O^T += V^T P^T ----
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          mma_16816(acc[nb][mt], vf[mt][0], vf[mt][1], vf[mt][2], vf[mt][3], pb[nb][0], pb[nb][1]);
+        mma_16816(acc[mt], vf[mt][0], vf[mt][1], vf[mt][2], vf[mt][3], pb[0], pb[1]);
     }
     if (bail) break;
 
@@ -313,66 +298,63 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
     float* slot =
         p.partials + (2 * static_cast<int64_t>(worker) + (first_of_range ? 0 : 1)) *
                          slot_floats(p.slot_rows);
+    bool has[2];
+    float inv[2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      bool has[2];
-      float inv[2];
+    for (int h = 0; h < 2; ++h) {
+      float l = l_run[h];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float l = l_run[nb][h];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const int row = nb * 8 + 2 * t + h;
-        const bool mine = row < p.rows;
-        has[h] = mine && anc[(row >> p.group_shift) & 63] != 0 && l != 0.f;
-        inv[h] = has[h] ? 1.f / l : 0.f;
-        if (mine && g == 0) {
-          if (whole) {
-            const int64_t orow =
-                (static_cast<int64_t>(sg.b) * p.n_nodes + (row >> p.group_shift)) * p.num_q_heads +
-                sg.item * p.group + (row & (p.group - 1));
-            p.lse[orow] =
-                has[h] ? (m_run[nb][h] + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-          } else {
-            float* ml = slot + static_cast<int64_t>(kHeadDim) * p.slot_rows;
-            ml[row] = has[h] ? m_run[nb][h] : -INFINITY;
-            ml[p.slot_rows + row] = has[h] ? l : 0.f;
-          }
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      const int row = 2 * t + h;
+      const bool mine = row < p.rows;
+      has[h] = mine && anc[(row >> p.group_shift) & 63] != 0 && l != 0.f;
+      inv[h] = has[h] ? 1.f / l : 0.f;
+      if (mine && g == 0) {
+        if (whole) {
+          const int64_t orow =
+              (static_cast<int64_t>(sg.b) * p.n_nodes + (row >> p.group_shift)) * p.num_q_heads +
+              sg.item * p.group + (row & (p.group - 1));
+          p.lse[orow] =
+              has[h] ? (m_run[h] + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* ml = slot + static_cast<int64_t>(kHeadDim) * p.slot_rows;
+          ml[row] = has[h] ? m_run[h] : -INFINITY;
+          ml[p.slot_rows + row] = has[h] ? l : 0.f;
         }
       }
-      if (whole) {
-        // transposed back in registers: row g of the block, two dims per lane
-        const int row = nb * 8 + g;
-        __nv_bfloat16* orow =
-            static_cast<__nv_bfloat16*>(p.out) +
-            ((static_cast<int64_t>(sg.b) * p.n_nodes + (row >> p.group_shift)) * p.num_q_heads +
-             sg.item * p.group + (row & (p.group - 1))) *
-                kHeadDim +
-            2 * t;
+    }
+    if (whole) {
+      // transposed back in registers: row g of the block, two dims per lane
+      const int row = g;
+      __nv_bfloat16* orow =
+          static_cast<__nv_bfloat16*>(p.out) +
+          ((static_cast<int64_t>(sg.b) * p.n_nodes + (row >> p.group_shift)) * p.num_q_heads +
+           sg.item * p.group + (row & (p.group - 1))) *
+              kHeadDim +
+          2 * t;
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          const uint32_t lo =
-              movmatrix_trans(pack_bf16x2(has[0] ? acc[nb][mt][0] * inv[0] : 0.f,
-                                          has[1] ? acc[nb][mt][1] * inv[1] : 0.f));
-          const uint32_t hi =
-              movmatrix_trans(pack_bf16x2(has[0] ? acc[nb][mt][2] * inv[0] : 0.f,
-                                          has[1] ? acc[nb][mt][3] * inv[1] : 0.f));
-          if (row < p.rows) {
-            *reinterpret_cast<uint32_t*>(orow + 16 * mt) = lo;
-            *reinterpret_cast<uint32_t*>(orow + 16 * mt + 8) = hi;
-          }
+      for (int mt = 0; mt < 8; ++mt) {
+        const uint32_t lo =
+            movmatrix_trans(pack_bf16x2(has[0] ? acc[mt][0] * inv[0] : 0.f,
+                                        has[1] ? acc[mt][1] * inv[1] : 0.f));
+        const uint32_t hi =
+            movmatrix_trans(pack_bf16x2(has[0] ? acc[mt][2] * inv[0] : 0.f,
+                                        has[1] ? acc[mt][3] * inv[1] : 0.f));
+        if (row < p.rows) {
+          *reinterpret_cast<uint32_t*>(orow + 16 * mt) = lo;
+          *reinterpret_cast<uint32_t*>(orow + 16 * mt + 8) = hi;
         }
-      } else {
+      }
+    } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = nb * 8 + 2 * t + h;
-          if (row < p.rows) {
-            float* o = slot + static_cast<int64_t>(row) * kHeadDim + g;
+      for (int h = 0; h < 2; ++h) {
+        const int row = 2 * t + h;
+        if (row < p.rows) {
+          float* o = slot + static_cast<int64_t>(row) * kHeadDim + g;
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-              o[16 * mt] = acc[nb][mt][h];
-              o[16 * mt + 8] = acc[nb][mt][2 + h];
-            }
+          for (int mt = 0; mt < 8; ++mt) {
+            o[16 * mt] = acc[mt][h];
+            o[16 * mt + 8] = acc[mt][2 + h];
           }
         }
       }
@@ -387,20 +369,11 @@ tree_stream_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-namespace {
-template <int NB>
-cudaError_t launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                   const TreeParams& p, int sms, int dev, cudaStream_t stream) {
-  return launch_form<tree_stream_kernel<NB>>(kStreamWarps * 32, StreamCfg<NB>::kSmemBytes, sms,
-                                             qmap, kmap, vmap, p, dev, stream);
-}
-}  // namespace
-
 cudaError_t launch_stream_form(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, const TreeParams& p, int sms, int dev,
                                cudaStream_t stream) {
-  return p.rows <= 8 ? launch<1>(qmap, kmap, vmap, p, sms, dev, stream)
-                     : launch<2>(qmap, kmap, vmap, p, sms, dev, stream);
+  return launch_form<tree_stream_kernel>(kStreamWarps * 32, StreamCfg::kSmemBytes, sms, qmap, kmap,
+                                         vmap, p, dev, stream);
 }
 
 }  // namespace tree
