@@ -116,6 +116,26 @@ def test_tree_many_rows():
     check_tree(c)
 
 
+@pytest.mark.parametrize("N,group,ps", [(1, 1, 16), (1, 8, 128), (2, 4, 64), (3, 2, 32), (8, 1, 16),
+                                        (4, 2, 256), (2, 2, 48 * 8), (5, 1, 128)])
+def test_tree_many_items_of_few_rows(N, group, ps):
+    """Up to 8 query rows of more items than SMs: the warp-level form. Contexts
+    around its 16-key tiles, long ones that are cut, dead nodes and padding."""
+    rng = np.random.default_rng(N + group)
+    B = 90
+    ctx = rng.integers(0, 100, B)
+    ctx[:8] = [0, 1, 15, 16, 17, 700, 2000, 3000]
+    tree = rng.integers(0, N + 1, B)
+    tree[:8] = N
+    c = S.tree_case(14, ctx.tolist(), tree.tolist(), N, hq=2 * group, hkv=2, ps=ps, pad=(9, 30))
+    if N > 1:
+        c.parents[5, 1] = 7          # no such parent
+    out, lse, err = run_tree(c)
+    ro, rl, rerr, skip = S.tree_oracle(c)
+    assert err == rerr and not skip
+    assert_attention_close(out, lse, ro, rl)
+
+
 def test_tree_bad_entries():
     c = S.tree_case(8, [100, 50, 60, 40, 33, 70], [6, 6, 6, 6, 6, 6], 6)
     c.slots[1] = 99                # past the table
