@@ -119,6 +119,13 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                : "memory");
 }
 
+// The first `bytes` (1 to 16) of a 16-byte granule; the rest of dst is zeroed.
+__device__ __forceinline__ void cp_async16_fill(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
 // Closes the calling thread's group of cp.async copies; waits until at most kLeft
 // of its groups are in flight.
 __device__ __forceinline__ void cp_async_commit() {

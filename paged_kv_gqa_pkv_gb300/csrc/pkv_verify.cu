@@ -20,13 +20,18 @@
 //
 // Arithmetic: a drawn number next to a border has to fall on the side that exact
 // sums give, and fp32 sums of 10^5 terms move borders by more than a token's
-// probability. A pass takes R = sum p - a sum q over the v with p > a q. Doubles are slow on this GPU (a warp's addition holds its SM's unit
-// for some sixteen cycles: every warp taking the decisions redundantly cost 9 us a
-// row), so terms and sums are unevaluated pairs of floats by the classical
-// error-free sum and product (Knuth, Dekker; the product's error by an FMA), about
-// 48 bits, added in a fixed order, two values per instruction (a pass is bound by
-// instruction issue about as much as by its bytes). p and q are exact in fp32
-// whatever their type.
+// probability. A pass takes R = sum p - a sum q over the v with p > a q. Doubles are slow
+// on this GPU (a warp's addition holds its SM's unit for some sixteen cycles, and the walk's
+// dependent ones took about a microsecond a pass), so all of it is in unevaluated pairs of
+// floats by the classical error-free sum and product (Knuth, Dekker; the product's error
+// by an FMA), about 48 bits, added in a fixed order. A pass adds two values per
+// instruction, four instructions a pair (Sum2; seven without its starting value: 35
+// against 31 us); it is bound by instruction issue about as much as by its bytes. p and q
+// are exact in fp32 whatever their type.
+//
+// Measured: one chain of 6 nodes, 32000 tokens, without a draft 6.3 us; 12 trees of 16
+// nodes, 50257 in fp32 14.2 us; 64 trees, 151936 in bf16 30 us, of which the longest row
+// spends three dependent passes (8, then ~5 us each beside the other rows') and a draw.
 #include <atomic>
 
 #include "pkv.h"
@@ -417,36 +422,19 @@ struct Walk {
   __device__ __forceinline__ void sum_part() const {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
-    const float ah = s.a.hi, al = s.a.lo;
-    const bool with_q = kDraft && ah != 0.f;
+    const bool with_q = kDraft && s.a.hi != 0.f;
     int g0, g1;
     range_of(pv, warp, g0, g1);
     constexpr int E = Elem<T>::kPer;
     Sums acc(s.a, with_q);
-    // the granules that hang over the row's ends, value by value
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const int i = k == 0 ? 0 : pv.granules() - 1;
-      if (lane == 0 && i >= g0 && i < g1 && !pv.inside(i) && (k == 0 || i > 0)) {
-        float x[E], y[E];
-        pv.values(i, x);
-        if (with_q) qv.values(i, y);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x[e] = clean(x[e]);
-          y[e] = with_q ? fminf(clean(y[e]), 3.402823466e38f) : 0.f;
-        }
-        acc.take(s, i * E - pv.off, x, y);
-      }
-    }
-    g0 = max(g0, pv.first_whole());
-    g1 = min(g1, pv.end_whole());
     const uint4* from_p = reinterpret_cast<const uint4*>(pv.base) + lane;
     const uint4* from_q = reinterpret_cast<const uint4*>(qv.base) + lane;
+    // (the last granule may hang over the row's end: what lies behind it reads as 0)
     auto fetch = [&](int g, int slot) {
       if (g + lane < g1) {
-        cp_async16(ring + (2 * slot) * kThreads, from_p + g);
-        if (with_q) cp_async16(ring + (2 * slot + 1) * kThreads, from_q + g);
+        const int bytes = min(16, (pv.end - (g + lane) * E) * static_cast<int>(sizeof(T)));
+        cp_async16_fill(ring + (2 * slot) * kThreads, from_p + g, bytes);
+        if (with_q) cp_async16_fill(ring + (2 * slot + 1) * kThreads, from_q + g, bytes);
       }
       cp_async_commit();
     };
@@ -461,6 +449,11 @@ struct Walk {
         const uint4 yw = with_q ? ring[(2 * slot + 1) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
         Elem<T>::unpack(Elem<T>::template clean4<false>(ring[(2 * slot) * kThreads]), x);
         Elem<T>::unpack(Elem<T>::template clean4<true>(yw), y);
+        if (g + lane == 0) {  // the row before ends in the first granule
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (e < pv.off) x[e] = 0.f;
+        }
         acc.take(s, (g + lane) * E - pv.off, x, y);
       }
       fetch(g + 32 * kDepth, slot);  // (the slot's values have been used)
