@@ -18,11 +18,13 @@ constexpr int merge_cols(bool row_major) { return row_major ? 8 : 16; }
 
 // Joins the partials of items cut by range borders, and writes the rows of
 // items that attend nothing. grid (items, parts): a CTA takes every parts-th
-// block of its item's units; a unit is a row and eight head dims (16 bytes of
-// out). merge_split threads share a unit's partials where items have many, each
-// taking every merge_split-th, kMergeUnroll at a time. Neighbouring threads read
-// neighbouring addresses: along the head dims where a partial's O is row-major
-// (kRowMajor, the streaming kernel's), along the rows where it is column-major.
+// block of its item's units; a unit is a row and merge_cols head dims. merge_split
+// threads share a unit's partials where items have many, each taking every
+// merge_split-th, kMergeUnroll at a time. Neighbouring threads have neighbouring units,
+// along the head dims where a partial's O is row-major (kRowMajor), along the rows where
+// it is column-major (the wide form's), so that they read neighbouring addresses. (With a
+// unit's sharers side by side, one user's 4096 keys took 20 us for 15 at 32 rows, 42 for
+// 26 at 256.)
 template <bool kRowMajor>
 __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const TreeParams p) {
   constexpr int kMergeCols = merge_cols(kRowMajor);
@@ -50,11 +52,11 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
     if (w0 == w1) return;  // one range: written out there
     first_slot = u == w0 * per ? 0 : 1;  // later ranges hold the item in their first slot
   }
-  const int share = tid % split;
+  const int share = tid >> (31 - __clz(per_block));  // (a power of two)
   const int stride = kRowMajor ? p.slot_rows : kMaxRows;  // rows of a partial
   const int64_t floats = slot_floats(stride);
   for (int block = blockIdx.y; block * per_block < units; block += gridDim.y) {
-    const int unit = block * per_block + tid / split;
+    const int unit = block * per_block + (tid & (per_block - 1));
     const bool mine = unit < units;
     const int prow = kRowMajor ? unit / kVecs : unit % rows;
     const int col = (kRowMajor ? unit % kVecs : unit / rows) * kMergeCols;
@@ -119,17 +121,17 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
       __syncthreads();
       if (share == 0) {
         float top = M;
-        for (int k = 1; k < split; ++k) top = fmaxf(top, s_part[tid + k][kMergeCols]);
+        for (int k = 1; k < split; ++k) top = fmaxf(top, s_part[tid + k * per_block][kMergeCols]);
         L = 0.f;
 #pragma unroll
         for (int e = 0; e < kMergeCols; ++e) acc[e] = 0.f;
         for (int k = 0; k < split; ++k) {
-          const float l = s_part[tid + k][kMergeCols + 1];
+          const float l = s_part[tid + k * per_block][kMergeCols + 1];
           if (l == 0.f) continue;
-          const float a = ex2(s_part[tid + k][kMergeCols] - top);
+          const float a = ex2(s_part[tid + k * per_block][kMergeCols] - top);
           L = fmaf(l, a, L);
 #pragma unroll
-          for (int e = 0; e < kMergeCols; ++e) acc[e] = fmaf(s_part[tid + k][e], a, acc[e]);
+          for (int e = 0; e < kMergeCols; ++e) acc[e] = fmaf(s_part[tid + k * per_block][e], a, acc[e]);
         }
         M = top;
       }

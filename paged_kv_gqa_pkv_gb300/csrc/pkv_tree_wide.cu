@@ -6,8 +6,11 @@
 // over S in tensor memory, O += P V. A key tile is taken in two halves with an S each
 // (kHalfKeys), so that a warpgroup's softmax of one half runs while the tensor cores
 // have the other half's products: with one S per row tile, product, softmax and product
-// took turns (256 rows, 8 x 32768 keys: 251 -> 215 us, 949 TFLOP/s). Bound by the softmax
-// warps' issue there, by segment ends on short contexts (32 x ~2560 keys: 116 us).
+// took turns (256 rows, 8 x 32768 keys: 251 -> 215 us). There a CTA has a 256 x 128 tile
+// every 2.0 us, 66 % of the matrix peak with the rows past the trees counted; what bounds
+// it is the chain of a half tile (product, softmax, product, each waiting for the one
+// before). On short contexts the ends of segments weigh too: 32 x ~2560 keys take 97 us, of
+// which the merge of the cut items' partials, 30 MB from L2, is 13.
 #include "pkv_tree.cuh"
 
 namespace pkv {
