@@ -1,7 +1,6 @@
 """The operators for drafted tokens and for pages on the GPU, against the
 float64 oracle: tree attention, verification, the commit of an accepted path,
-page updates and pool compaction, and a run of them as a serving step uses
-them.
+page updates and pool compaction.
 
 Tolerances. Attention: those of the other attention tests (max-abs 2e-2,
 mean-abs 2e-3, LSE 1e-3): P and the output are each rounded to bf16 (2^-8 of
