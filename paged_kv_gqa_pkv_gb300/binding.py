@@ -23,7 +23,6 @@ Functions keep the names of the C entry points: ``pkv_append``,
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -477,33 +476,38 @@ def _tensor(name: str, t, dtype: torch.dtype, shape, dev: int) -> int:
                      f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _device_of(name: str, t, dtype: torch.dtype, ndim: int) -> int:
-    """The device that a call runs on: that of its first tensor."""
-    _need(t, name, dtype, ndim)
-    return t.get_device()
-
-
 def _cache(k_pool, v_pool, page_table, page_size: int):
     """Device, descriptor and addresses of a call's cache."""
-    dev = _device_of("k_pool", k_pool, torch.bfloat16, 3)
-    v = _tensor("v_pool", v_pool, torch.bfloat16, k_pool.shape, dev)
+    _need(k_pool, "k_pool", torch.bfloat16, 3)
+    dev, shape = k_pool.get_device(), k_pool.shape
+    v = _tensor("v_pool", v_pool, torch.bfloat16, shape, dev)
     _need(page_table, "page_table", torch.int32, 2)
-    table = _tensor("page_table", page_table, torch.int32, page_table.shape, dev)
-    return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, table
+    if page_table.get_device() != dev:
+        raise ValueError(f"page_table: expected a tensor on cuda:{dev}, got {page_table.device}")
+    return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, page_table.data_ptr()
 
 
-def _result(name: str, t, dtype: torch.dtype, shape, dev: int, like: torch.Tensor):
+def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A buffer of a call on `stream` (None: the current one), in that stream's
+    memory, so that nothing of another stream can reuse it meanwhile."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _result(name: str, t, dtype: torch.dtype, shape, dev: int, like: torch.Tensor, stream):
     """The caller's output tensor, or a new one, and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _empty(shape, dtype, like, stream)
         return t, t.data_ptr()
     return t, _tensor(name, t, dtype, shape, dev)
 
 
-def _scratch(workspace, nbytes: int, dev: int, like: torch.Tensor) -> torch.Tensor:
+def _scratch(workspace, nbytes: int, dev: int, like: torch.Tensor, stream) -> torch.Tensor:
     """The caller's workspace, or one of the size the call needs."""
     if workspace is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=like.device)
+        return _empty(max(int(nbytes), 256), torch.uint8, like, stream)
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
             not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
@@ -517,18 +521,6 @@ def _dev_err(t, dev: int) -> Optional[int]:
 # The handle of the current stream without the stream object around it (a few
 # microseconds less per call), where this PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _on_its_stream(call):
-    """With ``stream=`` given, makes it the current one for the call, so that
-    outputs and workspaces allocated here belong to the stream that uses them."""
-    @functools.wraps(call)
-    def run(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, stream=stream, **kw)
-    return run
 
 
 def _run(name: str, dev: int, stream, fn, *args) -> None:
@@ -560,7 +552,6 @@ def pkv_tree_workspace_size(k_pool, page_table, page_size: int, batch: int, n_no
     return int(n)
 
 
-@_on_its_stream
 def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_idx, ctx_lens,
                        page_size: int, scale: float, out=None, lse=None, workspace=None,
                        dev_err=None, stream=None):
@@ -580,12 +571,12 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N, float(scale))
-    out, out_p = _result("out", out, torch.bfloat16, q.shape, dev, q)
-    lse, lse_p = _result("lse", lse, torch.float32, (B, N, hq), dev, q)
+    out, out_p = _result("out", out, torch.bfloat16, q.shape, dev, q, stream)
+    lse, lse_p = _result("lse", lse, torch.float32, (B, N, hq), dev, q, stream)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_tree_workspace_size(desc_p, B, N, hq), dev, q)
+                         lib.pkv_tree_workspace_size(desc_p, B, N, hq), dev, q, stream)
     _run("pkv_tree_attention", dev, stream, lib.pkv_tree_attention, desc_p, k, v, table, *args,
          out_p, lse_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
     return out, lse
@@ -594,7 +585,6 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
 _PROBS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-@_on_its_stream
 def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_sample,
                     draft_probs=None, path=None, tokens=None, n_accepted=None, dev_err=None,
                     stream=None):
@@ -606,7 +596,8 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
     kind = target_probs.dtype if isinstance(target_probs, torch.Tensor) else None
     if kind not in _PROBS_TYPES:
         raise ValueError("target_probs must be an fp32 or bf16 tensor")
-    dev = _device_of("target_probs", target_probs, kind, 3)
+    _need(target_probs, "target_probs", kind, 3)
+    dev = target_probs.get_device()
     B, N, V = target_probs.shape
     i32, nodes, rows = torch.int32, (B, N), (B,)
     args = (target_probs.data_ptr(),
@@ -617,15 +608,14 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("u_accept", u_accept, torch.float32, nodes, dev),
             _tensor("u_sample", u_sample, torch.float32, rows, dev), B, N)
-    path, path_p = _result("path", path, i32, nodes, dev, target_probs)
-    tokens, tokens_p = _result("tokens", tokens, i32, nodes, dev, target_probs)
-    n_accepted, n_p = _result("n_accepted", n_accepted, i32, rows, dev, target_probs)
+    path, path_p = _result("path", path, i32, nodes, dev, target_probs, stream)
+    tokens, tokens_p = _result("tokens", tokens, i32, nodes, dev, target_probs, stream)
+    n_accepted, n_p = _result("n_accepted", n_accepted, i32, rows, dev, target_probs, stream)
     _run("pkv_verify_tree", dev, stream, load_library().pkv_verify_tree, *args, path_p, tokens_p,
          n_p, _dev_err(dev_err, dev))
     return path, tokens, n_accepted
 
 
-@_on_its_stream
 def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx_lens,
                     page_size: int, new_lens=None, dev_err=None, stream=None):
     """Moves the K/V rows of the accepted nodes path[b, :n_accepted[b]] from
@@ -640,7 +630,7 @@ def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx
             _tensor("n_accepted", n_accepted, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N)
-    new_lens, new_p = _result("new_lens", new_lens, i32, rows, dev, path)
+    new_lens, new_p = _result("new_lens", new_lens, i32, rows, dev, path, stream)
     _run("pkv_commit_path", dev, stream, load_library().pkv_commit_path, ctypes.byref(desc), k, v,
          table, *args, new_p, _dev_err(dev_err, dev))
     return new_lens
@@ -654,7 +644,6 @@ def pkv_update_workspace_size(k_pool, page_table, page_size: int, n: int) -> int
     return int(size)
 
 
-@_on_its_stream
 def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots, keep_lens,
                      new_lens, page_size: int, workspace=None, dev_err=None,
                      stream=None) -> None:
@@ -674,7 +663,7 @@ def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots
     lib = load_library()
     desc_p = ctypes.byref(desc)
     workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_update_workspace_size(desc_p, n), dev, k_pool)
+                         lib.pkv_update_workspace_size(desc_p, n), dev, k_pool, stream)
     _run("pkv_update_pages", dev, stream, lib.pkv_update_pages, desc_p, k, v, table, *args,
          workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
 
@@ -687,18 +676,18 @@ def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
     return int(size)
 
 
-@_on_its_stream
 def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num_live=None,
                       workspace=None, dev_err=None, stream=None):
     """Moves the live pages to the low end of the pool (K/V rows, table
     entries and counts), in place. Returns num_live [1], how many there are."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     refs = _tensor("page_refs", page_refs, torch.int32, (desc.num_pages,), dev)
-    num_live, live_p = _result("num_live", num_live, torch.int32, (1,), dev, page_refs)
+    num_live, live_p = _result("num_live", num_live, torch.int32, (1,), dev, page_refs,
+                               stream)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_compact_workspace_size(desc_p), dev, k_pool)
+                         lib.pkv_compact_workspace_size(desc_p), dev, k_pool, stream)
     _run("pkv_compact_pages", dev, stream, lib.pkv_compact_pages, desc_p, k, v, table, refs,
          live_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
     return num_live
