@@ -276,3 +276,119 @@ def test_refused_workspaces_and_outputs(how):
         binding.pkv_update_pages(m.k, m.v, m.table, refs, one, one, m.i32([30]), m.i32([40]), 16,
                                  workspace=ws)
     m.equal()
+
+
+def test_calls_without_buffers_are_captured():
+    """Results and workspaces allocated inside the capture; two graphs replayed in
+    turn, each with inputs changed in place between replays."""
+    to = lambda a: (a if isinstance(a, torch.Tensor) else torch.from_numpy(a)).cuda()  # noqa: E731
+    cases = [S.tree_case(31, [900, 40], [12, 7], 12, hq=8, hkv=2),
+             S.tree_case(32, [64, 64, 500], [3, 5, 5], 5, hq=4, hkv=2, ps=32)]
+    ver = S.verify_case(33, 3, 9, 700)
+    graphs = []
+    for c in cases:
+        a = [to(x) for x in (c.k, c.v, c.table, c.q, c.parents, c.lens, c.slots, c.ctx)]
+        vt = [to(x) for x in (ver.target, ver.tokens, ver.parents, ver.lens, ver.u, ver.us)]
+        binding.pkv_tree_attention(*a, c.ps, c.scale)
+        binding.pkv_verify_tree(*vt)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = binding.pkv_tree_attention(*a, c.ps, c.scale) + binding.pkv_verify_tree(*vt)
+        graphs.append((g, a, vt, r, c))
+    rng = np.random.default_rng(34)
+    for _ in range(3):
+        for g, a, vt, r, c in graphs:
+            c.q = torch.from_numpy(rng.standard_normal(tuple(c.q.shape)).astype(np.float32)).bfloat16()
+            ver.u = torch.from_numpy(rng.random(tuple(ver.u.shape)).astype(np.float32))
+            a[3].copy_(c.q)
+            vt[4].copy_(ver.u)
+            g.replay()
+            torch.cuda.synchronize()
+            ro, rl, err, _ = S.tree_oracle(c)
+            assert err == 0
+            assert_attention_close(r[0].cpu(), r[1].cpu(), ro, rl)
+            f = lambda t: t.double().numpy()  # noqa: E731
+            want = spec.verify_tree(f(ver.target), None, ver.tokens.numpy(), ver.parents, ver.lens,
+                                    f(ver.u), f(ver.us))
+            for x, w in zip(r[2:], want):
+                assert np.array_equal(x.cpu().numpy(), w)
+
+
+def test_a_pool_past_32_bits():
+    """4.3 million pages of 16 tokens (8.8e9 elements per pool, more pages than the
+    smallest chunks of the page plans): fork, commit, attention and compaction."""
+    ps, pages, slots, cols = 16, 4_300_000, 6, 48
+    rows = pages * ps
+    k = torch.empty((rows, 1, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    mark = torch.arange(rows, dtype=torch.int32, device="cuda")[:, None, None]
+    k.view(torch.int32).copy_(mark)          # a row's number, 64 times
+    v.view(torch.int32).copy_(-mark)
+    del mark
+    rng = np.random.default_rng(41)
+    table = np.full((slots, cols), -1, dtype=np.int32)
+    lens = {1: 500, 2: 333, 3: 700}
+    for s, n in lens.items():
+        m = -(-n // ps)
+        table[s, :m] = rng.choice(np.arange(pages - 5000 * s, pages - 5000 * (s - 1)), m, False)
+    refs = np.zeros(pages, dtype=np.int32)
+    refs[0] = 1
+    refs[1:3_000_000:2] = 1                  # holds of the caller's own
+    for e in table[table > 0]:
+        refs[e] += 1
+    i32 = lambda x: torch.from_numpy(np.array(x, dtype=np.int32)).cuda()  # noqa: E731
+    tab, cnt, err = i32(table), i32(refs), i32([0])
+    none = np.zeros((rows, 0), dtype=np.uint8)   # the oracle's pools: nothing in them
+    row = lambda t, s, n: (t[s, np.arange(n) // ps].astype(np.int64) * ps +  # noqa: E731
+                           np.arange(n) % ps)
+    held = lambda r: k.view(torch.int32)[torch.from_numpy(r).cuda(), 0, 0].cpu().numpy()  # noqa: E731
+    heldv = lambda r: -v.view(torch.int32)[torch.from_numpy(r).cuda(), 0, 63].cpu().numpy()  # noqa: E731
+
+    # slot 4 branches off slot 1 mid-page, slot 3 gets room
+    call = ([4, 3], [1, 3], [437, 700], [460, 720])
+    binding.pkv_update_pages(k, v, tab, cnt, *map(i32, call), ps, dev_err=err)
+    _, _, t2, r2, e2 = spec.update_pages(none, none, table, refs, *call, ps)
+    assert e2 == 0 and int(err.item()) == 0
+    assert np.array_equal(tab.cpu().numpy(), t2) and np.array_equal(cnt.cpu().numpy(), r2)
+    for get in (held, heldv):
+        assert np.array_equal(get(row(t2, 4, 437)), row(table, 1, 437))
+
+    # an accepted path of slot 3's last positions
+    before = held(row(t2, 3, 720))
+    new = binding.pkv_commit_path(k, v, tab, i32([[0, 3, 4, 7, -1, -1, -1, -1]]), i32([4]), i32([3]),
+                                  i32([700]), ps, dev_err=err)   # nodes 0 .. 7 of 8
+    assert new.item() == 704
+    assert np.array_equal(held(row(t2, 3, 704))[700:], before[[700, 703, 704, 707]])
+
+    # attention of a tree behind slot 2, whose rows get numbers that are finite
+    update = ([2], [2], [333], [339])
+    binding.pkv_update_pages(k, v, tab, cnt, *map(i32, update), ps, dev_err=err)
+    _, _, t3, r3, _ = spec.update_pages(none, none, t2, r2, *update, ps)
+    at = row(t3, 2, 339)
+    kk, vv = (torch.from_numpy(rng.standard_normal((339, 1, 128)).astype(np.float32)).bfloat16()
+              for _ in range(2))
+    k[torch.from_numpy(at).cuda()], v[torch.from_numpy(at).cuda()] = kk.cuda(), vv.cuda()
+    q = torch.from_numpy(rng.standard_normal((1, 6, 4, 128)).astype(np.float32)).bfloat16()
+    par = np.array([[-1, 0, 0, 1, 3, 2]], dtype=np.int32)
+    out, lse = binding.pkv_tree_attention(k, v, tab, q.cuda(), i32(par), i32([6]), i32([2]),
+                                          i32([333]), ps, 0.09, dev_err=err)
+    pad = lambda x: bf16_bits(torch.cat([x, torch.zeros(13, 1, 128).bfloat16()]))  # noqa: E731
+    small = np.arange(22, dtype=np.int32)[None].repeat(2, 0)
+    ro, rl, e, _ = spec.tree_attention(bf16_bits(q), pad(kk), pad(vv), small, par, [6], [1], [333],
+                                       ps, 0.09)
+    assert e == 0 and int(err.item()) == 0
+    assert_attention_close(out.cpu(), lse.cpu(), ro, rl)
+
+    # the caller's holds end, slot 2 leaves, the pool is packed
+    cnt[1:3_000_000:2] -= 1
+    r3[1:3_000_000:2] -= 1
+    gone = ([2], [0], [0], [0])
+    binding.pkv_update_pages(k, v, tab, cnt, *map(i32, gone), ps, dev_err=err)
+    _, _, t4, r4, _ = spec.update_pages(none, none, t3, r3, *gone, ps)
+    was = {s: held(row(t4, s, n)) for s, n in ((1, 500), (3, 704), (4, 437))}
+    n = binding.pkv_compact_pages(k, v, tab, cnt, ps, dev_err=err)
+    _, _, t5, r5, live, e5 = spec.compact_pages(none, none, t4, r4, ps)
+    assert e5 == 0 and int(err.item()) == 0 and n.item() == live
+    assert np.array_equal(tab.cpu().numpy(), t5) and np.array_equal(cnt.cpu().numpy(), r5)
+    for s, w in was.items():
+        assert np.array_equal(held(row(t5, s, len(w))), w)
