@@ -443,19 +443,21 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const Commi
   const int slot = p.batch_idx[b];
   const int ctx = p.ctx_lens[b];
   const int n = p.n_accepted[b];
+  // (read beside the lengths, whatever they turn out to be)
+  const int i = threadIdx.x;
+  const int32_t* path = p.path + static_cast<int64_t>(b) * p.n_nodes;
+  const int a = i < p.n_nodes ? path[i] : 0;
+  const int before = i > 0 && i < p.n_nodes ? path[i - 1] : -1;
   int err = 0;
   if (slot < 0 || slot >= p.max_batch) err = PKV_DEV_ERR_BAD_SLOT;
   else if (slot > 0 && (n < 0 || n > p.n_nodes)) err = PKV_DEV_ERR_BAD_TREE;
   else if (slot > 0 && ctx < 0) err = PKV_DEV_ERR_BAD_POS;
   const bool live = slot > 0 && !err && n > 0;
   int mine = 0;
-  const int i = threadIdx.x;
   if (live && i < n) {
-    const int32_t* path = p.path + static_cast<int64_t>(b) * p.n_nodes;
-    const int a = path[i];
     const int64_t from = static_cast<int64_t>(ctx) + a;
     const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.page_size;
-    if (a < 0 || a >= p.n_nodes || (i > 0 && path[i - 1] >= a)) {
+    if (a < 0 || a >= p.n_nodes || before >= a) {
       mine = PKV_DEV_ERR_BAD_TREE;
     } else if (from >= cap) {
       mine = PKV_DEV_ERR_BAD_POS;

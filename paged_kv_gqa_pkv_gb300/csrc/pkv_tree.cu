@@ -17,9 +17,9 @@ constexpr int merge_cols(bool row_major) { return row_major ? 8 : 16; }
 }  // namespace
 
 // Joins the partials of items cut by range borders, and writes the rows of
-// items that attend nothing. grid (items, parts): a CTA takes every parts-th
-// block of its item's units; a unit is a row and merge_cols head dims. merge_split
-// threads share a unit's partials where items have many, each taking every
+// items that attend nothing. grid (items of a row, parts, rows): a CTA takes every
+// parts-th block of its item's units; a unit is a row and merge_cols head dims.
+// merge_split threads share a unit's partials where items have many, each taking every
 // merge_split-th, kMergeUnroll at a time. Neighbouring threads have neighbouring units,
 // along the head dims where a partial's O is row-major (kRowMajor), along the rows where
 // it is column-major (the wide form's), so that they read neighbouring addresses. (With a
@@ -31,8 +31,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
   __shared__ float s_part[kMergeThreads][kMergeCols + 2];
   pdl_wait_primary();
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / p.items_per_row, item = blockIdx.x % p.items_per_row;
-  const int kvh = item / p.row_blocks, rb = item % p.row_blocks;
+  const int b = blockIdx.z, item = blockIdx.x;
+  const int kvh = p.row_blocks == 1 ? item : item / p.row_blocks;
+  const int rb = item - kvh * p.row_blocks;
   const int before = p.prefix[b], tiles = p.prefix[b + 1] - before;
   const int split = p.merge_split;
   const int per_block = kMergeThreads / split;
@@ -139,8 +140,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
     if (mine && share == 0) {
       const bool has = L != 0.f;
       const float inv = has ? 1.f / L : 0.f;
-      const int64_t orow = (static_cast<int64_t>(b) * p.n_nodes + r / p.group) * p.num_q_heads +
-                           kvh * p.group + r % p.group;
+      const int64_t orow = (static_cast<int64_t>(b) * p.n_nodes + (r >> p.group_shift)) *
+                               p.num_q_heads +
+                           kvh * p.group + (r & (p.group - 1));
 #pragma unroll
       for (int e = 0; e < kMergeCols; e += 8) {
         uint4 w;
@@ -234,8 +236,8 @@ cudaError_t launch_merge(const TreeParams& p, int sms, cudaStream_t stream) {
   const int blocks = (p.slot_rows * (kHeadDim / merge_cols(!wide)) + per_block - 1) / per_block;
   const int want = (16 * sms + items - 1) / items;
   return launch_kernel(wide ? tree_merge_kernel<false> : tree_merge_kernel<true>,
-                       dim3(items, blocks < want ? blocks : want), dim3(kMergeThreads), 0, stream,
-                       /*programmatic=*/true, p);
+                       dim3(p.items_per_row, blocks < want ? blocks : want, p.batch),
+                       dim3(kMergeThreads), 0, stream, /*programmatic=*/true, p);
 }
 
 }  // namespace
