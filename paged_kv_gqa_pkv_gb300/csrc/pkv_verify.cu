@@ -30,7 +30,7 @@
 // are exact in fp32 whatever their type.
 //
 // Measured: one chain of 6 nodes, 32000 tokens, without a draft 6.3 us; 12 trees of 16
-// nodes, 50257 in fp32 14.2 us; 64 trees, 151936 in bf16 30 us, of which the longest row
+// nodes, 50257 in fp32 14.2 us; 64 trees, 151936 in bf16 29 us, of which the longest row
 // spends three dependent passes (8, then ~5 us each beside the other rows') and a draw.
 #include <atomic>
 
@@ -351,26 +351,6 @@ struct Walk {
     g1 = static_cast<int>((w + 1) * per < total ? (w + 1) * per : total);
   }
 
-  // the residual's terms of one granule
-  __device__ __forceinline__ void terms(float ah, float al, int g, int off,
-                                        const float (&x)[Elem<T>::kPer],
-                                        const float (&y)[Elem<T>::kPer],
-                                        Pair (&t)[Elem<T>::kPer]) const {
-#pragma unroll
-    for (int e = 0; e < Elem<T>::kPer; ++e) {
-      if constexpr (kDraft) t[e] = residual(clean(x[e]), clean(y[e]), ah, al);
-      else t[e] = {clean(x[e]), 0.f};
-    }
-    if constexpr (!kDraft) {
-      for (int k = 0; k < s.n_refused; ++k) {
-        const int at = s.refused[k] + off - g * Elem<T>::kPer;
-#pragma unroll
-        for (int e = 0; e < Elem<T>::kPer; ++e)
-          if (at == e) t[e].hi = 0.f;
-      }
-    }
-  }
-
   // Sums of p and q over the tokens with p > a q, a granule at a time.
   struct Sums {
     static constexpr int E = Elem<T>::kPer;
@@ -532,20 +512,19 @@ struct Walk {
 
   // The ordered draw, by all threads of the CTA that holds the token, over the
   // granules of the warp that held it in the pass: each thread sums a few of them,
-  // the running sums pick the thread, and that one picks the token. (One warp
-  // alone took 10 us for its 300 granules.) Returns the token in the thread that
-  // picked it, -1 in the others.
+  // the running sums pick the thread, and its warp looks at that thread's values, one
+  // per lane. (One warp alone took 10 us for its 300 granules.) Returns the token in
+  // one thread, -1 in the others.
   __device__ int draw() {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
-    const float ah = s.a.hi, al = s.a.lo;
     const Pair t = s.draw_at;
     int g0, g1;
     range_of(pv, s.draw_warp, g0, g1);
     constexpr int E = Elem<T>::kPer;
     const int per = (g1 - g0 + kWarps * 32 - 1) / (kWarps * 32);
     const int a0 = min(g0 + (32 * warp + lane) * per, g1), a1 = min(a0 + per, g1);
-    const bool with_q = kDraft && ah != 0.f;
+    const bool with_q = kDraft && s.a.hi != 0.f;
     // a granule that lies inside the row comes as it was loaded, in xw and yw
     auto cleaned = [&](int g, const uint4& xw, const uint4& yw, float (&x)[E], float (&y)[E]) {
       Elem<T>::unpack(xw, x);
@@ -598,28 +577,43 @@ struct Walk {
     const uint32_t fs = __ballot_sync(0xffffffffu, f >= 0), es = __ballot_sync(0xffffffffu, e >= 0);
     const int w = fs != 0u ? __ffs(fs) - 1 : 31 - __clz(es | 1u);
     const int l = __shfl_sync(0xffffffffu, fs != 0u ? f : e, w);
-    const Pair before = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    // that thread's values again, one per lane of its warp
     int at = -1;
-    if (warp == w && lane == l) {
-      // the same sums, value by value: the first past t, or the last with mass
-      // where rounding leaves none
-      if (lane > 0) add(front, before);
-      bool found = false;
-      for (int g = a0; g < a1 && !found; ++g) {
-        float x[E], y[E];
-        Pair tm[E];
-        cleaned(g, raw_p(g), raw_q(g), x, y);
-        terms(ah, al, g, pv.off, x, y, tm);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const bool in = with_q ? fmaf(-al, y[e], fmaf(-ah, y[e], x[e])) > 0.f : tm[e].hi > 0.f;
-          if (in && !found) {
-            at = g * E + e - pv.off;
-            add(front, tm[e]);
-            found = above(front, t);
+    if (warp == w) {
+      const Pair up = {__shfl_up_sync(0xffffffffu, incl.hi, 1),
+                       __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      if (lane > 0) add(front, up);
+      Pair at_front = shfl(front, l);
+      const int v0 = max(__shfl_sync(0xffffffffu, a0, l) * E, pv.off);
+      const int v1 = min(__shfl_sync(0xffffffffu, a1, l) * E, pv.end);
+      for (int v = v0; v < v1; v += 32) {
+        const int i = v + lane;
+        Pair term = {0.f, 0.f};
+        bool in = false;
+        if (i < v1) {
+          const float x = clean(Elem<T>::get(pv.base + i));
+          if constexpr (kDraft) {
+            const float y = with_q ? clean(Elem<T>::get(qv.base + i)) : 0.f;
+            term = residual(x, y, s.a.hi, s.a.lo);
+            // (the pass's own test, so that a residual with any token has one here)
+            in = fmaf(-s.a.lo, y, fmaf(-s.a.hi, y, x)) > 0.f;
+          } else {
+            in = x > 0.f;
+            for (int k = 0; k < s.n_refused; ++k) in = in && s.refused[k] + pv.off != i;
+            if (in) term.hi = x;
           }
         }
+        const Pair run = scan<32>(term, lane);
+        Pair upto = at_front;
+        add(upto, run);
+        const uint32_t over = __ballot_sync(0xffffffffu, in && above(upto, t));
+        const uint32_t any = __ballot_sync(0xffffffffu, in);
+        // the first past t, or the last with mass where rounding leaves none
+        if (any != 0u) at = v - pv.off + (over != 0u ? __ffs(over) - 1 : 31 - __clz(any));
+        if (over != 0u) break;
+        add(at_front, shfl(run, 31));
       }
+      if (lane != 0) at = -1;
     }
     return at;
   }
