@@ -487,31 +487,18 @@ def _cache(k_pool, v_pool, page_table, page_size: int):
     return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, page_table.data_ptr()
 
 
-def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """A buffer of a call on `stream` (None: the current one), in that stream's
-    memory, so that nothing of another stream can reuse it meanwhile."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
 def _result(name: str, t, dtype: torch.dtype, shape, dev: int, like: torch.Tensor, stream):
-    """The caller's output tensor, or a new one, and its address."""
-    if t is None:
-        t = _empty(shape, dtype, like, stream)
-        return t, t.data_ptr()
-    return t, _tensor(name, t, dtype, shape, dev)
-
-
-def _scratch(workspace, nbytes: int, dev: int, like: torch.Tensor, stream) -> torch.Tensor:
-    """The caller's workspace, or one of the size the call needs."""
-    if workspace is None:
-        return _empty(max(int(nbytes), 256), torch.uint8, like, stream)
-    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
-            not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
-    return workspace
+    """The caller's output tensor, or a new one, and its address. A new one is in
+    the memory of the stream that writes it, so that nothing else can reuse it
+    meanwhile."""
+    if t is not None:
+        return t, _tensor(name, t, dtype, shape, dev)
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
 
 
 def _dev_err(t, dev: int) -> Optional[int]:
@@ -521,6 +508,21 @@ def _dev_err(t, dev: int) -> Optional[int]:
 # The handle of the current stream without the stream object around it (a few
 # microseconds less per call), where this PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# PyTorch's caching allocator without a tensor around the memory: a workspace
+# that lives for one call costs 2.5 us this way and 5.7 as a tensor.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _handle(name: str, dev: int, stream) -> int:
+    """The handle of `stream`, or of the current stream of device `dev`."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _run(name: str, dev: int, stream, fn, *args) -> None:
@@ -530,15 +532,31 @@ def _run(name: str, dev: int, stream, fn, *args) -> None:
         with torch.cuda.device(dev):
             _run(name, dev, stream, fn, *args)
         return
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(dev)
+    st = fn(*args, _handle(name, dev, stream))
+    if st != PKV_OK:
+        raise PkvError(name, st)
+
+
+def _run_with(workspace, size, name: str, dev: int, stream, err, fn, *args) -> None:
+    """_run of fn(*args, workspace, its bytes, err, stream) with the caller's
+    workspace, or one of size() bytes that goes back to the stream's memory."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _run_with(workspace, size, name, dev, stream, err, fn, *args)
+        return
+    handle = _handle(name, dev, stream)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
+                not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+        st = fn(*args, workspace.data_ptr(), workspace.nbytes, err, handle)
     else:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    st = fn(*args, handle)
+        nbytes = max(size(), 256)
+        ptr = _raw_alloc(nbytes, handle)
+        try:
+            st = fn(*args, ptr, nbytes, err, handle)
+        finally:
+            _raw_delete(ptr)
     if st != PKV_OK:
         raise PkvError(name, st)
 
@@ -575,10 +593,9 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
     lse, lse_p = _result("lse", lse, torch.float32, (B, N, hq), dev, q, stream)
     lib = load_library()
     desc_p = ctypes.byref(desc)
-    workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_tree_workspace_size(desc_p, B, N, hq), dev, q, stream)
-    _run("pkv_tree_attention", dev, stream, lib.pkv_tree_attention, desc_p, k, v, table, *args,
-         out_p, lse_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
+    _run_with(workspace, lambda: lib.pkv_tree_workspace_size(desc_p, B, N, hq),
+              "pkv_tree_attention", dev, stream, _dev_err(dev_err, dev), lib.pkv_tree_attention,
+              desc_p, k, v, table, *args, out_p, lse_p)
     return out, lse
 
 
@@ -662,10 +679,8 @@ def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots
             _tensor("new_lens", new_lens, i32, rows, dev), n)
     lib = load_library()
     desc_p = ctypes.byref(desc)
-    workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_update_workspace_size(desc_p, n), dev, k_pool, stream)
-    _run("pkv_update_pages", dev, stream, lib.pkv_update_pages, desc_p, k, v, table, *args,
-         workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
+    _run_with(workspace, lambda: lib.pkv_update_workspace_size(desc_p, n), "pkv_update_pages", dev,
+              stream, _dev_err(dev_err, dev), lib.pkv_update_pages, desc_p, k, v, table, *args)
 
 
 def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
@@ -686,8 +701,7 @@ def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num
                                stream)
     lib = load_library()
     desc_p = ctypes.byref(desc)
-    workspace = _scratch(workspace, 0 if workspace is not None else
-                         lib.pkv_compact_workspace_size(desc_p), dev, k_pool, stream)
-    _run("pkv_compact_pages", dev, stream, lib.pkv_compact_pages, desc_p, k, v, table, refs,
-         live_p, workspace.data_ptr(), workspace.nbytes, _dev_err(dev_err, dev))
+    _run_with(workspace, lambda: lib.pkv_compact_workspace_size(desc_p), "pkv_compact_pages", dev,
+              stream, _dev_err(dev_err, dev), lib.pkv_compact_pages, desc_p, k, v, table, refs,
+              live_p)
     return num_live
