@@ -487,17 +487,18 @@ def _cache(k_pool, v_pool, page_table, page_size: int):
     return dev, cache_desc(k_pool, page_table, page_size), k_pool.data_ptr(), v, page_table.data_ptr()
 
 
-def _result(name: str, t, dtype: torch.dtype, shape, dev: int, like: torch.Tensor, stream):
-    """The caller's output tensor, or a new one, and its address. A new one is in
-    the memory of the stream that writes it, so that nothing else can reuse it
+def _result(name: str, t, like: torch.Tensor, dev: int, stream, shape=None, dtype=None):
+    """The caller's output tensor, or a new one, and its address: of the type and
+    shape of the (checked) input `like`, or of those given. A new one is in the
+    memory of the stream that writes it, so that nothing else can reuse it
     meanwhile."""
     if t is not None:
-        return t, _tensor(name, t, dtype, shape, dev)
-    if stream is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    else:
+        return t, _tensor(name, t, dtype or like.dtype, like.shape if shape is None else shape, dev)
+    if stream is not None:
         with torch.cuda.stream(stream):
-            t = torch.empty(shape, dtype=dtype, device=like.device)
+            return _result(name, None, like, dev, None, shape, dtype)
+    t = torch.empty_like(like) if shape is None else \
+        torch.empty(shape, dtype=dtype, device=like.device)
     return t, t.data_ptr()
 
 
@@ -589,8 +590,8 @@ def pkv_tree_attention(k_pool, v_pool, page_table, q, parents, tree_lens, batch_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N, float(scale))
-    out, out_p = _result("out", out, torch.bfloat16, q.shape, dev, q, stream)
-    lse, lse_p = _result("lse", lse, torch.float32, (B, N, hq), dev, q, stream)
+    out, out_p = _result("out", out, q, dev, stream)
+    lse, lse_p = _result("lse", lse, q, dev, stream, (B, N, hq), torch.float32)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     _run_with(workspace, lambda: lib.pkv_tree_workspace_size(desc_p, B, N, hq),
@@ -625,9 +626,9 @@ def pkv_verify_tree(target_probs, draft_tokens, parents, tree_lens, u_accept, u_
             _tensor("tree_lens", tree_lens, i32, rows, dev),
             _tensor("u_accept", u_accept, torch.float32, nodes, dev),
             _tensor("u_sample", u_sample, torch.float32, rows, dev), B, N)
-    path, path_p = _result("path", path, i32, nodes, dev, target_probs, stream)
-    tokens, tokens_p = _result("tokens", tokens, i32, nodes, dev, target_probs, stream)
-    n_accepted, n_p = _result("n_accepted", n_accepted, i32, rows, dev, target_probs, stream)
+    path, path_p = _result("path", path, parents, dev, stream)
+    tokens, tokens_p = _result("tokens", tokens, parents, dev, stream)
+    n_accepted, n_p = _result("n_accepted", n_accepted, tree_lens, dev, stream)
     _run("pkv_verify_tree", dev, stream, load_library().pkv_verify_tree, *args, path_p, tokens_p,
          n_p, _dev_err(dev_err, dev))
     return path, tokens, n_accepted
@@ -647,7 +648,7 @@ def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx
             _tensor("n_accepted", n_accepted, i32, rows, dev),
             _tensor("batch_idx", batch_idx, i32, rows, dev),
             _tensor("ctx_lens", ctx_lens, i32, rows, dev), B, N)
-    new_lens, new_p = _result("new_lens", new_lens, i32, rows, dev, path, stream)
+    new_lens, new_p = _result("new_lens", new_lens, ctx_lens, dev, stream)
     _run("pkv_commit_path", dev, stream, load_library().pkv_commit_path, ctypes.byref(desc), k, v,
          table, *args, new_p, _dev_err(dev_err, dev))
     return new_lens
@@ -697,8 +698,7 @@ def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num
     entries and counts), in place. Returns num_live [1], how many there are."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     refs = _tensor("page_refs", page_refs, torch.int32, (desc.num_pages,), dev)
-    num_live, live_p = _result("num_live", num_live, torch.int32, (1,), dev, page_refs,
-                               stream)
+    num_live, live_p = _result("num_live", num_live, page_refs, dev, stream, (1,), torch.int32)
     lib = load_library()
     desc_p = ctypes.byref(desc)
     _run_with(workspace, lambda: lib.pkv_compact_workspace_size(desc_p), "pkv_compact_pages", dev,
