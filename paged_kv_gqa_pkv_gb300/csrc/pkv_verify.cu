@@ -122,6 +122,22 @@ __device__ __forceinline__ Pair warp_sum(Pair x, int lane) {
   return x;
 }
 
+// Two sums at once: shuffles stay in program order, so that one sum's would wait for
+// the other's additions.
+template <int kLanes>
+__device__ __forceinline__ void warp_sum2(Pair& x, Pair& y, int lane) {
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+    const Pair u = shfl_xor(x, o), v = shfl_xor(y, o);
+    const bool up = lane & o;
+    Pair a = up ? u : x, b = up ? v : y;
+    add(a, up ? x : u);
+    add(b, up ? y : v);
+    x = a;
+    y = b;
+  }
+}
+
 // Inclusive running sums over the lanes, for lanes below kLanes.
 template <int kLanes>
 __device__ __forceinline__ Pair scan(Pair x, int lane) {
@@ -345,7 +361,8 @@ struct Walk {
   __device__ __forceinline__ void range_of(const RowView<T>& v, int wp, int& g0, int& g1) const {
     const int total = v.granules();
     const int warps = p.cluster * kWarps;
-    const int per = ((total + warps - 1) / warps + 31) / 32 * 32;
+    // (a division by warps, a power of two)
+    const int per = (((total + warps - 1) >> (31 - __clz(warps))) + 31) / 32 * 32;
     const int64_t w = static_cast<int64_t>(rank) * kWarps + wp;
     g0 = static_cast<int>(w * per < total ? w * per : total);
     g1 = static_cast<int>((w + 1) * per < total ? (w + 1) * per : total);
@@ -440,9 +457,13 @@ struct Walk {
       slot = slot + 1 < kDepth ? slot + 1 : 0;
     }
     cp_async_wait<0>();
-    const Pair sp = warp_sum(acc.ps.total(), lane);
-    Pair sq = {0.f, 0.f};
-    if (with_q) sq = warp_sum(acc.qs.total(), lane);
+    Pair sp = acc.ps.total(), sq = {0.f, 0.f};
+    if (with_q) {
+      sq = acc.qs.total();
+      warp_sum2<32>(sp, sq, lane);
+    } else {
+      sp = warp_sum(sp, lane);
+    }
     if (lane == 0) {
       s.warp_p[warp] = sp;
       s.warp_q[warp] = sq;
@@ -462,8 +483,9 @@ struct Walk {
     sum_part();
     __syncthreads();
     // (every kWarps lanes add the same numbers in the same order)
-    const Pair mine = minus(warp_sum<kWarps>(s.warp_p[lane % kWarps], lane),
-                            times(r.a, warp_sum<kWarps>(s.warp_q[lane % kWarps], lane)));
+    Pair sp = s.warp_p[lane % kWarps], sq = s.warp_q[lane % kWarps];
+    warp_sum2<kWarps>(sp, sq, lane);
+    const Pair mine = minus(sp, times(r.a, sq));
     Pair* slots = s.cta_sum[passes & 1];
     if (lane < p.cluster) cluster_store(&slots[rank], lane, mine);
     // one barrier per pass: the next pass writes the other half, and the one
