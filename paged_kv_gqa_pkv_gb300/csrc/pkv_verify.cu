@@ -30,7 +30,7 @@
 // are exact in fp32 whatever their type.
 //
 // Measured: one chain of 6 nodes, 32000 tokens, without a draft 6.3 us; 12 trees of 16
-// nodes, 50257 in fp32 14.2 us; 64 trees, 151936 in bf16 29 us, of which the longest row
+// nodes, 50257 in fp32 12.7 us; 64 trees, 151936 in bf16 29 us, of which the longest row
 // spends three dependent passes (8, then ~5 us each beside the other rows') and a draw.
 #include <atomic>
 
@@ -355,10 +355,13 @@ struct Walk {
   const int lane, warp;
   uint4* ring;  // this thread's slots: [kDepth][p, q], kThreads apart
   int passes = 0;
+  int held = -1;        // node whose rows the ring holds whole, -1: none
+  bool held_q = false;  // the draft's too
   static constexpr int kThreads = kWarps * 32;
 
   // granules [g0, g1) of a row are warp wp's of this CTA
-  __device__ __forceinline__ void range_of(const RowView<T>& v, int wp, int& g0, int& g1) const {
+  // Whether a part fits the ring (the same for all warps).
+  __device__ __forceinline__ bool range_of(const RowView<T>& v, int wp, int& g0, int& g1) const {
     const int total = v.granules();
     const int warps = p.cluster * kWarps;
     // (a division by warps, a power of two)
@@ -366,6 +369,7 @@ struct Walk {
     const int64_t w = static_cast<int64_t>(rank) * kWarps + wp;
     g0 = static_cast<int>(w * per < total ? w * per : total);
     g1 = static_cast<int>((w + 1) * per < total ? (w + 1) * per : total);
+    return per <= 32 * kDepth;
   }
 
   // Sums of p and q over the tokens with p > a q, a granule at a time.
@@ -416,12 +420,15 @@ struct Walk {
   // A thread's granules come through kDepth slots of its own in shared memory, so
   // that a row's pass waits for memory about once (with four loads in flight
   // per thread a pass of few rows took 6.5 us for 76 KB per CTA, all of it latency).
-  __device__ __forceinline__ void sum_part() const {
+  __device__ __forceinline__ void sum_part() {
     const RowView<T> pv(p.target, row0 + s.node, p.vocab);
     const RowView<T> qv(kDraft ? p.draft : p.target, row0 + s.node, p.vocab);
     const bool with_q = kDraft && s.a.hi != 0.f;
     int g0, g1;
-    range_of(pv, warp, g0, g1);
+    const bool fits = range_of(pv, warp, g0, g1);
+    // a node's later passes find its rows where the first one left them (14.0 -> 12.7 us
+    // for 12 rows; reading the draw's part from there too cost registers, and 2 %)
+    const bool have = fits && held == s.node && (held_q || !with_q);
     constexpr int E = Elem<T>::kPer;
     Sums acc(s.a, with_q);
     const uint4* from_p = reinterpret_cast<const uint4*>(pv.base) + lane;
@@ -436,7 +443,8 @@ struct Walk {
       cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kDepth; ++k) fetch(g0 + 32 * k, k);
+    for (int k = 0; k < kDepth; ++k)
+      if (!have) fetch(g0 + 32 * k, k);
     int slot = 0;
     for (int g = g0; g < g1; g += 32) {
       cp_async_wait<kDepth - 1>();
@@ -457,6 +465,8 @@ struct Walk {
       slot = slot + 1 < kDepth ? slot + 1 : 0;
     }
     cp_async_wait<0>();
+    held_q = with_q || (have && held_q);
+    held = fits ? s.node : -1;
     Pair sp = acc.ps.total(), sq = {0.f, 0.f};
     if (with_q) {
       sq = acc.qs.total();
