@@ -212,6 +212,17 @@ def test_verify_shapes(shape, draft):
         check_verify(S.verify_case(200 + seed, 4, 20, 5, draft=draft, shape=shape))
 
 
+@pytest.mark.parametrize("B,V,kind", [(2, 120001, torch.float32), (2, 230003, torch.bfloat16),
+                                      (40, 60001, torch.float32), (40, 110011, torch.bfloat16)])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_rows_larger_than_shared_memory(B, V, kind, draft):
+    """Vocabularies whose parts do not fit a CTA's ring, in both CTA sizes, with
+    several refusals at one node."""
+    c = S.verify_case(V, B, 4, V, draft=draft, kind=kind, shape="star", tree=[4] * B)
+    c.u[::2] = 1.5                   # every second row refuses all of its drafts
+    check_verify(c)
+
+
 def test_verify_one_node_and_padding():
     c = S.verify_case(5, 3, 1, 100, tree=[1, 0, 1])
     got = check_verify(c)
