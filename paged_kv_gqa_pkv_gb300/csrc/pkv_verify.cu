@@ -67,9 +67,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // Unevaluated sum of two floats.
 struct Pair {
@@ -688,6 +694,10 @@ verify_tree_kernel(const VerifyParams p) {
     }
     return;
   }
+  // A CTA's shared memory may be written by the others once it is known to have
+  // started: every thread says so here, and the gather covers the wait below.
+  __syncwarp();
+  cluster_arrive();
   if (threadIdx.x < kNodes) {
     const int i = threadIdx.x;
     float px = 0.f, qx = 0.f;
@@ -712,6 +722,7 @@ verify_tree_kernel(const VerifyParams p) {
     s.u[i] = u;
   }
   __syncthreads();
+  cluster_wait();  // before any sum is stored to another CTA
 
   const float u_sample = p.u_sample[b];
   Walk<T, kDraft, kWarps> walk{p, s, n0, rank, lane, warp, ring + threadIdx.x};

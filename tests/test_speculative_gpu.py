@@ -223,6 +223,17 @@ def test_verify_rows_larger_than_shared_memory(B, V, kind, draft):
     check_verify(c)
 
 
+@pytest.mark.parametrize("V", [4097, 8193, 16385])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_verify_many_short_rows_of_several_ctas(V, kind):
+    """Many more clusters (of 2, 4 and 8 CTAs) than fit the GPU, each with one
+    short pass, every third row padding: the sums that a cluster exchanges come
+    right after its CTAs' start."""
+    B = 700
+    check_verify(S.verify_case(V, B, 1, V, draft=False, kind=kind,
+                               tree=[0 if b % 3 == 1 else 1 for b in range(B)]))
+
+
 def test_verify_one_node_and_padding():
     c = S.verify_case(5, 3, 1, 100, tree=[1, 0, 1])
     got = check_verify(c)
