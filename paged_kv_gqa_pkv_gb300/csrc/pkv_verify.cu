@@ -442,7 +442,8 @@ struct Walk {
     // (the last granule may hang over the row's end: what lies behind it reads as 0)
     auto fetch = [&](int g, int slot) {
       if (g + lane < g1) {
-        const int bytes = min(16, (pv.end - (g + lane) * E) * static_cast<int>(sizeof(T)));
+        // (in values first: a row's bytes pass 32 bits)
+        const int bytes = min(E, pv.end - (g + lane) * E) * static_cast<int>(sizeof(T));
         cp_async16_fill(ring + (2 * slot) * kThreads, from_p + g, bytes);
         if (with_q) cp_async16_fill(ring + (2 * slot + 1) * kThreads, from_q + g, bytes);
       }

@@ -262,6 +262,29 @@ def test_verification_of_rows_past_32_bits():
     assert (toks[:, :39] == V - 1).all() and (toks[:, 39] == 7).all()
 
 
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [(1 << 29) + 5, (1 << 30) - 1, 1 << 30])
+def test_verification_of_the_longest_rows(V, kind):
+    """Rows whose bytes, or whose values, pass 31 bits: the largest vocabulary that
+    is taken, and borders below it. Four tokens have the mass, at the row's ends, in
+    its middle and where the remaining bytes fall under 2^31; the drafted one is
+    refused, so the draw is from the other three."""
+    at = sorted([0, V // 2, V - (1 << 29) + 1, V - 1])
+    t = torch.zeros((2, 2, V), dtype=kind, device="cuda")
+    t[:, 0, at] = torch.tensor([0.125, 0.25, 0.125, 0.5], device="cuda").to(kind)
+    tok = torch.full((2, 2), V - 1, dtype=torch.int32, device="cuda")
+    parents = torch.tensor([[-1, 0]] * 2, dtype=torch.int32, device="cuda")
+    lens = torch.full((2,), 2, dtype=torch.int32, device="cuda")
+    left = np.cumsum([0.125, 0.25, 0.125])   # 0.75 > 0.5: the last token is refused
+    want = lambda u: at[int(np.nonzero(left > u * 0.5)[0][0])]  # noqa: E731
+    for u in ((0.0, 0.3), (0.5, 0.99)):
+        path, toks, n = binding.pkv_verify_tree(
+            t, tok, parents, lens, torch.full((2, 2), 0.75, device="cuda"),
+            torch.tensor(u, device="cuda"))
+        assert n.cpu().tolist() == [1, 1]
+        assert toks[:, 0].cpu().tolist() == [want(x) for x in u]
+
+
 @pytest.mark.parametrize("how", ["small", "misaligned", "device", "type"])
 def test_refused_workspaces_and_outputs(how):
     m = S.Mirror(4, [30], 16, 1, 8, 4, slots=3)
