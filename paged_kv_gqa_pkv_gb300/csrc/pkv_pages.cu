@@ -381,7 +381,11 @@ __global__ void __launch_bounds__(kPlanThreads) compact_apply_kernel(const Pages
     if (e < n_live || e >= p.num_pages) continue;
     const int c = e / p.chunk_pages;
     const int in_chunk = e - c * p.chunk_pages - p.free_before[e];  // live pages below it there
-    if (p.live_list[static_cast<int64_t>(c) * p.chunk_pages + in_chunk] != e ||
+    // (a free page above its chunk's last live one has no place in the list)
+    const int end = min((c + 1) * p.chunk_pages, p.num_pages);
+    const int in_list = end - c * p.chunk_pages - (prefix[c + 1] - prefix[c]);
+    if (in_chunk >= in_list ||
+        p.live_list[static_cast<int64_t>(c) * p.chunk_pages + in_chunk] != e ||
         live_prefix(c) + in_chunk < stay) {
       set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PAGE);
       continue;

@@ -507,3 +507,61 @@ def test_compact_entries_of_free_pages_stay():
     for g, w in zip(got, want):
         assert np.array_equal(g, w)
     assert got[5] == spec.BAD_PAGE
+
+
+def compact_workspace(st, word):
+    k, t = dev(S.from_bits(st.k)), dev(st.table)
+    n = binding.pkv_compact_workspace_size(k, t, st.ps)
+    return torch.full((n // 4,), word, dtype=torch.int32, device="cuda").view(torch.uint8)
+
+
+def check_compact_in(st, workspace):
+    err = new_dev_err()
+    k, v, t, r = dev(S.from_bits(st.k)), dev(S.from_bits(st.v)), dev(st.table), dev(st.refs)
+    n = binding.pkv_compact_pages(k, v, t, r, st.ps, workspace=workspace, dev_err=err)
+    torch.cuda.synchronize()
+    got = (bf16_bits(k.cpu()), bf16_bits(v.cpu()), t.cpu().numpy(), r.cpu().numpy(),
+           int(n.item()), int(err.item()))
+    want = spec.compact_pages(st.k, st.v, st.table, st.refs, st.ps)
+    for name, g, w in zip(("k", "v", "table", "refs", "live", "err"), got, want):
+        assert np.array_equal(g, w), name
+    return got
+
+
+@pytest.mark.parametrize("dangling", [9, 15, 18, 19])
+def test_compact_entries_of_free_pages_whatever_the_workspace_holds(dangling):
+    """Every word of the workspace is the number of the free page that an entry
+    names, below the highest live page and above it."""
+    st = S.pages_state(11, [], 16, 1, 20, 4, slots=3)
+    st.refs[[1, 2, 8, 13]] = 1
+    st.table[1] = [1, 2, 8, 13]
+    st.table[2, 1] = dangling
+    got = check_compact_in(st, compact_workspace(st, dangling))
+    assert got[5] == spec.BAD_PAGE and got[2][2, 1] == dangling
+
+
+@pytest.mark.parametrize("dangling", [4000, 4095, 4096, 8100, 8191, 8192, 8999])
+def test_compact_entries_of_free_pages_in_several_chunks(dangling):
+    """The same over three chunks of counts, with most pages free."""
+    st = S.pages_state(12, [], 16, 1, 9000, 8, slots=9)
+    rng = np.random.default_rng(dangling)
+    used = np.setdiff1d(1 + rng.permutation(8999)[:700], [dangling])
+    st.refs[used] = 1
+    st.table[1:8] = rng.choice(used, (7, 8))
+    st.table[8, 3] = dangling
+    got = check_compact_in(st, compact_workspace(st, dangling))
+    assert got[5] == spec.BAD_PAGE and got[2][8, 3] == dangling
+
+
+def test_compact_twice_on_one_workspace():
+    """What an earlier call left in the workspace names a page that is free now."""
+    st = S.pages_state(13, [], 16, 1, 20, 4, slots=3)
+    st.refs[[1, 2, 3, 9]] = 1
+    st.table[1] = [1, 2, 3, 9]
+    ws = compact_workspace(st, -1)
+    assert check_compact_in(st, ws)[5] == 0
+    st.refs[[3, 9]], st.refs[8] = 0, 1
+    st.table[1] = [1, 2, 8, -1]
+    st.table[2, 0] = 9
+    got = check_compact_in(st, ws)
+    assert got[5] == spec.BAD_PAGE and got[2][2, 0] == 9
