@@ -510,9 +510,12 @@ def _dev_err(t, dev: int) -> Optional[int]:
 # microseconds less per call), where this PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # PyTorch's caching allocator without a tensor around the memory: a workspace
-# that lives for one call costs 2.5 us this way and 5.7 as a tensor.
+# that lives for one call costs 2.5 us this way and 5.7 as a tensor, which it is
+# where this PyTorch does not have them.
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+if _raw_delete is None:
+    _raw_alloc = None
 
 
 def _handle(name: str, dev: int, stream) -> int:
@@ -546,6 +549,9 @@ def _run_with(workspace, size, name: str, dev: int, stream, err, fn, *args) -> N
             _run_with(workspace, size, name, dev, stream, err, fn, *args)
         return
     handle = _handle(name, dev, stream)
+    if workspace is None and _raw_alloc is None:
+        with torch.cuda.stream(stream):   # (None: the current one)
+            workspace = torch.empty(max(size(), 256), dtype=torch.uint8, device=f"cuda:{dev}")
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
                 not workspace.is_contiguous():

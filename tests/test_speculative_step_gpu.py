@@ -301,6 +301,31 @@ def test_refused_workspaces_and_outputs(how):
     m.equal()
 
 
+@pytest.mark.parametrize("named", [False, True])
+def test_workspaces_without_the_allocators_raw_calls(monkeypatch, named):
+    """A PyTorch that lacks the raw allocation calls: workspaces are tensors of the
+    call's stream, and the results are the same."""
+    c = S.tree_case(23, [900, 80], [16, 9], 16)
+    to = lambda a: (a if isinstance(a, torch.Tensor) else torch.from_numpy(a)).cuda()  # noqa: E731
+    args = [to(x) for x in (c.k, c.v, c.table, c.q, c.parents, c.lens, c.slots, c.ctx)] + \
+        [c.ps, c.scale]
+    want = binding.pkv_tree_attention(*args)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(binding, "_raw_alloc", None)
+    stream = torch.cuda.Stream() if named else None
+    more = []
+    for _ in range(10):
+        more.append(binding.pkv_tree_attention(*args, stream=stream))
+        torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for o, l in more:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    m = S.Mirror(5, [30, 50], 16, 1, 20, 6, slots=4)
+    m.update([1, 3], [1, 2], [30, 40], [45, 45])
+    m.compact()
+    m.equal()
+
+
 def test_calls_without_buffers_are_captured():
     """Results and workspaces allocated inside the capture; two graphs replayed in
     turn, each with inputs changed in place between replays."""
