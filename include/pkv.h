@@ -509,7 +509,8 @@ pkv_status pkv_verify_tree(const void* target_probs, const void* draft_probs, in
  * before anything overwrites it). path: int32 [batch, n_nodes] with
  * path[b, 0..n) strictly increasing in [0, n_nodes), as pkv_verify_tree
  * writes it. new_lens: int32 [batch] or null; new_lens[b] = ctx + n (it may be
- * ctx_lens itself). Rows with slot 0 or n = 0 move nothing and give ctx. A
+ * ctx_lens itself; where several layers' calls share ctx_lens, in the last one's
+ * only). Rows with slot 0 or n = 0 move nothing and give ctx. A
  * slot out of range sets PKV_DEV_ERR_BAD_SLOT, an n or a path that breaks the
  * above PKV_DEV_ERR_BAD_TREE, a position past the table PKV_DEV_ERR_BAD_POS, a
  * page entry out of range at a moved position PKV_DEV_ERR_BAD_PAGE: the row
@@ -564,7 +565,18 @@ size_t pkv_update_workspace_size(const pkv_cache_desc* cache, int n);
  * pages where the needs of the rows up to it exceed the free ones). Entries of
  * the destination outside [1, num_pages) count as unreserved.
  * page_size x num_kv_heads must be below 2^25. page_table, page_refs, k_pool and
- * v_pool are updated in place. workspace: at least pkv_update_workspace_size()
+ * v_pool are updated in place.
+ *
+ * One call serves one pool pair, and its copies follow from the table and counts
+ * that it finds. A second layer's call on the updated state would find the pages
+ * handed out already and leave its own rows behind, without an error. So every
+ * layer's call takes the state as it was before the first one's: layers with a
+ * table and counts each have that; where layers share them, all calls but the last
+ * are made on copies (device to device, before the first call; the result depends
+ * on the state alone, so every copy ends as the shared state does, and can be
+ * dropped).
+ *
+ * workspace: at least pkv_update_workspace_size()
  * bytes, 256-byte aligned, no initialisation needed; calls that share one must
  * be stream-ordered.
  */
@@ -587,7 +599,11 @@ size_t pkv_compact_workspace_size(const pkv_cache_desc* cache);
  * page numbered L or more, in ascending order, moves to the k-th free page
  * below L: its K and V rows are copied, every entry of page_table that names
  * it is rewritten, and its count goes with it. Pages below L that are live
- * stay where they are; afterwards the live pages are 0 .. L-1. num_live: int32
+ * stay where they are; afterwards the live pages are 0 .. L-1. Pages that only
+ * the caller's own holds keep alive move like the others, and nothing says where
+ * to: a page that has to be found again belongs in a slot of the table. Several
+ * layers that share a table and counts: as for pkv_update_pages, all calls but the
+ * last on copies of the state before the first. num_live: int32
  * [1] or null, receives L. page_refs as for pkv_update_pages, none negative. An
  * entry of page_table that names a free page at or past L sets
  * PKV_DEV_ERR_BAD_PAGE and is left as it is; other entries outside

@@ -645,7 +645,7 @@ def pkv_commit_path(k_pool, v_pool, page_table, path, n_accepted, batch_idx, ctx
     """Moves the K/V rows of the accepted nodes path[b, :n_accepted[b]] from
     positions ctx_lens[b] + node to ctx_lens[b], ctx_lens[b] + 1, ... in
     place. Returns new_lens [B] = ctx_lens + n_accepted (``new_lens`` may be
-    ctx_lens itself)."""
+    ctx_lens itself, with several layers in the last one's call)."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     _need(path, "path", torch.int32, 2)
     B, N = path.shape
@@ -674,7 +674,10 @@ def pkv_update_pages(k_pool, v_pool, page_table, page_refs, dst_slots, src_slots
     """Fork, reserve, copy on write, truncate and free, in place: slot
     dst_slots[i] gets the first keep_lens[i] tokens of slot src_slots[i] (pages
     shared) and pages of its own for the positions up to new_lens[i].
-    page_refs [num_pages] counts the table entries that use each page (0: free)."""
+    page_refs [num_pages] counts the table entries that use each page (0: free).
+    A call moves the rows of one layer's pools. Layers that share page_table and
+    page_refs make all calls but the last on clones of both, taken before the
+    first: on the updated state a layer's rows would stay behind."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     _need(dst_slots, "dst_slots", torch.int32, 1)
     n = dst_slots.shape[0]
@@ -701,7 +704,8 @@ def pkv_compact_workspace_size(k_pool, page_table, page_size: int) -> int:
 def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num_live=None,
                       workspace=None, dev_err=None, stream=None):
     """Moves the live pages to the low end of the pool (K/V rows, table
-    entries and counts), in place. Returns num_live [1], how many there are."""
+    entries and counts), in place. Returns num_live [1], how many there are.
+    Layers that share page_table and page_refs: as for ``pkv_update_pages``."""
     dev, desc, k, v, table = _cache(k_pool, v_pool, page_table, page_size)
     refs = _tensor("page_refs", page_refs, torch.int32, (desc.num_pages,), dev)
     num_live, live_p = _result("num_live", num_live, page_refs, dev, stream, (1,), torch.int32)

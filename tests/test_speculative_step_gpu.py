@@ -55,6 +55,61 @@ def test_a_loop_of_steps(ps, N):
     m.equal()
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_layers_that_share_one_table(captured):
+    """Three layers' pools behind one table: all calls but the last on clones of the
+    table and counts from before the first. A fork, copies on write, an accepted path
+    and a compaction; every layer's bytes, and every clone, equal the oracle's."""
+    ps, hkv, pages = 16, 2, 40
+    st = S.pages_state(6, [37, 20, 5], ps, hkv, pages, 6, slots=7)
+    rng = np.random.default_rng(6)
+    bits = [S.pool_bits(rng, pages * ps, hkv) for _ in range(3)]
+    pools = [[S.from_bits(x).cuda() for x in b] for b in bits]
+    i32 = lambda x: torch.from_numpy(np.array(x, dtype=np.int32)).cuda()  # noqa: E731
+    table, refs, err = i32(st.table), i32(st.refs), i32([0])
+    calls = [([4, 5], [1, 2], [37, 18], [37, 25]), ([1, 4, 3], [1, 4, 3], [37, 37, 5], [45, 40, 5]),
+             ([2], [2], [0], [0])]
+    gpu_calls = [[i32(x) for x in call] for call in calls]
+    slots, ctx = i32([1, 4]), i32([37, 37])
+    path, n = i32([[0, 2, 3, -1], [1, 2, -1, -1]]), i32([3, 2])
+    states = lambda: [(table.clone(), refs.clone()) for _ in pools[1:]] + [(table, refs)]  # noqa: E731
+
+    def steps():
+        for call in gpu_calls:
+            for (k, v), (t, r) in zip(pools, states()):
+                binding.pkv_update_pages(k, v, t, r, *call, ps, dev_err=err)
+        for i, (k, v) in enumerate(pools):
+            binding.pkv_commit_path(k, v, table, path, n, slots, ctx, ps, dev_err=err,
+                                    new_lens=ctx if i == len(pools) - 1 else None)
+        last = states()
+        for (k, v), (t, r) in zip(pools, last):
+            binding.pkv_compact_pages(k, v, t, r, ps, dev_err=err)
+        return last
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            last = steps()
+        graph.replay()
+    else:
+        last = steps()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and ctx.cpu().tolist() == [40, 39]
+    for (kb, vb), (k, v) in zip(bits, pools):
+        t, r = st.table, st.refs
+        for call in calls:
+            kb, vb, t, r, e = spec.update_pages(kb, vb, t, r, *call, ps)
+            assert e == 0
+        kb, vb, _, e = spec.commit_path(kb, vb, t, path.cpu().numpy(), [3, 2], [1, 4], [37, 37], ps)
+        assert e == 0
+        kb, vb, t, r, _, e = spec.compact_pages(kb, vb, t, r, ps)
+        assert e == 0
+        assert np.array_equal(bf16_bits(k.cpu()), kb) and np.array_equal(bf16_bits(v.cpu()), vb)
+    assert np.array_equal(table.cpu().numpy(), t) and np.array_equal(refs.cpu().numpy(), r)
+    for t, r in last[:-1]:
+        assert torch.equal(t, table) and torch.equal(r, refs)
+
+
 def test_steps_between_captured_decode_steps():
     """The table that captured decode steps hold is updated by the page
     operators between replays."""
