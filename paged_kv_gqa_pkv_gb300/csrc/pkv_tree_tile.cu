@@ -175,6 +175,14 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap qmap,
     tma_prefetch_desc(&vmap);
   }
   if (warp == 2) tmem_alloc(tmem_slot, C::kTmemCols);
+  // Q's rows past the item's, which no load writes, are 0: the scores of what an earlier
+  // kernel left there could send every tile through the slow path (33 of 64 rows, 64 x
+  // 768 keys: 72 us after a call with large q, 63 after others)
+  const int spare = (C::kRows - p.rows) * 8;  // 16-byte pieces of each half
+  for (int i = threadIdx.x; i < C::kWorkers * 2 * spare; i += C::kThreads)
+    *reinterpret_cast<uint4*>(smem + i / spare * C::kOperHalf + p.rows * 128 + i % spare * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   pdl_wait_primary();
   pdl_launch_dependents();  // the merge waits for this grid before it reads anything
   tile_prefix<kBN>(p, s_prefix, s_scan);
