@@ -65,6 +65,39 @@ def tree_oracle(c):
                                c.lens, c.slots, c.ctx, c.ps, c.scale)
 
 
+def tree_rows(c, rows):
+    """Batch rows `rows` of a case without errors, from the definition in 64 bits,
+    whole products at a time: per row (out, lse, A, e) of its live nodes with
+    A = sum_t w_t |V[t]|, what an error of the weights relative to themselves moves
+    the output by, and e = max_t sum_d |scale q_d K[t]_d|, what rounding errors of the
+    scores are relative to."""
+    from oracle.paged_attention import bf16_bits_to_f64
+    res = []
+    for b in rows:
+        ctx, n = int(c.ctx[b]), int(c.lens[b])
+        t = np.arange(ctx + n)
+        at = torch.from_numpy(c.table[int(c.slots[b])][t // c.ps].astype(np.int64) * c.ps + t % c.ps)
+        f64 = lambda x: bf16_bits_to_f64(bf16_bits(x))  # noqa: E731
+        k, v, q = f64(c.k[at]), f64(c.v[at]), f64(c.q[b, :n])
+        sees = np.zeros((n, 1, ctx + n), dtype=bool)
+        sees[:, :, :ctx] = True
+        for i, kin in enumerate(spec.ancestors(c.parents[b], n)):
+            sees[i, 0, [ctx + a for a in kin]] = True
+        group = q.shape[1] // k.shape[1]
+        out, lse, mass, size = (np.zeros(s) for s in (q.shape, q.shape[:2], q.shape, q.shape[:2]))
+        for h in range(k.shape[1]):
+            of = slice(h * group, (h + 1) * group)
+            x = np.where(sees, c.scale * (q[:, of] @ k[:, h].T), -np.inf)
+            m = x.max(-1, keepdims=True)
+            w = np.exp(x - m)
+            l = w.sum(-1, keepdims=True)
+            out[:, of], mass[:, of] = w / l @ v[:, h], w / l @ np.abs(v[:, h])
+            lse[:, of] = (m + np.log(l))[..., 0]
+            size[:, of] = np.where(sees, c.scale * (np.abs(q[:, of]) @ np.abs(k[:, h]).T), 0).max(-1)
+        res.append((out, lse, mass, size))
+    return res
+
+
 def verify_case(seed, B, N, V, draft=True, kind=torch.float32, shape="random", spread=2.5,
                 tree=None):
     g = torch.Generator().manual_seed(seed)

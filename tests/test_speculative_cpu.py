@@ -160,6 +160,17 @@ def test_siblings_do_not_see_each_other():
         np.testing.assert_allclose(l[0], lse[0, path], atol=1e-12)
 
 
+def test_whole_products_equal_the_oracle():
+    c = S.tree_case(3, [20, 0, 33], [5, 4, 1], 5, hq=4, hkv=2, shape="forest")
+    out, lse, err, _ = S.tree_oracle(c)
+    assert err == 0
+    for b, (o, l, mass, size) in enumerate(S.tree_rows(c, range(3))):
+        n = c.lens[b]
+        np.testing.assert_allclose(o, out[b, :n], atol=1e-12)
+        np.testing.assert_allclose(l, lse[b, :n], atol=1e-12)
+        assert (mass >= np.abs(o)).all() and (size > 0).all()
+
+
 def test_nested_residuals_collapse():
     """max(max(p - a q, 0) - R q, 0) = max(p - (a + R) q, 0), the kernel's form."""
     rng = np.random.default_rng(0)

@@ -159,6 +159,55 @@ def test_tree_large_scores_and_order_of_maxima():
     check_tree(c)
 
 
+def check_tree_rows(c, rows, out, lse):
+    """Against whole products in 64 bits. Tolerances: products of bf16 values are
+    exact in fp32 and 128 of them are summed there, an error of at most 2^-23 of the
+    sum of magnitudes each (a tensor core truncates), and as much for the scaling to
+    log2 units and the exponential's argument: e = 131 * 2^-23 * max sum |scale q K|.
+    The weights' errors are e and the roundings of P to bf16, 2^-8 relative at most, the
+    output's rounding is 2^-8 of the value; sums of positive terms in fp32 add less than
+    (keys) * 2^-24, the exponentials and the logarithm (2^-22 each, of the weights, the
+    rescales and the merge) 2^-20. Nodes past the tree give 0 and -inf."""
+    for b, (ro, rl, mass, size) in zip(rows, S.tree_rows(c, rows)):
+        n, keys = int(c.lens[b]), int(c.ctx[b] + c.lens[b])
+        e = 131 * 2.0 ** -23 * size + keys * 2.0 ** -24 + 2.0 ** -20
+        o, l = out[b].double().numpy(), lse[b].double().numpy()
+        assert (o[n:] == 0).all() and np.isneginf(l[n:]).all()
+        bad = np.abs(l[:n] - rl) - (e + 2.0 ** -22 * np.abs(rl))
+        assert bad.max() <= 0, (b, "lse", bad.max())
+        bad = np.abs(o[:n] - ro) - (2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * e[..., None]) * mass)
+        assert bad.max() <= 0, (b, "out", bad.max())
+
+
+@pytest.mark.parametrize("N,group", [(1, 1), (2, 4), (3, 4), (8, 4), (16, 4), (17, 4), (32, 4),
+                                     (17, 8), (64, 4), (64, 8)])
+@pytest.mark.parametrize("scores", ["even", "growing"])
+def test_tree_more_tiles_than_workers(N, group, scores):
+    """384 items of up to 8 key tiles: every worker's range has several tiles and
+    segments, in all forms (up to 8, 64, 128 and 256 query rows, and blocks of 256).
+    With growing scores a row's maximum rises by about 14 in log2 units from one
+    128-key tile to the next for a third of the rows, by less or hardly for the others;
+    without, it never moves by 8. The workspace is full of NaN."""
+    rng = np.random.default_rng(N + group)
+    B, hkv = 48, 8
+    ctx = rng.integers(250, 900, B)
+    ctx[::5] = rng.integers(0, 140, len(ctx[::5]))
+    tree = rng.integers(max(1, N // 2), N + 1, B)
+    c = S.tree_case(15, ctx.tolist(), tree.tolist(), N, hq=hkv * group, hkv=hkv, ps=64, pad=(9,))
+    if scores == "growing":
+        for b in range(B):
+            t = np.arange(ctx[b] + tree[b])
+            at = torch.from_numpy(c.table[b + 1][t // 64].astype(np.int64) * 64 + t % 64)
+            c.k[at] *= torch.from_numpy(0.5 + t / 32.0).bfloat16()[:, None, None]
+        c.q *= torch.from_numpy(rng.choice([0.02, 0.3, 1.0], c.q.shape[:3] + (1,))).bfloat16()
+    k, t = dev(c.k), dev(c.table)
+    n = binding.pkv_tree_workspace_size(k, t, c.ps, B, N, hkv * group)
+    out, lse, err = run_tree(c, workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+    assert err == 0
+    check_tree_rows(c, [0, 1, 2, 20, 33, 46, 47], out, lse)
+    assert torch.all(out[9] == 0) and torch.all(torch.isneginf(lse[9]))
+
+
 def test_tree_same_bits_twice_and_on_a_side_stream():
     c = S.tree_case(11, [1500, 800], [30, 64], 64, hq=8, hkv=2, ps=64)
     a = run_tree(c)
