@@ -442,8 +442,9 @@ struct Walk {
     // (the last granule may hang over the row's end: what lies behind it reads as 0)
     auto fetch = [&](int g, int slot) {
       if (g + lane < g1) {
-        // (in values first: a row's bytes pass 32 bits)
-        const int bytes = min(E, pv.end - (g + lane) * E) * static_cast<int>(sizeof(T));
+        // (by the values that hang over: the bytes left of a row pass 32 bits)
+        const int over = max((g + lane + 1) * E - pv.end, 0);
+        const int bytes = 16 - over * static_cast<int>(sizeof(T));
         cp_async16_fill(ring + (2 * slot) * kThreads, from_p + g, bytes);
         if (with_q) cp_async16_fill(ring + (2 * slot + 1) * kThreads, from_q + g, bytes);
       }
