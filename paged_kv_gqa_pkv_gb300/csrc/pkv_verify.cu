@@ -30,7 +30,7 @@
 // are exact in fp32 whatever their type.
 //
 // Measured: one chain of 6 nodes, 32000 tokens, without a draft 6.3 us; 12 trees of 16
-// nodes, 50257 in fp32 12.7 us; 64 trees, 151936 in bf16 29 us, of which the longest row
+// nodes, 50257 in fp32 12.8 us; 64 trees, 151936 in bf16 29 us, of which the longest row
 // spends three dependent passes (8, then ~5 us each beside the other rows') and a draw.
 #include <atomic>
 
@@ -67,14 +67,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+// (for a barrier that orders no writes)
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   cluster_wait();
 }
 // Unevaluated sum of two floats.
@@ -697,9 +698,11 @@ verify_tree_kernel(const VerifyParams p) {
     return;
   }
   // A CTA's shared memory may be written by the others once it is known to have
-  // started: every thread says so here, and the gather covers the wait below.
+  // started: every thread says so here, and the gather covers the wait below. (A
+  // releasing arrive took 0.2 to 0.4 us of a call, waiting behind the first pass
+  // gained nothing.)
   __syncwarp();
-  cluster_arrive();
+  cluster_arrive_relaxed();
   if (threadIdx.x < kNodes) {
     const int i = threadIdx.x;
     float px = 0.f, qx = 0.f;
