@@ -424,7 +424,10 @@ size_t pkv_tree_workspace_size(const pkv_cache_desc* cache, int batch, int n_nod
  * int32 [batch]; out: bf16 like q; lse: fp32 [batch, n_nodes, num_q_heads].
  * Nodes at or past tree_lens[b] (padding) and every node of a row with slot 0
  * give out 0, lse -inf. n_nodes is 1 .. PKV_MAX_TREE_NODES; ctx_lens[b] may be
- * 0. A slot outside [0, max_batch) sets PKV_DEV_ERR_BAD_SLOT, a tree_lens[b]
+ * 0. Scores, softmax sums and products are held in fp32; the weights exp(..) are
+ * rounded to bf16 for the product with V, as in the decode and the prefills (their
+ * sum takes them unrounded), and out is rounded once: each is off by at most 2^-8
+ * of its value. A slot outside [0, max_batch) sets PKV_DEV_ERR_BAD_SLOT, a tree_lens[b]
  * outside [0, n_nodes] PKV_DEV_ERR_BAD_TREE, a negative ctx_lens[b] or
  * ctx + tree_lens[b] past the table PKV_DEV_ERR_BAD_POS: the row gives 0 /
  * -inf. A parent outside [-1, i) sets PKV_DEV_ERR_BAD_TREE; that node and

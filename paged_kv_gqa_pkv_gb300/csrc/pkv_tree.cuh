@@ -6,7 +6,9 @@
 // context, which every row sees whole, and the tree's own nodes, where a row sees
 // its ancestors. So the keys stream once per (sequence, kv head) however large the
 // tree is (up to 256 rows; above that the rows are blocks of 256, which read the
-// keys once each, from L2 as a rule).
+// keys once each: a worker takes a sequence's second block after the first, when the
+// other workers' keys have passed through L2. 32 sequences of ~2560 keys at 8 kv heads
+// and 384 rows read 715 MB from DRAM, twice the keys' bytes).
 //
 // Work list: all (sequence, kv head, row block) items' key tiles in one list, cut
 // into equal ranges, one per worker (a CTA, a warpgroup or a warp); a range's pieces
@@ -20,6 +22,11 @@
 // the context needs no mask; in the last ones a row's visible keys are the context's
 // and its word shifted to the tree's place. V rows past the last node are zeroed
 // before the product (stale slots may hold any bits, and 0 * NaN is not 0).
+//
+// Numbers: S, the maxima and sums and O are fp32. P is rounded to bf16, the type of V,
+// which the MMAs take with it: 2^-8 of each weight at most, and the sums take the
+// unrounded weights. Against 64 bits the output's error is 2.3e-3 of its size, of which
+// its own rounding to bf16 is 1.7e-3.
 #pragma once
 
 #include <atomic>
