@@ -606,12 +606,13 @@ size_t pkv_compact_workspace_size(const pkv_cache_desc* cache);
  * the caller's own holds keep alive move like the others, and nothing says where
  * to: a page that has to be found again belongs in a slot of the table. Several
  * layers that share a table and counts: as for pkv_update_pages, all calls but the
- * last on copies of the state before the first. num_live: int32
- * [1] or null, receives L. page_refs as for pkv_update_pages, none negative. An
- * entry of page_table that names a free page at or past L sets
- * PKV_DEV_ERR_BAD_PAGE and is left as it is; other entries outside
- * [0, num_pages) are left too. workspace: at least
- * pkv_compact_workspace_size() bytes, 256-byte aligned, no initialisation
+ * last on copies of the state before the first.
+ * num_live: int32 [1] or null, receives L. page_refs as for pkv_update_pages, none
+ * negative. An entry of page_table that names a free page at or past L sets
+ * PKV_DEV_ERR_BAD_PAGE and is left as it is; entries outside [0, num_pages) are
+ * left without an error, and so are those of free pages below L, which then name
+ * what has moved there (pkv_update_pages leaves no such entries). workspace: at
+ * least pkv_compact_workspace_size() bytes, 256-byte aligned, no initialisation
  * needed; calls that share one must be stream-ordered.
  */
 pkv_status pkv_compact_pages(const pkv_cache_desc* cache, void* k_pool, void* v_pool,
