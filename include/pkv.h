@@ -29,6 +29,14 @@
  *                           committed context
  *   pkv_update_pages      - fork, reserve, copy on write, truncate and free
  *   pkv_compact_pages     - live pages moved to the low end of the pool
+ * and, for attention whose keys and values come from one latent vector a token
+ * that all heads share (further operators of this library):
+ *   pkv_rotate            - the rotary embedding, interleaved or in halves
+ *   pkv_latent_append     - new tokens' rows, normalised and rotated, written
+ *                           through the page table
+ *   pkv_latent_gather     - cached rows read back through the page table
+ *   pkv_latent_decode_attention  - the absorbed form, over the cached rows
+ *   pkv_latent_prefill_attention - the expanded form, packed sequences
  *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -45,8 +53,8 @@
  *  - Calls only enqueue work on `stream` (NULL = the legacy default stream),
  *    never synchronise it, and keep no state between calls, so they may be
  *    captured into a CUDA graph.
- *  - head_dim must be 128; num_q_heads / num_kv_heads (the GQA group) must be
- *    1, 2, 4 or 8; page_size must be a positive multiple of 16; bf16 tensors
+ *  - head_dim must be 128 (the pkv_latent_* calls: 576, with num_kv_heads 1);
+ *    num_q_heads / num_kv_heads (the GQA group) must be 1, 2, 4 or 8; page_size must be a positive multiple of 16; bf16 tensors
  *    must be 16-byte aligned; int32/fp32 arrays 4-byte aligned.
  */
 #ifndef PKV_H
@@ -619,6 +627,126 @@ pkv_status pkv_compact_pages(const pkv_cache_desc* cache, void* k_pool, void* v_
                              int32_t* page_table, int32_t* page_refs, int32_t* num_live,
                              void* workspace, size_t workspace_bytes, int32_t* dev_err,
                              cudaStream_t stream);
+
+/* Sizes of the pkv_latent_* calls: a cache row is a token's latent, then its
+ * rotated part; expanded, a head's key is its own part, then the token's
+ * rotated part. */
+#define PKV_LATENT_DIM 512
+#define PKV_LATENT_ROTATED 64
+#define PKV_LATENT_ROW 576
+#define PKV_LATENT_KEY 128
+#define PKV_LATENT_VALUE 128
+
+/*
+ * pkv_rotate - the rotary position embedding of tokens' heads, in place or into
+ * another tensor.
+ *
+ * x: bf16, the value d of head h of token i at x[i * x_token_stride + h *
+ * x_head_stride + d], 0 <= d < dims; out likewise with its own strides (in
+ * values, >= 0). So the rotated dims may be a part of a longer head: x points at
+ * its first. dims is even; rope_cos, rope_sin: fp32 [rope_len, dims / 2]
+ * row-major, the cosines and sines of position p in row p (whatever scaling for
+ * long contexts they hold is the caller's). With j < dims / 2, c and s of
+ * (positions[i], j), the pair (a, b) = (x_j, x_{j + dims/2}), or (x_{2j},
+ * x_{2j+1}) with interleaved = 1, becomes
+ *     (a c - b s, b c + a s)
+ * computed in fp32 and rounded to nearest even once. out may be x itself with the
+ * same strides; otherwise no value of out may lie on one of x that the call
+ * reads. Values of out must not lie on one another: strides for which the inner
+ * axis's rows do not end before the outer one's next are PKV_ERR_ARG (x may
+ * repeat values: a stride of 0). A token whose position is outside [0, rope_len)
+ * is not written and sets PKV_DEV_ERR_BAD_POS. Pointers need 2-byte (x, out) and
+ * 4-byte alignment; with 16-byte alignment of all four tensors, strides that are
+ * multiples of 8 and dims of 16 (8 if interleaved) the call moves 16 bytes at a
+ * time. n_tokens >= 0, num_heads >= 1.
+ */
+pkv_status pkv_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, int n_tokens,
+                      int num_heads, int dims, int interleaved, const int32_t* positions,
+                      const float* rope_cos, const float* rope_sin, int rope_len,
+                      int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * pkv_latent_append - new tokens' latents and position parts into the paged cache.
+ *
+ * The cache of a layer is one pool, bf16 [num_pages * page_size, 576] contiguous,
+ * described by a pkv_cache_desc with num_kv_heads = 1, head_dim = 576; page table,
+ * slots and positions are as for pkv_append. x_new: bf16, token i's 576 values at
+ * x_new + i * x_token_stride (a multiple of 8; >= 0): its latent l, then its position
+ * part. With norm_weight (fp32 [512], 16-byte aligned) the latent becomes
+ *     l_d * norm_weight[d] / sqrt(mean_d(l_d^2) + norm_eps)
+ * (norm_eps finite and >= 0, else PKV_ERR_ARG; ignored without a weight), without
+ * it is copied bit for bit. The position part is rotated as by pkv_rotate with
+ * dims = 64 and tables [rope_len, 32], 16-byte aligned. Each value is rounded to bf16
+ * once. Tokens of slot 0 are skipped; a bad slot, position (also one past
+ * rope_len) or page entry skips the token and sets its bit. Two tokens that
+ * address one row race.
+ */
+pkv_status pkv_latent_append(const pkv_cache_desc* cache, void* pool, const int32_t* page_table,
+                             const void* x_new, int64_t x_token_stride,
+                             const int32_t* batch_idx, const int32_t* input_pos, int n_tokens,
+                             const float* rope_cos, const float* rope_sin, int rope_len,
+                             int interleaved, const float* norm_weight, float norm_eps,
+                             int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * pkv_latent_gather - sequences' cached rows, one after another.
+ *
+ * Row starts[b] + t of out (bf16 [total, 576], contiguous, 16-byte aligned), for 0 <= t <
+ * starts[b + 1] - starts[b], becomes the pool row of position t of slot slots[b]
+ * (byte for byte). slots: int32 [n_seqs]; starts: int32 [n_seqs + 1], ascending
+ * (equal neighbours: an empty sequence) from 0 or more to at most total, else
+ * PKV_DEV_ERR_LAYOUT is set and what is written is unspecified (never outside
+ * out). Rows before starts[0], from starts[n_seqs] on, and those of slot 0 stay as
+ * they were. A bad slot, a position past the table or a bad page entry sets its
+ * bit and leaves the row as it was.
+ */
+pkv_status pkv_latent_gather(const pkv_cache_desc* cache, const void* pool,
+                             const int32_t* page_table, const int32_t* slots,
+                             const int32_t* starts, int n_seqs, int total, void* out,
+                             int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * pkv_latent_decode_workspace_size - bytes of workspace pkv_latent_decode_attention
+ * needs on the CURRENT device (0 for invalid arguments).
+ */
+size_t pkv_latent_decode_workspace_size(const pkv_cache_desc* cache, int batch, int n_q,
+                                        int num_heads);
+
+/*
+ * pkv_latent_decode_attention - attention of new tokens over the cached rows (the
+ * absorbed form: queries and results live in the latent's space), on tcgen05
+ * tensor cores.
+ *
+ * q: bf16 [batch, n_q, num_heads, 576], contiguous: a head's query times its
+ * up-projection of keys (512), then its rotated part (64). Row b's n_q tokens are
+ * the last of the first n = seq_lens[b] positions of slot c = batch_idx[b] (their
+ * own rows are in the pool: pkv_latent_append first); token j sees the rows
+ * t < e = n - (n_q - 1 - j). With C[t] the row of position t:
+ *   lse[b, j, h] = ln sum_{t<e} exp(scale * q[b,j,h] . C[t])                    (fp32)
+ *   out[b, j, h] = sum_{t<e} exp(scale * q[b,j,h] . C[t] - lse) C[t][0:512]
+ * out: bf16 [batch, n_q, num_heads, 512], 32-byte aligned; lse: fp32 [batch, n_q,
+ * num_heads]. e <= 0, slot 0 and n = 0 give out 0, lse -inf. Scores, sums and
+ * products are held in fp32; the weights exp(..) are rounded to bf16 for the product
+ * (their sum takes them unrounded) and out is rounded once. A slot outside [0,
+ * max_batch) sets PKV_DEV_ERR_BAD_SLOT, an n < 0 or past the table
+ * PKV_DEV_ERR_BAD_POS: the row gives 0 / -inf. A page entry out of range within the
+ * first n rows sets PKV_DEV_ERR_BAD_PAGE and leaves the row unspecified. The pool is
+ * only read; rows past n may hold any bits. A NaN or infinity in a row below n
+ * reaches every query of the sequence.
+ * n_q 1 .. 64; num_heads 1 .. 1024; batch any count >= 0 (above 512 rows the call runs
+ * as equal launches that share the workspace); page_size any multiple of 16; scale
+ * finite and > 0. workspace: at least pkv_latent_decode_workspace_size() bytes,
+ * 256-byte aligned, owned by the caller, no initialisation needed; calls that
+ * share one must be stream-ordered. All tensors are device memory. The
+ * same inputs give the same bits on every run.
+ */
+pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, const void* pool,
+                                       const int32_t* page_table, const void* q, int num_heads,
+                                       const int32_t* batch_idx, const int32_t* seq_lens,
+                                       int batch, int n_q, float scale, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes,
+                                       int32_t* dev_err, cudaStream_t stream);
 
 /* Static, human-readable name of a status. */
 const char* pkv_status_string(pkv_status status);

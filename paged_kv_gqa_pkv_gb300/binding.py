@@ -16,6 +16,8 @@ Functions keep the names of the C entry points: ``pkv_append``,
 ``pkv_stage_from_host``, ``pkv_tree_workspace_size``, ``pkv_tree_attention``,
 ``pkv_verify_tree``, ``pkv_commit_path``, ``pkv_update_workspace_size``,
 ``pkv_update_pages``, ``pkv_compact_workspace_size``, ``pkv_compact_pages``,
+``pkv_rotate``, ``pkv_latent_append``, ``pkv_latent_gather``,
+``pkv_latent_decode_workspace_size``, ``pkv_latent_decode_attention``,
 ``pkv_status_string``, ``pkv_status_from_device_error`` and
 ``pkv_last_cuda_error_string``.
 """
@@ -43,6 +45,11 @@ DEV_ERR_BAD_TREE = 0x20
 DEV_ERR_NO_PAGES = 0x40
 DEV_ERR_BAD_PROBS = 0x80
 MAX_TREE_NODES = 64
+LATENT_DIM = 512       # a cache row of shared latents: the latent,
+LATENT_ROTATED = 64    # then the rotated part
+LATENT_ROW = LATENT_DIM + LATENT_ROTATED
+LATENT_KEY = 128       # expanded: a head's own part of a key
+LATENT_VALUE = 128     # expanded: a head's value
 
 EXPORTED = ("pkv_append", "pkv_append_rope", "pkv_decode_workspace_size", "pkv_decode_attention",
             "pkv_decode_append_attention", "pkv_decode_attention_static_scratch",
@@ -51,6 +58,8 @@ EXPORTED = ("pkv_append", "pkv_append_rope", "pkv_decode_workspace_size", "pkv_d
             "pkv_stage_from_host", "pkv_tree_workspace_size", "pkv_tree_attention",
             "pkv_verify_tree", "pkv_commit_path", "pkv_update_workspace_size",
             "pkv_update_pages", "pkv_compact_workspace_size", "pkv_compact_pages",
+            "pkv_rotate", "pkv_latent_append", "pkv_latent_gather",
+            "pkv_latent_decode_workspace_size", "pkv_latent_decode_attention",
             "pkv_status_string",
             "pkv_status_from_device_error", "pkv_last_cuda_error_string")
 
@@ -138,6 +147,20 @@ def load_library() -> ctypes.CDLL:
     lib.pkv_compact_workspace_size.restype = c_size
     lib.pkv_compact_pages.argtypes = [desc_p, vp, vp, i32p, i32p, i32p, vp, c_size, i32p, vp]
     lib.pkv_compact_pages.restype = c_int
+    i64 = ctypes.c_int64
+    lib.pkv_rotate.argtypes = [vp, i64, i64, vp, i64, i64, c_int, c_int, c_int, c_int, i32p, f32p,
+                               f32p, c_int, i32p, vp]
+    lib.pkv_rotate.restype = c_int
+    lib.pkv_latent_append.argtypes = [desc_p, vp, i32p, vp, i64, i32p, i32p, c_int, f32p, f32p,
+                                      c_int, c_int, f32p, c_float, i32p, vp]
+    lib.pkv_latent_append.restype = c_int
+    lib.pkv_latent_gather.argtypes = [desc_p, vp, i32p, i32p, i32p, c_int, c_int, vp, i32p, vp]
+    lib.pkv_latent_gather.restype = c_int
+    lib.pkv_latent_decode_workspace_size.argtypes = [desc_p, c_int, c_int, c_int]
+    lib.pkv_latent_decode_workspace_size.restype = c_size
+    lib.pkv_latent_decode_attention.argtypes = [desc_p, vp, i32p, vp, c_int, i32p, i32p, c_int,
+                                                c_int, c_float, vp, f32p, vp, c_size, i32p, vp]
+    lib.pkv_latent_decode_attention.restype = c_int
     lib.pkv_status_string.argtypes = [c_int]
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error_string.argtypes = []
@@ -715,3 +738,142 @@ def pkv_compact_pages(k_pool, v_pool, page_table, page_refs, page_size: int, num
               stream, _dev_err(dev_err, dev), lib.pkv_compact_pages, desc_p, k, v, table, refs,
               live_p)
     return num_live
+
+
+def _rope_tables(cos, sin, half: int, dev: int):
+    """The addresses of a call's cosines and sines, fp32 [L, half], and L."""
+    _need(cos, "rope_cos", torch.float32, 2)
+    if cos.shape[1] != half:
+        raise ValueError(f"rope tables must be [L, {half}], got {list(cos.shape)}")
+    return (_tensor("rope_cos", cos, torch.float32, cos.shape, dev),
+            _tensor("rope_sin", sin, torch.float32, cos.shape, dev), cos.shape[0])
+
+
+def _strided(name: str, t, dev, shape=None, inner: int = 1) -> int:
+    """The address of a bf16 CUDA tensor whose last dim is contiguous and whose other strides
+    are free (of length-1 dims they do not matter)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or (dev is not None and t.get_device() != dev) or \
+            (shape is not None and t.shape != shape) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        want = "" if shape is None else f" of shape {list(shape)}"
+        raise ValueError(f"{name}: expected a bfloat16 CUDA tensor{want} with a contiguous last dim, "
+                         f"got {t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
+    return t.data_ptr()
+
+
+def pkv_rotate(x, positions, rope_cos, rope_sin, interleaved: bool = False, out=None, dev_err=None,
+               stream=None):
+    """The rotary embedding of x [T, H, dims] bf16, a view of any token and head
+    stride (a slice ``q[..., a:b]`` rotates part of each head), by the fp32 tables
+    [L, dims / 2] at ``positions`` [T]. Pairs are the halves' (x_j, x_{j + dims/2}) or,
+    interleaved, neighbours (x_{2j}, x_{2j+1}). ``out`` is a view like x, x itself for a
+    rotation in place, or None for a new tensor. Returns it."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a tensor [T, H, dims]")
+    x_p = _strided("x", x, None)
+    dev = x.get_device()
+    T, H, dims = x.shape
+    if dims % 2 or dims == 0 or H == 0:
+        raise ValueError("x must be [T, H, dims] with at least one head and an even number of dims")
+    pos = _tensor("positions", positions, torch.int32, (T,), dev)
+    cos, sin, L = _rope_tables(rope_cos, rope_sin, dims // 2, dev)
+    if out is None:
+        out, out_p = _result("out", None, x, dev, stream, (T, H, dims), torch.bfloat16)
+    else:
+        out_p = _strided("out", out, dev, x.shape)
+    _run("pkv_rotate", dev, stream, load_library().pkv_rotate, x_p, x.stride(0), x.stride(1), out_p,
+         out.stride(0), out.stride(1), T, H, dims, int(bool(interleaved)), pos, cos, sin, L,
+         _dev_err(dev_err, dev))
+    return out
+
+
+def latent_cache_desc(pool: torch.Tensor, page_table: torch.Tensor, page_size: int) -> CacheDesc:
+    """The descriptor of a paged cache of shared latents, pool [num_pages * page_size, 576]."""
+    rows, row = pool.shape
+    if page_size <= 0 or rows % page_size:
+        raise ValueError("pool rows must be a multiple of page_size")
+    return CacheDesc(rows // page_size, page_size, 1, row, page_table.shape[0], page_table.shape[1])
+
+
+def _latent_cache(pool, page_table, page_size: int):
+    """Device, descriptor and addresses of a call's latent cache."""
+    _need(pool, "pool", torch.bfloat16, 2)
+    _need(page_table, "page_table", torch.int32, 2)
+    dev = pool.get_device()
+    if page_table.get_device() != dev:
+        raise ValueError(f"page_table: expected a tensor on cuda:{dev}, got {page_table.device}")
+    return dev, latent_cache_desc(pool, page_table, page_size), pool.data_ptr(), page_table.data_ptr()
+
+
+def pkv_latent_append(pool, page_table, x_new, batch_idx, input_pos, page_size: int, rope_cos,
+                      rope_sin, norm_weight=None, norm_eps: float = 1e-6, interleaved: bool = False,
+                      dev_err=None, stream=None) -> None:
+    """Writes new tokens' rows x_new [N, 576] bf16 (a view of any token stride: the latent,
+    then the position part) into the pool [num_pages * page_size, 576] through the page
+    table: the latent normalised with ``norm_weight`` fp32 [512] if given, the position
+    part rotated by the fp32 tables [L, 32] at input_pos [N]."""
+    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
+    if not isinstance(x_new, torch.Tensor) or x_new.dim() != 2 or x_new.shape[1] != LATENT_ROW:
+        raise ValueError(f"x_new must be a tensor [N, {LATENT_ROW}]")
+    x_p = _strided("x_new", x_new, dev)
+    n = x_new.shape[0]
+    b = _tensor("batch_idx", batch_idx, torch.int32, (n,), dev)
+    pos = _tensor("input_pos", input_pos, torch.int32, (n,), dev)
+    cos, sin, L = _rope_tables(rope_cos, rope_sin, LATENT_ROTATED // 2, dev)
+    w = None if norm_weight is None else \
+        _tensor("norm_weight", norm_weight, torch.float32, (LATENT_DIM,), dev)
+    _run("pkv_latent_append", dev, stream, load_library().pkv_latent_append, ctypes.byref(desc),
+         pool_p, table, x_p, x_new.stride(0), b, pos, n, cos, sin, L, int(bool(interleaved)), w,
+         float(norm_eps), _dev_err(dev_err, dev))
+
+
+def pkv_latent_gather(pool, page_table, slots, starts, total: int, page_size: int, out=None,
+                      dev_err=None, stream=None):
+    """The cached rows of sequences, one after another: row starts[b] + t of the result
+    [total, 576] is the row of position t of slot slots[b], t < starts[b + 1] - starts[b].
+    Rows that no sequence covers stay as they were. Returns ``out`` (a new one if None)."""
+    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
+    _need(slots, "slots", torch.int32, 1)
+    n = slots.shape[0]
+    slots_p = _tensor("slots", slots, torch.int32, (n,), dev)
+    starts_p = _tensor("starts", starts, torch.int32, (n + 1,), dev)
+    out, out_p = _result("out", out, pool, dev, stream, (int(total), pool.shape[1]), torch.bfloat16)
+    _run("pkv_latent_gather", dev, stream, load_library().pkv_latent_gather, ctypes.byref(desc), pool_p,
+         table, slots_p, starts_p, n, int(total), out_p, _dev_err(dev_err, dev))
+    return out
+
+
+def pkv_latent_decode_workspace_size(pool, page_table, page_size: int, batch: int, n_q: int,
+                                     num_heads: int) -> int:
+    desc = latent_cache_desc(pool, page_table, page_size)
+    n = load_library().pkv_latent_decode_workspace_size(ctypes.byref(desc), batch, n_q, num_heads)
+    if n == 0:
+        raise PkvError("pkv_latent_decode_workspace_size", 1)
+    return int(n)
+
+
+def pkv_latent_decode_attention(pool, page_table, q, batch_idx, seq_lens, page_size: int,
+                                scale: float, out=None, lse=None, workspace=None, dev_err=None,
+                                stream=None):
+    """Attention of new tokens over a paged cache of shared latents (the absorbed form). q
+    [B, n_q, H, 576] bf16, or [B, H, 576] for one token a row: row b's tokens are the last
+    n_q of the seq_lens[b] positions of slot batch_idx[b], each sees the rows up to its own
+    (appended first). Returns (out [B, n_q, H, 512] bf16, lse [B, n_q, H] fp32), without the
+    n_q axis where q has none."""
+    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4) or q.shape[-1] != desc.head_dim:
+        raise ValueError(f"q must be a tensor [B, n_q, H, {desc.head_dim}] or [B, H, {desc.head_dim}]")
+    q_p = _tensor("q", q, torch.bfloat16, q.shape, dev)
+    B, H = q.shape[0], q.shape[-2]
+    n_q = q.shape[1] if q.dim() == 4 else 1
+    args = (q_p, H, _tensor("batch_idx", batch_idx, torch.int32, (B,), dev),
+            _tensor("seq_lens", seq_lens, torch.int32, (B,), dev), B, n_q, float(scale))
+    out, out_p = _result("out", out, q, dev, stream, (*q.shape[:-1], LATENT_DIM), torch.bfloat16)
+    lse, lse_p = _result("lse", lse, q, dev, stream, q.shape[:-1], torch.float32)
+    lib = load_library()
+    desc_p = ctypes.byref(desc)
+    _run_with(workspace, lambda: lib.pkv_latent_decode_workspace_size(desc_p, B, n_q, H),
+              "pkv_latent_decode_attention", dev, stream, _dev_err(dev_err, dev),
+              lib.pkv_latent_decode_attention, desc_p, pool_p, table, *args, out_p, lse_p)
+    return out, lse
