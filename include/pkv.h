@@ -725,7 +725,7 @@ size_t pkv_latent_decode_workspace_size(const pkv_cache_desc* cache, int batch, 
  * t < e = n - (n_q - 1 - j). With C[t] the row of position t:
  *   lse[b, j, h] = ln sum_{t<e} exp(scale * q[b,j,h] . C[t])                    (fp32)
  *   out[b, j, h] = sum_{t<e} exp(scale * q[b,j,h] . C[t] - lse) C[t][0:512]
- * out: bf16 [batch, n_q, num_heads, 512], 32-byte aligned; lse: fp32 [batch, n_q,
+ * out: bf16 [batch, n_q, num_heads, 512], 16-byte aligned; lse: fp32 [batch, n_q,
  * num_heads]. e <= 0, slot 0 and n = 0 give out 0, lse -inf. Scores, sums and
  * products are held in fp32; the weights exp(..) are rounded to bf16 for the product
  * (their sum takes them unrounded) and out is rounded once. A slot outside [0,

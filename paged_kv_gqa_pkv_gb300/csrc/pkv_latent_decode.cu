@@ -23,12 +23,14 @@
 // of 8 KB in flight: 6.76 TB/s of distinct cache rows, 12.8 TB/s into the SMs; the copy
 // bandwidth is 6.78.) The MMAs of a tile take ~2200-2500 cycles, its bytes ~3300.
 //
-// Roles per CTA: warp 0 loads (TMA through the page table); warp 1 issues the MMAs (of the
-// pair: CTA 0's only); warps 2-5 are softmax and epilogue, lane l and l + 64 sharing row l.
+// Roles per CTA: warps 0 and 6 load (TMA through the page table); warp 1 issues the MMAs (of
+// the pair: CTA 0's only); warps 2-5 are softmax and epilogue, lanes l and l + 64 sharing row l.
 //
-// Work: the tiles of all (sequence, 128-row block) items in a row are cut into equal
-// ranges, one per pair of CTAs; an item that a cut splits leaves unnormalised partials,
-// which a second kernel joins. Cuts close to an item's end move there.
+// Work: where the (sequence, 128-row block) items are no more than the pairs of CTAs, each pair
+// takes one item or an equal part of one; the parts are as short as their number allows, unless
+// whole items are about as short. Else the items' tiles in a row are cut into equal ranges. Parts
+// of an item leave unnormalised partials, which a second kernel joins.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -46,7 +48,8 @@ constexpr int kChunk = 64 * 128;           // [64 rows x 64 values], 128-byte sw
 constexpr int kChunks = kRow / 64;         // 9
 constexpr int kKGroups = 3;                // S's loads and barriers: three chunks at a time
 constexpr int kVGroups = 2;                // PV's: the CTA's dims 0-127 and 128-255
-constexpr int kLatThreads = 6 * 32;
+constexpr int kLatThreads = 7 * 32;
+constexpr int kAhead = 3;                  // tiles whose rows are asked for in L2 ahead
 constexpr int kMaxRowsPerLaunch = 512;     // sequences of one launch
 
 // shared memory, offsets from a 1024-aligned base
@@ -55,8 +58,8 @@ constexpr int kOffK = kOffQ + kChunks * kChunk;       // [9 chunks][64 own keys]
 constexpr int kOffV = kOffK + kChunks * kChunk;       // [2 key halves][4 own chunks][64 keys]
 constexpr int kOffP = kOffV + 8 * kChunk;             // [2 key halves][64 query rows]
 constexpr int kOffBar = kOffP + 2 * kChunk;
-constexpr int kNumBars = 2 * kKGroups + 2 * kVGroups + 7;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;      // tmem slot, abort flag, range
+constexpr int kNumBars = 2 * kKGroups + 2 * kVGroups + 8;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;      // tmem slot, abort flag, first segment
 constexpr int kOffMax = kOffMisc + 32;                // [2][128] row maxima, [128] sums
 constexpr int kLatSmem = kOffMax + 3 * 128 * 4 + 1024;  // + slack for the alignment
 static_assert(kLatSmem <= kMaxDynSmem, "shared memory above the opt-in limit");
@@ -65,7 +68,24 @@ constexpr uint32_t kColS = 256;            // TMEM: O in columns 0-255, S in 256
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, 256, true);
 
+// n / d for 0 <= n < 2^31 as a product: with 2^(l-1) < d <= 2^l and m = floor(2^(31+l) / d) + 1
+// (below 2^32), n m / 2^(31+l) exceeds n / d by less than 1 / d.
+struct Divisor {
+  uint32_t m;
+  int shift;
+  int d;
+};
+inline Divisor make_divisor(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  return {static_cast<uint32_t>((1ull << (31 + l)) / d + 1), 31 + l, d};
+}
+__device__ __forceinline__ int div_by(int n, const Divisor& v) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * v.m) >> v.shift);
+}
+
 struct LatentDecodeParams {
+  const __nv_bfloat16* pool;
   const int32_t* page_table;
   const int32_t* batch_idx;
   const int32_t* seq_lens;
@@ -73,19 +93,20 @@ struct LatentDecodeParams {
   float* lse;              // [batch, n_q * heads]
   float* part_o;           // [2 * workers][block_rows][512]
   float* part_ml;          // [2 * workers][block_rows][2]
+  int4* part_item;         // [workers]: parts of the item that the range ends (0: none), its place
   int32_t* dev_err;
   int batch;
-  int heads;
+  Divisor heads;
   int n_q;
   int rows;                // n_q * heads
-  int row_blocks;          // ceil(rows / 128)
+  Divisor row_blocks;      // ceil(rows / 128)
   int block_rows;          // min(rows, 128): rows of a partial
-  int page_size;
+  Divisor page_size;
   int num_pages;
   int max_batch;
   int max_blocks;
   int box_rows;            // rows of one TMA box: 16, 32 or 64
-  int workers;             // pairs of CTAs
+  Divisor workers;         // pairs of CTAs
   float qscale;            // scale * log2(e)
 };
 
@@ -107,38 +128,26 @@ __device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
+// Arrives on a barrier of either CTA. What the barriers of the pair order is shared memory
+// that its own CTA's threads wrote (behind a proxy fence) or TMA filled, and tensor memory;
+// no thread reads what a thread of the other CTA wrote. So the default, CTA-scope semantics
+// do: a release or acquire at cluster scope waits for the thread's whole memory traffic
+// (arriving took 1000-3400 cycles a tile).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Waits that see what threads of the other CTA released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity,
-                                          volatile int* abort_flag) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-}
-
 // One box of a tiled load whose bytes count on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
                                                  int x, int y, int z) {
@@ -203,117 +212,70 @@ __device__ __forceinline__ bool named_bar_all(int id, int n, bool v) {
   return r != 0;
 }
 
-// 32 bytes to global memory in one instruction: a whole sector per lane.
-__device__ __forceinline__ void st_global_v8(void* a, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // ------------------------------------------------------------------- work --
 
-// Keys of a sequence's last query; 0 for padding and for rows that are refused (*err).
-__device__ __forceinline__ int seq_keys(const LatentDecodeParams& p, int b, int* err) {
+// Keys of a sequence's last query, 0 for padding and for rows that are refused (*err); its slot.
+__device__ __forceinline__ int seq_keys(const LatentDecodeParams& p, int b, int* err, int* slot_out) {
   const int slot = __ldg(p.batch_idx + b);
   const int n = __ldg(p.seq_lens + b);
+  *slot_out = slot;
   *err = 0;
   if (slot == 0) return 0;
   if (slot < 0 || slot >= p.max_batch) *err = PKV_DEV_ERR_BAD_SLOT;
-  else if (n < 0 || n > p.max_blocks * p.page_size) *err = PKV_DEV_ERR_BAD_POS;
+  else if (n < 0 || n > p.max_blocks * p.page_size.d) *err = PKV_DEV_ERR_BAD_POS;
   return *err ? 0 : n;
 }
 __device__ __forceinline__ int key_tiles(int n) {
   return n / kKeys + (n % kKeys != 0);
 }
-
-// The tiles of all items in a row: sequence by sequence, its row blocks one after another.
-// A warp's view: lane l holds the tiles of sequences l * per .. l * per + per - 1.
-struct Flat {
-  long long total;
-  long long before;  // tiles before this lane's sequences
-  long long own;     // tiles of this lane's sequences
-  int per;
-};
-__device__ __forceinline__ Flat flat_load(const LatentDecodeParams& p, int lane) {
-  Flat f;
-  f.per = (p.batch + 31) / 32;
-  f.own = 0;
-  for (int k = 0; k < f.per; ++k) {
-    const int b = lane * f.per + k;
-    int err;
-    if (b < p.batch) f.own += static_cast<long long>(key_tiles(seq_keys(p, b, &err))) * p.row_blocks;
-  }
-  long long incl = f.own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  f.before = incl - f.own;
-  f.total = __shfl_sync(0xffffffffu, incl, 31);
-  return f;
-}
-// The sequence that holds flat tile x (0 <= x < total) and the tiles before it.
-__device__ __forceinline__ void flat_find(const LatentDecodeParams& p, const Flat& f, int lane,
-                                          long long x, int* seq, long long* base) {
-  const bool mine = x >= f.before && x < f.before + f.own;
-  int b = 0;
-  long long at = f.before;
-  if (mine) {
-    for (int k = 0; k < f.per; ++k) {
-      int err;
-      const int s = lane * f.per + k;
-      const long long n = static_cast<long long>(key_tiles(seq_keys(p, s, &err))) * p.row_blocks;
-      if (x < at + n) {
-        b = s;
-        break;
-      }
-      at += n;
-    }
-  }
-  const uint32_t who = __ballot_sync(0xffffffffu, mine);
-  const int src = who ? __ffs(who) - 1 : 0;
-  *seq = __shfl_sync(0xffffffffu, b, src);
-  *base = __shfl_sync(0xffffffffu, at, src);
+// Whether the sequence of n keys ends inside a 16-key step of tile j: rows past its end, which
+// may hold any bits, would take part in PV.
+__device__ __forceinline__ bool ragged(int n, int j) {
+  return n - j * kKeys < kKeys && (n & 15) != 0;
 }
 
-// The cut at flat tile x inside the item [i0, i1): where it is close to one of the item's
-// ends it moves there, which saves a partial result (256 KB written and read again for
-// 128 rows) for a little imbalance.
-__device__ __forceinline__ long long snap_cut(long long x, long long i0, long long i1,
-                                              long long total, int workers) {
-  const long long near = (total / workers + 4) / 8;
-  if (x - i0 <= near && x - i0 <= i1 - x) return i0;
-  if (i1 - x <= near) return i1;
+// The schedule, from the sequences' tiles alone, so that it needs no other kernel's work.
+//
+// Up to as many items as workers: an item of nt tiles is cut into ceil(nt / S) equal parts, for the
+// smallest S (in steps of 1/16) at which all parts find a worker; every worker has one part, loads Q
+// once and has nothing to wait for between items. Where the longest item has at most kWholeSlack
+// tiles more than S nothing is cut at all: partial results are 256 KB each for 128 rows, written,
+// read and joined by a kernel that is otherwise done at once (a cut costs about two tiles' time).
+//
+// More items than workers: the tiles of all items stand in a row (at most 2^30, which the host sees
+// to), sequence by sequence, its row blocks one after another; worker w's range begins at tile
+// w * each + min(w, more). A cut inside an item moves to one of its ends if that is at most
+// kCutReach tiles away, and to the closer one.
+constexpr int kWholeSlack = 1;
+constexpr int kCutReach = 3;
+__device__ __forceinline__ int move_cut(int x, int i0, int i1) {
+  if (x - i0 <= kCutReach && x - i0 <= i1 - x) return i0;
+  if (i1 - x <= kCutReach) return i1;
   return x;
-}
-__device__ __forceinline__ long long raw_cut(long long total, int workers, int w) {
-  return total * w / workers;
 }
 
 // One worker's walk over its range: an item's tiles j0 .. j1 - 1 at a time.
 struct Walk {
-  long long x, end, base;  // base: tiles before sequence b
-  int b;                   // the current segment's sequence
-  int rb, n, nt, j0, j1;   // its row block, keys, tiles, and the range of tiles
+  int x, end;          // flat tiles: behind the current segment, the range's end
+  int b, base, n;      // sequence, the tiles before it, its keys
+  int slot;
+  int rb, nt, j0, j1;  // the segment's row block, tiles of its item, and range of tiles
 };
 __device__ __forceinline__ bool walk_next(const LatentDecodeParams& p, Walk& w) {
   if (w.x >= w.end) return false;
-  long long span;
+#pragma unroll 1
   for (;;) {
-    int err;
-    w.n = seq_keys(p, w.b, &err);
     w.nt = key_tiles(w.n);
-    span = static_cast<long long>(w.nt) * p.row_blocks;
+    const int span = w.nt * p.row_blocks.d;
     if (w.x < w.base + span) break;
     w.base += span;
-    ++w.b;
+    int err;
+    w.n = seq_keys(p, ++w.b, &err, &w.slot);
   }
-  const long long in = w.x - w.base;
-  w.rb = static_cast<int>(in / w.nt);
-  w.j0 = static_cast<int>(in % w.nt);
-  const long long left = w.end - w.x;
-  w.j1 = left < w.nt - w.j0 ? w.j0 + static_cast<int>(left) : w.nt;
+  const int in = w.x - w.base;
+  w.rb = p.row_blocks.d == 1 ? 0 : in / w.nt;
+  w.j0 = in - w.rb * w.nt;
+  w.j1 = min(w.nt, w.j0 + (w.end - w.x));
   w.x += w.j1 - w.j0;
   return true;
 }
@@ -322,25 +284,27 @@ __device__ __forceinline__ bool walk_next(const LatentDecodeParams& p, Walk& w) 
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
-                     const __grid_constant__ CUtensorMap cmap, const LatentDecodeParams p) {
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap,
+                     const LatentDecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* k_full = bars;                    // [3] CTA 0: both CTAs' chunks have landed
   uint64_t* k_empty = k_full + kKGroups;      // [3] both: S has read them
-  uint64_t* v_full = k_empty + kKGroups;      // [2] each CTA its own
+  uint64_t* v_full = k_empty + kKGroups;      // [2] CTA 0: both CTAs' values have landed
   uint64_t* v_empty = v_full + kVGroups;      // [2] both: PV has read them
   uint64_t* q_full = v_empty + kVGroups;      // CTA 0
   uint64_t* q_empty = q_full + 1;             // both: the item's last S is done
   uint64_t* s_full = q_empty + 1;             // [2] both
-  uint64_t* p_full = s_full + 2;              // CTA 0: P and the values of both CTAs are there
+  uint64_t* p_full = s_full + 2;              // CTA 0: both CTAs' P is there
   uint64_t* pv_done = p_full + 1;             // both
   uint64_t* o_free = pv_done + 1;             // CTA 0: both epilogues have read O
+  uint64_t* v_tail = o_free + 1;              // each CTA: the values of a ragged tile
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  long long* s_range = reinterpret_cast<long long*>(smem + kOffMisc + 8);  // x, end
-  int* s_seq = reinterpret_cast<int*>(smem + kOffMisc + 24);
+  int* s_walk = reinterpret_cast<int*>(smem + kOffMisc + 8);  // the first segment
   float* s_max = reinterpret_cast<float*>(smem + kOffMax);
 
   const int warp = threadIdx.x >> 5;
@@ -364,9 +328,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     mbar_init(p_full, 8);   // the four softmax warps of both CTAs
     mbar_init(pv_done, 1);
     mbar_init(o_free, 8);
+    mbar_init(v_tail, 1);
+    *s_abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&cmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -375,114 +342,227 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  if (warp == 0) {
-    const Flat f = flat_load(p, lane);
-    long long cut[2], base = 0;
-    int seq = 0;
-#pragma unroll
-    for (int k = 1; k >= 0; --k) {
-      const long long x = raw_cut(f.total, p.workers, worker + k);
-      cut[k] = x;
-      if (x < f.total) {
-        flat_find(p, f, lane, x, &seq, &base);
-        int err;
-        const int nt = key_tiles(seq_keys(p, seq, &err));
-        const long long i0 = base + (x - base) / nt * nt;
-        cut[k] = snap_cut(x, i0, i0 + nt, f.total, p.workers);
-      }
-    }
-    // (a cut that moved to its item's end is past sequence `seq`: the walk steps on)
-    if (lane == 0) {
-      s_range[0] = cut[0];
-      s_range[1] = cut[1];
-      *s_seq = seq;
-      *reinterpret_cast<long long*>(smem + kOffMax) = base;  // read before any maximum is written
-      *s_abort = (p.dev_err != nullptr &&
-                  (*reinterpret_cast<volatile int32_t*>(p.dev_err) & PKV_DEV_ERR_TIMEOUT))
-                     ? 1
-                     : 0;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk w;
-  w.x = s_range[0];
-  w.end = s_range[1];
-  w.b = *s_seq;
-  w.base = *reinterpret_cast<long long*>(smem + kOffMax);
-  __syncthreads();
+  pdl_wait_primary();
+  pdl_launch_dependents();
 
+  // The schedule: every sequence's keys, in P's place in shared memory (no P is written before
+  // all warps have read what follows); warp 0 finds this pair's range among their tiles and goes
+  // on with its loads while the others read what it found. (What runs once costs mostly the
+  // latency of its instructions: little code, loops not unrolled.)
+  int* keys_of = reinterpret_cast<int*>(smem + kOffP);
+#pragma unroll 1
+  for (int b = threadIdx.x; b < p.batch; b += kLatThreads) {
+    int err;
+    keys_of[b] = seq_keys(p, b, &err, &keys_of[kMaxRowsPerLaunch + b]);
+  }
+  __syncthreads();
   if (warp == 0) {
+    int total = 0, items = 0, most = 0;
+#pragma unroll 1
+    for (int b = lane; b < p.batch; b += 32) {
+      const int nt = key_tiles(keys_of[b]);
+      total += nt;
+      items += nt > 0;
+      most = max(most, nt);
+    }
+    total = __reduce_add_sync(0xffffffffu, total) * p.row_blocks.d;
+    items = __reduce_add_sync(0xffffffffu, items) * p.row_blocks.d;
+    most = __reduce_max_sync(0xffffffffu, most);
+    const int each = div_by(total, p.workers);
+    const int more = total - each * p.workers.d;
+    const bool parts = items <= p.workers.d;
+    int part_len = max(each + (more > 0), 1);
+    if (parts) {
+      for (;; part_len += max(1, part_len >> 4)) {
+        if (most <= part_len + kWholeSlack) {
+          part_len = max(most, 1);
+          break;
+        }
+        int n = 0;
+#pragma unroll 1
+        for (int b = lane; b < p.batch; b += 32)
+          n += (key_tiles(keys_of[b]) + part_len - 1) / part_len;
+        if (__reduce_add_sync(0xffffffffu, n) * p.row_blocks.d <= p.workers.d) break;
+      }
+    }
+    // what the scan counts: parts, or tiles
+    const int x0 = parts ? worker : worker * each + min(worker, more);
+    const int x1 = parts ? worker : x0 + each + (worker < more ? 1 : 0);
+    if (lane == 0) {
+      s_walk[0] = s_walk[1] = parts ? 0 : total;  // (past the last: no work)
+      s_walk[6] = 0;
+    }
+    __syncwarp();
+    int run = 0;
+#pragma unroll 1
+    for (int g = 0; g < p.batch && run <= x1; g += 32) {
+      const int b = g + lane;
+      const int n = b < p.batch ? keys_of[b] : 0;
+      const int nt = key_tiles(n);
+      const int unit = parts ? (nt + part_len - 1) / part_len : nt;
+      const int span = unit * p.row_blocks.d;
+      int incl = span;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int base = run + incl - span;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+      bool first = x0 >= base && x0 < base + span;
+      int walk_base = base;
+      if (parts) {
+        if (first) {
+          const int in = x0 - base;
+          const int rb = in / unit, k = in - rb * unit;
+          const int len = nt / unit, longer = nt - len * unit;  // the first parts are one longer
+          s_walk[0] = rb * nt + k * len + min(k, longer);
+          s_walk[1] = rb * nt + (k + 1) * len + min(k + 1, longer);
+          walk_base = 0;
+          s_walk[6] = k > 0 && k + 1 == unit ? unit : 0;  // ends an item of that many parts
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 1; k >= 0; --k) {
+          const int x = k ? x1 : x0;
+          if (x >= base && x < base + span) {
+            const int i0 = base + (p.row_blocks.d == 1 ? 0 : (x - base) / nt * nt);
+            const int i1 = i0 + nt;
+            const int c = move_cut(x, i0, i1);
+            s_walk[k] = c;
+            if (k == 0 && c > i0 && c < i1 && move_cut(x1, i0, i1) >= i1) {
+              // ends an item that it begins inside: as many workers before it as cuts in the item
+              int u = worker;
+              while (move_cut((u - 1) * each + min(u - 1, more), i0, i1) > i0) --u;
+              s_walk[6] = worker - u + 2;
+            }
+          }
+        }
+      }
+      if (first) {
+        // (a cut that moved to its item's end may lie past the sequence: the walk steps on)
+        s_walk[2] = b;
+        s_walk[3] = walk_base;
+        s_walk[4] = n;
+        s_walk[5] = keys_of[kMaxRowsPerLaunch + b];
+      }
+    }
+    __syncwarp();
+    asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kLatThreads) : "memory");
+  } else {
+    named_bar_sync(2, kLatThreads);
+  }
+  Walk w;
+  w.x = s_walk[0], w.end = s_walk[1], w.b = s_walk[2], w.base = s_walk[3], w.n = s_walk[4];
+  w.slot = s_walk[5];
+  bool more = walk_next(p, w);
+
+  if (warp == 0 || warp == 6) {
     // ---------------------------------------------------- loads ----
+    // Warp 0 brings Q and the keys for S, warp 6 the values for PV: each waits for its own
+    // part of the shared memory only.
+    const bool keys = warp == 0;
     const int R = p.box_rows;
     const int half_boxes = 64 / R;   // boxes of a chunk
     uint32_t tc = 0, items = 0;
-    const uint32_t k_full0 = peer_u32(k_full, 0);
+    const uint32_t full0 = peer_u32(keys ? k_full : v_full, 0);
     const uint32_t q_full0 = peer_u32(q_full, 0);
     bool ok = true;
-    while (ok && walk_next(p, w)) {
-      const int slot = __ldg(p.batch_idx + w.b);
-      const int32_t* table = p.page_table + static_cast<long long>(slot) * p.max_blocks;
-      if (lane == 0) {
-        ok = items == 0 || wait_pair(q_empty, (items - 1) & 1, s_abort);
-        if (ok) {
-          if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kChunks * kChunk);
-          const int row = w.b * p.rows + w.rb * kRows + static_cast<int>(rank) * 64;
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_3d_pair(smem + kOffQ + c * kChunk, &qmap, q_full0, 0, row, c);
+    // Boxes: the rows of a tile that lie in one page, at most 64; warp 0 loads those of this
+    // CTA's half of the keys (`boxes` a tile), warp 6 those of the whole tile. Lane l holds the
+    // pool row of box l % boxes of tile (window's first) + l / boxes.
+    const int boxes = keys ? half_boxes : 2 * half_boxes;
+    const int box_sh = __ffs(boxes) - 1;
+    const int box0 = ((lane & (boxes - 1)) + (keys ? static_cast<int>(rank) * half_boxes : 0)) * R;
+    const int window = 32 >> box_sh;
+    // Where a page holds 64 rows one load brings all chunks of a group (loads of 8 KB one by
+    // one come to 47 bytes a cycle, of 24 KB to 82 on all SMs at once); else a lane issues the
+    // loads of one chunk of one box.
+    const int per = R == 64 ? 1 : keys ? 3 : 2;
+    for (; ok && more; more = walk_next(p, w)) {
+      const int32_t* table = p.page_table + static_cast<long long>(w.slot) * p.max_blocks;
+      if (keys) {
+        if (lane == 0) {
+          ok = items == 0 || wait_or_abort(q_empty, (items - 1) & 1, s_abort);
+          if (ok) {
+            if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kChunks * kChunk);
+            tma_load_3d_pair(smem + kOffQ, &qmap, q_full0, 0,
+                             w.b * p.rows + w.rb * kRows + static_cast<int>(rank) * 64, 0);
+          }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++items;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      ++items;
+      int row = 0;
+#pragma unroll 1
       for (int j = w.j0; ok && j < w.j1; ++j, ++tc) {
-        // lane k < 128 / R: the pool row of box k of the tile; past the last key, and for
-        // an entry without a page, page 0 as filler
-        int row = 0;
-        bool bad = false;
-        if (lane < 2 * half_boxes) {
-          const long long t = static_cast<long long>(j) * kKeys + lane * R;
-          if (t < w.n) {
-            const int blk = static_cast<int>(t) / p.page_size;
-            const int page = __ldg(table + blk);
-            if (page < 0 || page >= p.num_pages) bad = true;
-            else row = page * p.page_size + (static_cast<int>(t) - blk * p.page_size);
+        const int in = (j - w.j0) & (window - 1);
+        if (in == 0) {
+          // a window's pages, all at once; page 0 as filler past the last key, and where an
+          // entry names no page
+          const int tile = j + (lane >> box_sh);
+          const int t = tile * kKeys + box0;
+          row = 0;
+          if (tile < w.j1 && static_cast<uint32_t>(t) < static_cast<uint32_t>(w.n)) {
+            const int block = div_by(t, p.page_size);
+            const int page = __ldg(table + block);
+            if (page < 0 || page >= p.num_pages) set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PAGE);
+            else row = page * p.page_size.d + (t - block * p.page_size.d);
           }
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) set_dev_err(p.dev_err, PKV_DEV_ERR_BAD_PAGE);
-        // this CTA's keys for S: box `lane` of its half, from lane + rank * half_boxes
-        const int krow =
-            __shfl_sync(0xffffffffu, row, (lane + static_cast<int>(rank) * half_boxes) & 31);
-        for (int g = 0; ok && g < kKGroups; ++g) {
-          ok = tc == 0 || wait_pair(&k_empty[g], (tc - 1) & 1, s_abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * 3 * kChunk);
-          __syncwarp();
-          if (lane < half_boxes) {
-#pragma unroll
-            for (int c = 0; c < 3; ++c)
-              tma_load_3d_pair(smem + kOffK + (3 * g + c) * kChunk + lane * R * 128, &cmap,
-                               k_full0 + 8 * g, 0, krow, 3 * g + c);
+        if (keys) {
+          const int src = __shfl_sync(0xffffffffu, row, (in << box_sh) + lane / per);
+          uint8_t* dst = smem + kOffK + (lane % per) * kChunk + (lane / per) * R * 128;
+#pragma unroll 1
+          for (int g = 0; ok && g < kKGroups; ++g) {
+            ok = tc == 0 || wait_or_abort(&k_empty[g], (tc - 1) & 1, s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * 3 * kChunk);
+            __syncwarp();
+            if (lane < per * boxes)
+              tma_load_3d_pair(dst + 3 * g * kChunk, &kmap, full0 + 8 * g, 0, src,
+                               3 * g + lane % per);
           }
-        }
-        for (int g = 0; ok && g < kVGroups; ++g) {
-          ok = tc == 0 || wait_pair(&v_empty[g], (tc - 1) & 1, s_abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[g], 4 * kChunk);
-          __syncwarp();
-          if (lane < 2 * half_boxes) {
-            const int kh = lane / half_boxes;  // which half of the tile's keys
-            uint8_t* dst = smem + kOffV + (kh * 4 + 2 * g) * kChunk + (lane % half_boxes) * R * 128;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              tma_load_3d(dst + c * kChunk, &cmap, &v_full[g], 0, row,
-                          static_cast<int>(rank) * 4 + 2 * g + c);
+          // The rows of a tile come from memory into L2 some tiles before they are loaded: what
+          // shared memory holds in flight (72 KB) does not cover the latency under load.
+          const int ahead = in + kAhead;
+          const int at = lane >> box_sh;
+          if (row > 0 && (at == ahead || (in == 0 && at > 0 && at < ahead)))
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             p.pool + static_cast<long long>(row) * kRow),
+                         "r"(R * kRow * 2)
+                         : "memory");
+        } else {
+          const bool tail = ragged(w.n, j);
+          const uint32_t tail_own = peer_u32(v_tail, rank);
+          const int kh = lane / per >= half_boxes ? 1 : 0;  // which half of the tile's keys
+          const int src = __shfl_sync(0xffffffffu, row, (in << box_sh) + lane / per);
+          uint8_t* dst = smem + kOffV + (kh * 4 + lane % per) * kChunk +
+                         (lane / per - kh * half_boxes) * R * 128;
+#pragma unroll 1
+          for (int g = 0; ok && g < kVGroups; ++g) {
+            ok = tc == 0 || wait_or_abort(&v_empty[g], (tc - 1) & 1, s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // the values of a ragged tile are announced to this CTA's softmax warps, which zero
+            // the rows past its end, all others to the pair's MMA warp
+            if (lane == 0) {
+              if (tail) {
+                if (g == 0) mbar_arrive_expect_tx(v_tail, 8 * kChunk);
+              } else if (rank == 0) {
+                mbar_arrive_expect_tx(&v_full[g], 2 * 4 * kChunk);
+              }
+            }
+            __syncwarp();
+            if (lane < per * boxes)
+              tma_load_3d_pair(dst + 2 * g * kChunk, &vmap, tail ? tail_own : full0 + 8 * g, 0, src,
+                               static_cast<int>(rank) * 4 + 2 * g + lane % per);
           }
         }
       }
@@ -490,78 +570,115 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp == 1) {
     // ----------------------------------------------------- MMAs ----
-    if (rank == 0) {
+    // Two streams of products share the tensor pipe: S of the tiles, three chunks of the
+    // keys at a time, and PV. Whichever is ready is issued, PV first: S waits for rows from
+    // memory, and P for a softmax, and neither should hold up the other.
+    if (rank == 1) {
+      // The other CTA's warp issues for both. This one notes for the join whether the worker's
+      // range ends an item of several parts, and writes the rows of sequences without keys.
+      if (lane == 0) {
+        p.part_item[worker] = make_int4(s_walk[6], w.b, w.rb, 0);
+      }
+#pragma unroll 1
+      for (int b = worker; b < p.batch; b += p.workers.d) {
+        int err, slot;
+        if (seq_keys(p, b, &err, &slot) > 0) continue;
+        if (err && lane == 0) set_dev_err(p.dev_err, err);
+        const long long at = static_cast<long long>(b) * p.rows;
+        uint4* o = reinterpret_cast<uint4*>(p.out + at * kLatent);
+        for (long long e = lane; e < static_cast<long long>(p.rows) * (kLatent / 8); e += 32)
+          o[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = lane; e < p.rows; e += 32) p.lse[at + e] = -INFINITY;
+      }
+    } else if (elect_one()) {
       const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ), 0);
       const uint32_t k_lo = desc_lo(smem_u32(smem + kOffK), 0);
       const uint32_t p_lo = desc_lo(smem_u32(smem + kOffP), 0);
       const uint32_t v_lo = desc_lo(smem_u32(smem + kOffV), kChunk);
-      uint32_t tc = 0, items = 0;  // tiles whose PV has been issued; items begun
-      bool ok = true;
-      auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_pair(bar, parity, s_abort));
-      };
-      // S of tile number t: Q C^T into buffer t & 1
-      auto issue_s = [&](uint32_t t, bool last) -> bool {
-#pragma unroll 1
-        for (int g = 0; g < kKGroups; ++g) {
-          if (!wait_w(&k_full[g], t & 1)) return false;
+      Walk ws = w;                           // S's segment
+      bool s_more = more, p_more = more;
+      uint32_t ts = 0, s_items = 0;          // S's tile, items begun
+      uint32_t tp = 0, p_items = 0, fv = 0;  // PV's; tiles whose values v_full announced
+      int sj = ws.j0, pj = w.j0, sg = 0, pg = 0;
+      bool q_there = false, p_there = false;
+      uint64_t t0 = 0;
+      uint32_t idle = 0;
+      while (p_more) {
+        // P of tile tp (before an item's first PV both epilogues have read the last item's O)
+        if (!p_there)
+          p_there = mbar_test(p_full, tp & 1) &&
+                    (pj > w.j0 || p_items == 0 || mbar_test(o_free, (p_items - 1) & 1));
+        const bool tail = ragged(w.n, pj);
+        if (p_there && (tail || mbar_test(&v_full[pg], fv & 1))) {
           tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int c = 0; c < 3; ++c)
-              umma4_pair<32, 32>(tmem + kColS + 64 * (t & 1),
-                                 q_lo + (((3 * g + c) * kChunk) >> 4),
-                                 k_lo + (((3 * g + c) * kChunk) >> 4), kIdescS,
-                                 g + c > 0 ? 1u : 0u);
-            commit_pair(&k_empty[g]);
-            if (g == kKGroups - 1) {
-              commit_pair(&s_full[t & 1]);
-              if (last) commit_pair(q_empty);
-            }
-          }
-          __syncwarp();
-        }
-        return true;
-      };
-      while (ok && walk_next(p, w)) {
-        const int nt = w.j1 - w.j0;
-        ok = wait_w(q_full, items & 1) && issue_s(tc, nt == 1);
-        for (int i = 0; ok && i < nt; ++i) {
-          if (i + 1 < nt) ok = issue_s(tc + 1, i + 2 == nt);
-          ok = ok && wait_w(p_full, tc & 1);
-          if (ok && i == 0 && items > 0) ok = wait_w(o_free, (items - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const int left = w.n - (w.j0 + i) * kKeys;
+          const int left = w.n - pj * kKeys;
           const int steps = left >= kKeys ? 8 : (left + 15) >> 4;  // of 16 keys
-          if (elect_one()) {
+          const uint32_t b = v_lo + ((2 * pg * kChunk) >> 4);
+          const uint32_t acc = pj > w.j0 ? 1u : 0u;
+          const uint32_t d = tmem + 128 * pg;
+          if (steps == 8) {
+            umma4_pair<32, 2048>(d, p_lo, b, kIdescO, acc);
+            umma4_pair<32, 2048>(d, p_lo + (kChunk >> 4), b + ((4 * kChunk) >> 4), kIdescO, 1u);
+          } else {
 #pragma unroll 1
-            for (int g = 0; g < kVGroups; ++g) {
-              const uint32_t vg = v_lo + ((2 * g * kChunk) >> 4);
-#pragma unroll 1
-              for (int kh = 0; kh < 2; ++kh) {
-                const uint32_t a = p_lo + ((kh * kChunk) >> 4);
-                const uint32_t b = vg + ((kh * 4 * kChunk) >> 4);
-                const uint32_t acc = (i > 0 || kh > 0) ? 1u : 0u;
-                const int n = steps - 4 * kh;
-                if (n >= 4) {
-                  umma4_pair<32, 2048>(tmem + 128 * g, a, b, kIdescO, acc);
-                } else {
-                  for (int k = 0; k < n; ++k)
-                    umma1_pair(tmem + 128 * g, a + 2 * k, b + 128 * k, kIdescO,
-                               acc | (k > 0 ? 1u : 0u));
-                }
-              }
-              commit_pair(&v_empty[g]);
+            for (int k = 0; k < steps; ++k) {
+              const int kh = k >> 2, ks = k & 3;
+              umma1_pair(d, p_lo + ((kh * kChunk) >> 4) + 2 * ks,
+                         b + ((kh * 4 * kChunk) >> 4) + 128 * ks, kIdescO,
+                         acc | (k > 0 ? 1u : 0u));
             }
-            commit_pair(pv_done);
           }
-          __syncwarp();
-          ++tc;
+          commit_pair(&v_empty[pg]);
+          if (++pg == kVGroups) {
+            commit_pair(pv_done);
+            pg = 0;
+            p_there = false;
+            ++tp;
+            if (!tail) ++fv;
+            if (++pj == w.j1) {
+              ++p_items;
+              p_more = walk_next(p, w);
+              pj = w.j0;
+            }
+          }
+          idle = 0;
+          continue;
         }
-        ++items;
+        // S of tile ts goes into buffer ts & 1, which P of tile ts - 2 has been read from
+        bool s = s_more && ts <= tp + 1;
+        if (s) {
+          if (!q_there) q_there = mbar_test(q_full, s_items & 1);
+          s = q_there && mbar_test(&k_full[sg], ts & 1);
+        }
+        if (s) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            umma4_pair<32, 32>(tmem + kColS + 64 * (ts & 1), q_lo + (((3 * sg + c) * kChunk) >> 4),
+                               k_lo + (((3 * sg + c) * kChunk) >> 4), kIdescS,
+                               sg + c > 0 ? 1u : 0u);
+          commit_pair(&k_empty[sg]);
+          if (++sg == kKGroups) {
+            commit_pair(&s_full[ts & 1]);
+            sg = 0;
+            ++ts;
+            if (++sj == ws.j1) {
+              commit_pair(q_empty);
+              ++s_items;
+              q_there = false;
+              s_more = walk_next(p, ws);
+              sj = ws.j0;
+            }
+          }
+          idle = 0;
+          continue;
+        }
+        if (idle++ == 0) t0 = global_timer_ns();
+        if ((idle & 63u) == 0 && (*s_abort || global_timer_ns() - t0 > kWaitLimitNs)) {
+          *s_abort = 1;
+          break;
+        }
       }
-      if (!ok && lane == 0) *s_abort = 1;
     }
   } else {
     // ---------------------------------------- softmax and epilogue ----
@@ -572,21 +689,21 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t p_full0 = peer_u32(p_full, 0);
     const uint32_t o_free0 = peer_u32(o_free, 0);
     uint8_t* prow = smem + kOffP + hk * kChunk + r * 128;
-    uint32_t tc = 0;
+    uint32_t tc = 0, tails = 0;
     bool ok = true;
-    while (ok && walk_next(p, w)) {
+    for (; ok && more; more = walk_next(p, w)) {
       const int row = w.rb * kRows + static_cast<int>(rank) * 64 + r;  // row of the sequence
       const bool live = row < p.rows;
       const bool warp_live = __any_sync(0xffffffffu, live);
       // keys that the row sees: all but those of the drafts behind its token
-      const int lim = live ? w.n - (p.n_q - 1 - row / p.heads) : 0;
+      const int lim = live ? w.n - (p.n_q - 1 - div_by(row, p.heads)) : 0;
       float m_run = -INFINITY;  // running maximum of the row, raw score units
       float l_run = 0.f;        // sum over this thread's half of the keys
       bool left_together = false;
       for (int j = w.j0; j < w.j1; ++j, ++tc) {
         // a wait that gave up is told to the other warps at their next common barrier, so
         // that all four leave at the same place
-        ok = ok && wait_pair(&s_full[tc & 1], (tc >> 1) & 1, s_abort);
+        ok = ok && wait_or_abort(&s_full[tc & 1], (tc >> 1) & 1, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         uint32_t s[64];
@@ -660,10 +777,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         l_run = l_run * alpha + psum;
         m_run = m_use;
-        // the values of both halves have landed here; P and O are free once the last PV is done
-        ok = wait_or_abort(&v_full[0], tc & 1, s_abort) &&
-             wait_or_abort(&v_full[1], tc & 1, s_abort) &&
-             (tc == 0 || wait_pair(pv_done, (tc - 1) & 1, s_abort));
+        // P and O are free once the last PV is done
+        ok = tc == 0 || wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc_fence_after();
@@ -687,11 +802,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         // values of rows past the last key may hold any bits: their weights are 0, but
         // 0 * NaN is not, so the rows that share a 16-key step with live ones are zeroed
-        const int left = w.n - j * kKeys;
-        if (left < kKeys && (left & 15)) {
-          const int z0 = left, nz = 16 - (left & 15);
-          for (int q = tl; q < nz * 32; q += 128) {
-            const int key = z0 + (q >> 5);
+        if (ragged(w.n, j)) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(v_tail, tails & 1, s_abort));
+          ++tails;
+          if (!ok) continue;
+          const int left = w.n - j * kKeys;
+          for (int q = tl; q < (16 - (left & 15)) * 32; q += 128) {
+            const int key = left + (q >> 5);
             uint8_t* at = smem + kOffV + ((key >> 6) * 4 + ((q >> 3) & 3)) * kChunk +
                           (key & 63) * 128 + (q & 7) * 16;
             *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
@@ -704,7 +821,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       }
       // ---- the segment's end: O and the row's maximum and sum ----
       if (left_together) break;
-      ok = ok && wait_pair(pv_done, (tc - 1) & 1, s_abort);
+      ok = ok && wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
       float* const sums = s_max + 256;
       sums[tl] = l_run;
       ok = named_bar_all(1, 128, ok);
@@ -712,52 +829,85 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       if (ok) {
         const float l = l_run + sums[tl ^ 64];
         const bool whole = w.j0 == 0 && w.j1 == w.nt;
-        if (warp_live) {
-          if (whole) {
-            const bool has = live && l > 0.f;
-            const float inv = has ? 1.f / l : 0.f;
-            const long long at = static_cast<long long>(w.b) * p.rows + row;
-            __nv_bfloat16* orow = p.out + at * kLatent + hk * 256;
+        const int first = w.rb * kRows + static_cast<int>(rank) * 64;  // row of this CTA's row 0
+        const int live_rows = min(64, p.rows - first);
+        if (live_rows > 0) {
+          const bool has = live && l > 0.f;
+          const float inv = has ? 1.f / l : 0.f;
+          const long long at = static_cast<long long>(w.b) * p.rows + first;
+          const int part = 2 * worker + (w.j0 == 0 ? 1 : 0);
+          const long long pat = static_cast<long long>(part) * p.block_rows + (first - w.rb * kRows);
+          if (live && hk == 0) {
+            if (whole) {
+              p.lse[at + r] =
+                  has ? (m_run * p.qscale + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            } else {
+              p.part_ml[2 * (pat + r)] = m_run;
+              p.part_ml[2 * (pat + r) + 1] = l;
+            }
+          }
+          // Through shared memory, 128 bytes of each half row a round (64 values of the result, 32
+          // of a partial), so that stores fill whole lines. Each half's two warps stage and store
+          // for themselves: a round at a time in P's place, or, where the worker is done, all
+          // rounds in Q's and the keys'.
+          const bool last = w.x >= w.end;
+          uint8_t* stage = smem + (last ? kOffQ : kOffP) + hk * kChunk;
+          const int rounds = whole ? 4 : 8;
+          const long long row_bytes = kLatent * (whole ? 2 : 4);
+          uint8_t* dst = (whole ? reinterpret_cast<uint8_t*>(p.out) + at * row_bytes
+                                : reinterpret_cast<uint8_t*>(p.part_o) + pat * row_bytes) +
+                         hk * (row_bytes / 2);
+          const int per = last ? rounds : 1;  // rounds staged side by side
 #pragma unroll 1
-            for (int q = 0; q < 256; q += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_lane + q, o);
-              tmem_wait_ld();
-              if (live) {
+          for (int rd = 0; rd < rounds; ++rd) {
+            uint8_t* st = stage + (last ? rd * 2 * kChunk : 0);
+            if (warp_live) {
+              uint32_t v[32];
+              if (whole) {
+                uint32_t a[64];
+                tmem_ld32(t_lane + 64 * rd, *reinterpret_cast<uint32_t(*)[32]>(&a[0]));
+                tmem_ld32(t_lane + 64 * rd + 32, *reinterpret_cast<uint32_t(*)[32]>(&a[32]));
+                tmem_wait_ld();
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                  uint32_t wv[8];
+                for (int e = 0; e < 32; ++e)
+                  v[e] = has ? pack_bf16x2(__uint_as_float(a[2 * e]) * inv,
+                                           __uint_as_float(a[2 * e + 1]) * inv)
+                             : 0u;
+              } else {
+                tmem_ld32(t_lane + 32 * rd, v);
+                tmem_wait_ld();
+              }
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const float a = __uint_as_float(o[16 * v + 2 * e]) * inv;
-                    const float b = __uint_as_float(o[16 * v + 2 * e + 1]) * inv;
-                    wv[e] = has ? pack_bf16x2(a, b) : 0u;
-                  }
-                  st_global_v8(orow + q + 16 * v, wv);
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(st + r * 128 + ((c ^ (r & 7)) << 4)) =
+                    make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            }
+            if (rd + 1 < rounds && last) continue;
+            named_bar_sync(3 + hk, 64);
+            // 16-byte pieces: eight neighbouring lanes store the 128 bytes of a row and round
+            const int c = r & 7;
+            uint8_t* const to = dst + (rd + 1 - per) * 128 + c * 16;
+#pragma unroll 1
+            for (int i0 = r >> 3; i0 < live_rows; i0 += 16) {
+#pragma unroll 1
+              for (int k = 0; k < per; k += 4) {
+                uint4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int sr = i0 + 8 * (i >> 2), kk = k + (i & 3);
+                  if (kk < per)
+                    x[i] = *reinterpret_cast<const uint4*>(stage + kk * 2 * kChunk + sr * 128 +
+                                                           ((c ^ (sr & 7)) << 4));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int sr = i0 + 8 * (i >> 2), kk = k + (i & 3);
+                  if (kk < per && sr < live_rows)
+                    *reinterpret_cast<uint4*>(to + sr * row_bytes + kk * 128) = x[i];
                 }
               }
             }
-            if (live && hk == 0)
-              p.lse[at] = has ? (m_run * p.qscale + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-          } else {
-            const int part = 2 * worker + (w.j0 == 0 ? 1 : 0);
-            const long long at = static_cast<long long>(part) * p.block_rows + (row - w.rb * kRows);
-            float* orow = p.part_o + at * kLatent + hk * 256;
-#pragma unroll 1
-            for (int q = 0; q < 256; q += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_lane + q, o);
-              tmem_wait_ld();
-              if (live) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  st_global_v8(orow + q + 8 * v, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * v]));
-              }
-            }
-            if (live && hk == 0) {
-              p.part_ml[2 * at] = m_run;
-              p.part_ml[2 * at + 1] = l;
-            }
+            if (!last) named_bar_sync(3 + hk, 64);  // the place may be written again
           }
         }
         tc_fence_before();
@@ -785,112 +935,142 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-// Joins the partials of split items, and writes the rows of sequences without keys. A warp
-// takes one row: 16 of its 512 values a lane, the partials one after another (their loads do
-// not depend on each other), with weights 2^(m_i - max m) and the sum of the l_i.
-constexpr int kJoinWarps = 8;
+// Joins the partials of split items: those of the worker whose range ends the item and of the
+// parts - 1 workers before it, the first of which left the partial of its last segment, the others
+// that of their first. Weights are 2^(m_i - max m), their sum that of the l_i. The warps of the
+// grid share the rows of all these items, where they are many enough a whole row each, else a
+// quarter.
+constexpr int kJoinWarps = 4;
 
-__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentDecodeParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int groups = (p.block_rows + kJoinWarps - 1) / kJoinWarps;
-  const int item = blockIdx.x / groups;
-  const int row_in = (blockIdx.x - item * groups) * kJoinWarps + (threadIdx.x >> 5);
-  const int b = item / p.row_blocks;
-  const int rb = item - b * p.row_blocks;
-  const int row = rb * kRows + row_in;
-  if (row_in >= p.block_rows || row >= p.rows) return;
-  int err;
-  const int n = seq_keys(p, b, &err);
-  const long long at = static_cast<long long>(b) * p.rows + row;
-  uint4* orow = reinterpret_cast<uint4*>(p.out + at * kLatent) + 2 * lane;
-  if (n == 0) {
-    if (err && lane == 0) set_dev_err(p.dev_err, err);
-    orow[0] = make_uint4(0u, 0u, 0u, 0u);
-    orow[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) p.lse[at] = -INFINITY;
-    return;
-  }
-  const Flat f = flat_load(p, lane);
-  // tiles before sequence b
-  long long base = 0;
-  {
-    const int owner = b / f.per;
-    long long v = f.before;
-    if (lane == owner) {
-      for (int s = owner * f.per; s < b; ++s) {
-        int e;
-        v += static_cast<long long>(key_tiles(seq_keys(p, s, &e))) * p.row_blocks;
+template <int kSplit>
+__device__ __forceinline__ void join_row(const LatentDecodeParams& p, const int4& item, int worker,
+                                         int row_in, int split, int lane) {
+  const int row = item.z * kRows + row_in;
+  if (row >= p.rows) return;
+  constexpr int kVecs = 4 / kSplit;  // 16-byte pieces of a lane
+  const int piece = split * (128 / kSplit) + lane;
+  float m = -INFINITY, l = 0.f;
+  float4 o[kVecs];
+#pragma unroll
+  for (int e = 0; e < kVecs; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int done = 0; done < item.x; done += 32) {
+    // 32 parts at a time, from the last down: lane i looks at that of worker u
+    const int n = min(32, item.x - done);
+    const int u = worker - done - lane;
+    const int part = 2 * u + (done + lane == item.x - 1 ? 1 : 0);
+    const long long pr = static_cast<long long>(part) * p.block_rows + row_in;
+    const float mi = lane < n ? __ldcg(p.part_ml + 2 * pr) : -INFINITY;
+    const float li = lane < n ? __ldcg(p.part_ml + 2 * pr + 1) : 0.f;
+    float mx = mi;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float mn = fmaxf(m, mx);
+    // (a range none of whose keys the row sees adds nothing)
+    const float take = mi == -INFINITY ? 0.f : ex2((mi - mn) * p.qscale);
+    const float keep = m == -INFINITY ? 0.f : ex2((m - mn) * p.qscale);
+    float ls = take * li;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    l = l * keep + ls;
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int pi = __shfl_sync(0xffffffffu, part, i);
+      const float t = __shfl_sync(0xffffffffu, take, i);
+      const float4* src = reinterpret_cast<const float4*>(
+          p.part_o + (static_cast<long long>(pi) * p.block_rows + row_in) * kLatent);
+      float4 v[kVecs];
+#pragma unroll
+      for (int e = 0; e < kVecs; ++e) v[e] = __ldcg(src + piece + 32 * e);
+      if (t > 0.f) {
+#pragma unroll
+        for (int e = 0; e < kVecs; ++e) {
+          o[e].x = fmaf(v[e].x, t, o[e].x);
+          o[e].y = fmaf(v[e].y, t, o[e].y);
+          o[e].z = fmaf(v[e].z, t, o[e].z);
+          o[e].w = fmaf(v[e].w, t, o[e].w);
+        }
       }
     }
-    base = __shfl_sync(0xffffffffu, v, owner);
-  }
-  const int nt = key_tiles(n);
-  const long long i0 = base + static_cast<long long>(rb) * nt, i1 = i0 + nt;
-  // the first worker whose range begins inside the item
-  int wf = static_cast<int>(i0 * p.workers / f.total);
-  auto cut = [&](int wk) -> long long {  // of a worker whose raw cut may lie outside: i0 or i1
-    const long long x = raw_cut(f.total, p.workers, wk);
-    if (x <= i0) return i0;
-    if (x >= i1) return i1;
-    return snap_cut(x, i0, i1, f.total, p.workers);
-  };
-  while (wf < p.workers && cut(wf) <= i0) ++wf;
-  if (wf >= p.workers || cut(wf) >= i1) return;  // one worker has the whole item
-  // partials: worker wf - 1's last one, then those of the workers that begin inside
-  float m = -INFINITY, l = 0.f;
-  float o[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) o[e] = 0.f;
-  auto add = [&](int part) {
-    const long long pr = static_cast<long long>(part) * p.block_rows + row_in;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + pr * kLatent) + 4 * lane;
-    const float4 v[4] = {src[0], src[1], src[2], src[3]};
-    const float mi = p.part_ml[2 * pr], li = p.part_ml[2 * pr + 1];
-    if (mi == -INFINITY) return;  // no key of this range is seen by the row
-    const float mn = fmaxf(m, mi);
-    const float keep = ex2((m - mn) * p.qscale), take = ex2((mi - mn) * p.qscale);
-    l = l * keep + li * take;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[4 * e] = o[4 * e] * keep + v[e].x * take;
-      o[4 * e + 1] = o[4 * e + 1] * keep + v[e].y * take;
-      o[4 * e + 2] = o[4 * e + 2] * keep + v[e].z * take;
-      o[4 * e + 3] = o[4 * e + 3] * keep + v[e].w * take;
-    }
     m = mn;
-  };
-  add(2 * (wf - 1) + 1);
-  for (int wk = wf; wk < p.workers; ++wk) {
-    const long long c = cut(wk);
-    if (c >= i1) break;
-    if (wk + 1 < p.workers && cut(wk + 1) == c) continue;  // an empty range
-    add(2 * wk);
   }
   const bool has = l > 0.f;
   const float inv = has ? 1.f / l : 0.f;
-  uint32_t wv[8];
+  const long long at = static_cast<long long>(item.y) * p.rows + row;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) wv[e] = has ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-  orow[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-  orow[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
-  if (lane == 0)
+  for (int e = 0; e < kVecs; ++e)
+    reinterpret_cast<uint2*>(p.out + at * kLatent)[piece + 32 * e] =
+        has ? make_uint2(pack_bf16x2(o[e].x * inv, o[e].y * inv),
+                         pack_bf16x2(o[e].z * inv, o[e].w * inv))
+            : make_uint2(0u, 0u);
+  if (lane == 0 && split == 0)
     p.lse[at] = has ? (m * p.qscale + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentDecodeParams p) {
+  constexpr int kMaxWorkers = 128;
+  __shared__ int4 s_item[kMaxWorkers];
+  __shared__ int s_worker[kMaxWorkers];
+  __shared__ int s_count;
+  const int lane = threadIdx.x & 31;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  // the items of several parts, in order of the workers that end them
+  if (threadIdx.x < 32) {
+    int count = 0;
+    int4 item[kMaxWorkers / 32];
+#pragma unroll
+    for (int k = 0; k < kMaxWorkers / 32; ++k) {
+      const int w = k * 32 + lane;
+      item[k] = w < p.workers.d ? __ldcg(p.part_item + w) : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxWorkers / 32; ++k) {
+      const uint32_t has = __ballot_sync(0xffffffffu, item[k].x > 0);
+      if (item[k].x > 0) {
+        const int at = count + __popc(has & ((1u << lane) - 1u));
+        s_item[at] = item[k];
+        s_worker[at] = k * 32 + lane;
+      }
+      count += __popc(has);
+    }
+    if (lane == 0) s_count = count;
+  }
+  __syncthreads();
+  const int count = s_count;
+  const int warps = gridDim.x * kJoinWarps;
+  const int id = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int rows = count * p.block_rows;
+  if (rows * 4 <= warps) {
+    if (id < rows * 4) {
+      const int i = (id >> 2) / p.block_rows;
+      join_row<4>(p, s_item[i], s_worker[i], (id >> 2) - i * p.block_rows, id & 3, lane);
+    }
+  } else {
+#pragma unroll 1
+    for (int u = id; u < rows; u += warps) {
+      const int i = u / p.block_rows;
+      join_row<1>(p, s_item[i], s_worker[i], u - i * p.block_rows, 0, lane);
+    }
+  }
 }
 
 namespace {
 
-// {64 values, rows, 9 chunks} view of an array of rows of 576; one box is `box_rows` rows of
-// one chunk, 128-byte swizzled.
-bool encode_rows_map(CUtensorMap* map, const void* base, long long rows, int box_rows) {
+// {64 values, rows, 9 chunks} view of an array of rows of 576; a box is `box_rows` rows of
+// `box_chunks` chunks, 128-byte swizzled.
+bool encode_rows_map(CUtensorMap* map, const void* base, long long rows, int box_rows,
+                     int box_chunks) {
   prefill_host::EncodeTiledFn enc = prefill_host::encode_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(rows), kChunks};
   const cuuint64_t strides[2] = {kRow * 2, 128u};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_chunks)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -902,20 +1082,26 @@ bool latent_rows_ok(int batch, int n_q, int heads) {
   return batch >= 0 && n_q >= 1 && n_q <= kMaxQueries && heads >= 1 && heads <= kMaxHeads &&
          static_cast<long long>(batch) * n_q * heads <= INT_MAX;
 }
-int launch_batch(int batch) {
-  const int launches = (batch + kMaxRowsPerLaunch - 1) / kMaxRowsPerLaunch;
-  return launches > 0 ? (batch + launches - 1) / launches : 0;
+// The most tiles that one sequence can have.
+long long seq_tiles(const pkv_cache_desc* c, int rows) {
+  return (static_cast<long long>(c->max_blocks) * c->page_size + kKeys - 1) / kKeys *
+         ((rows + kRows - 1) / kRows);
+}
+// Rows of one launch: equal launches of at most 512 rows and 2^30 tiles. 0: one row has more.
+int launch_batch(const pkv_cache_desc* c, int batch, int rows) {
+  const long long most = std::min<long long>(kMaxRowsPerLaunch, (1ll << 30) / seq_tiles(c, rows));
+  if (most == 0) return 0;
+  const long long launches = (batch + most - 1) / most;
+  return static_cast<int>(launches > 0 ? (batch + launches - 1) / launches : 1);
 }
 // Pairs of CTAs of a launch, and the bytes of its partials.
 int launch_workers(const pkv_cache_desc* c, int batch, int rows, int sm_count) {
-  const long long blocks = (static_cast<long long>(c->max_blocks) * c->page_size + kKeys - 1) / kKeys;
-  const long long tiles = blocks * batch * ((rows + kRows - 1) / kRows);
-  const int pairs = sm_count / 2;
-  return tiles < pairs ? static_cast<int>(tiles) : pairs;
+  return static_cast<int>(std::min<long long>(seq_tiles(c, rows) * batch, std::min(sm_count / 2, 128)));
 }
 size_t partial_bytes(int workers, int rows) {
   const size_t block_rows = rows < kRows ? rows : kRows;
-  return static_cast<size_t>(2 * workers) * block_rows * (kLatent + 2) * sizeof(float);
+  return static_cast<size_t>(workers) *
+         (2 * block_rows * (kLatent + 2) * sizeof(float) + sizeof(int4));
 }
 
 }  // namespace
@@ -930,7 +1116,9 @@ extern "C" size_t pkv_latent_decode_workspace_size(const pkv_cache_desc* cache, 
   int sms = 0;
   if (device_info(&sms) != PKV_OK) return 0;
   const int rows = n_q * num_heads;
-  const size_t n = partial_bytes(launch_workers(cache, launch_batch(batch), rows, sms), rows);
+  const int per = launch_batch(cache, batch, rows);
+  if (per == 0) return 0;
+  const size_t n = partial_bytes(launch_workers(cache, per, rows, sms), rows);
   return n < 256 ? 256 : n;
 }
 
@@ -946,20 +1134,23 @@ extern "C" pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, c
     return PKV_ERR_ARG;
   if (batch == 0) return PKV_OK;
   if (!pool || !page_table || !q || !batch_idx || !seq_lens || !out || !lse) return PKV_ERR_ARG;
-  if (!is_aligned(pool, 16) || !is_aligned(q, 16) || !is_aligned(out, 32) || !is_aligned(lse, 4) ||
+  if (!is_aligned(pool, 16) || !is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) ||
       !is_aligned(page_table, 4) || !is_aligned(batch_idx, 4) || !is_aligned(seq_lens, 4) ||
       !is_aligned(dev_err, 4) || !is_aligned(workspace, 256))
     return PKV_ERR_ALIGN;
   int sms = 0;
   if (const pkv_status st = device_info(&sms); st != PKV_OK) return st;
   const int rows = n_q * num_heads;
-  const int per = launch_batch(batch);
+  const int per = launch_batch(cache, batch, rows);
+  if (per == 0) return PKV_ERR_ARG;
   const int workers = launch_workers(cache, per, rows, sms);
   if (!workspace || workspace_bytes < partial_bytes(workers, rows)) return PKV_ERR_WORKSPACE;
   int box = 64;
   while (cache->page_size % box) box >>= 1;  // 16, 32 or 64
-  CUtensorMap cmap;
-  if (!encode_rows_map(&cmap, pool, static_cast<long long>(cache->num_pages) * cache->page_size, box))
+  const long long pool_rows = static_cast<long long>(cache->num_pages) * cache->page_size;
+  CUtensorMap kmap, vmap;
+  if (!encode_rows_map(&kmap, pool, pool_rows, box, box == 64 ? 3 : 1) ||
+      !encode_rows_map(&vmap, pool, pool_rows, box, box == 64 ? 2 : 1))
     return PKV_ERR_ARG;
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return record_cuda_status(e);
@@ -972,14 +1163,15 @@ extern "C" pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, c
     attr_set[dev].store(true, std::memory_order_release);
   }
   LatentDecodeParams p;
+  p.pool = static_cast<const __nv_bfloat16*>(pool);
   p.page_table = page_table;
   p.dev_err = dev_err;
-  p.heads = num_heads;
+  p.heads = make_divisor(num_heads);
   p.n_q = n_q;
   p.rows = rows;
-  p.row_blocks = (rows + kRows - 1) / kRows;
+  p.row_blocks = make_divisor((rows + kRows - 1) / kRows);
   p.block_rows = rows < kRows ? rows : kRows;
-  p.page_size = cache->page_size;
+  p.page_size = make_divisor(cache->page_size);
   p.num_pages = cache->num_pages;
   p.max_batch = cache->max_batch;
   p.max_blocks = cache->max_blocks;
@@ -989,23 +1181,24 @@ extern "C" pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, c
     const int n = batch - b0 < per ? batch - b0 : per;
     const long long first = static_cast<long long>(b0) * rows;
     const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(q) + first * kRow;
-    CUtensorMap qmap;
-    if (!encode_rows_map(&qmap, q0, static_cast<long long>(n) * rows, 64)) return PKV_ERR_ARG;
     p.batch_idx = batch_idx + b0;
     p.seq_lens = seq_lens + b0;
     p.out = static_cast<__nv_bfloat16*>(out) + first * kLatent;
     p.lse = lse + first;
     p.batch = n;
-    p.workers = launch_workers(cache, n, rows, sms);
+    const int w = launch_workers(cache, n, rows, sms);
+    p.workers = make_divisor(w);
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o + static_cast<size_t>(2 * p.workers) * p.block_rows * kLatent;
-    cudaError_t e = launch_kernel(latent_decode_kernel, dim3(2 * p.workers), dim3(kLatThreads),
-                                  kLatSmem, stream, true, qmap, cmap, p);
+    p.part_item = reinterpret_cast<int4*>(p.part_o + static_cast<size_t>(2 * w) * p.block_rows * kLatent);
+    p.part_ml = reinterpret_cast<float*>(p.part_item + w);
+    CUtensorMap qmap;
+    if (!encode_rows_map(&qmap, q0, static_cast<long long>(n) * rows, 64, kChunks))
+      return PKV_ERR_ARG;
+    cudaError_t e = launch_kernel(latent_decode_kernel, dim3(2 * w), dim3(kLatThreads), kLatSmem,
+                                  stream, true, qmap, kmap, vmap, p);
     if (e != cudaSuccess) return record_cuda_status(e);
-    const long long groups = (p.block_rows + kJoinWarps - 1) / kJoinWarps;
-    e = launch_kernel(latent_join_kernel,
-                      dim3(static_cast<unsigned>(groups * n * p.row_blocks)),
-                      dim3(kJoinWarps * 32), 0, stream, true, p);
+    if (w == 1) continue;  // nothing can be split
+    e = launch_kernel(latent_join_kernel, dim3(4 * sms), dim3(kJoinWarps * 32), 0, stream, true, p);
     if (e != cudaSuccess) return record_cuda_status(e);
   }
   return PKV_OK;
