@@ -748,6 +748,38 @@ pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, const void* 
                                        void* workspace, size_t workspace_bytes,
                                        int32_t* dev_err, cudaStream_t stream);
 
+/*
+ * pkv_latent_prefill_attention - causal attention of packed sequences in the
+ * expanded form, on tcgen05 tensor cores: each head has its own keys and values,
+ * up-projected from the latents, and all heads share a token's rotated part.
+ *
+ * Sequence s has the queries q_starts[s] .. q_starts[s+1]-1 and the keys k_starts[s]
+ * .. k_starts[s+1]-1 (its cached prefix, as pkv_latent_gather returns it, then its
+ * own tokens). With n queries and m keys, query i sees the keys t <= m - n + i:
+ *   x[t] = scale (q[i,h][0:128] . k_own[t,h] + q[i,h][128:192] . k_rot[t])
+ *   lse[i, h] = ln sum_t exp(x[t])   (fp32),
+ *   out[i, h] = sum_t exp(x[t] - lse) v[t, h]
+ * A query that sees no key gives out 0, lse -inf. q: bf16, 192 values a head; k_own,
+ * v: bf16, 128 a head; k_rot: bf16, 64 a token; strides of tokens and heads in values,
+ * multiples of 8, >= 0 and below 2^38 (so slices of wider rows and stride-0 heads do);
+ * the four tensors 16-byte aligned. out: bf16 [n_queries, num_heads, 128], 32-byte
+ * aligned; lse: fp32 [n_queries, num_heads]. q_starts, k_starts: int32 [n_seqs + 1], ascending
+ * (equal neighbours: no queries, no keys) from 0 or more to at most n_queries and
+ * n_keys, else PKV_DEV_ERR_LAYOUT is set and rows are unspecified (nothing is read or
+ * written outside the tensors). Rows of out and lse outside all sequences stay as
+ * they were. Scores, sums and products are held in fp32; the weights are rounded to
+ * bf16 for the product (their sum takes them unrounded) and out is rounded once. A NaN
+ * or infinity in a sequence's k or v may reach any query of that sequence and head,
+ * never another's. num_heads 1 .. 65535; scale finite and > 0. The same inputs give the
+ * same bits on every run.
+ */
+pkv_status pkv_latent_prefill_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_own,
+    int64_t k_token_stride, int64_t k_head_stride, const void* k_rot, int64_t r_token_stride,
+    const void* v, int64_t v_token_stride, int64_t v_head_stride, int num_heads,
+    const int32_t* q_starts, const int32_t* k_starts, int n_seqs, int n_queries, int n_keys,
+    float scale, void* out, float* lse, int32_t* dev_err, cudaStream_t stream);
+
 /* Static, human-readable name of a status. */
 const char* pkv_status_string(pkv_status status);
 

@@ -18,7 +18,7 @@ Functions keep the names of the C entry points: ``pkv_append``,
 ``pkv_update_pages``, ``pkv_compact_workspace_size``, ``pkv_compact_pages``,
 ``pkv_rotate``, ``pkv_latent_append``, ``pkv_latent_gather``,
 ``pkv_latent_decode_workspace_size``, ``pkv_latent_decode_attention``,
-``pkv_status_string``, ``pkv_status_from_device_error`` and
+``pkv_latent_prefill_attention``, ``pkv_status_string``, ``pkv_status_from_device_error`` and
 ``pkv_last_cuda_error_string``.
 """
 
@@ -60,7 +60,7 @@ EXPORTED = ("pkv_append", "pkv_append_rope", "pkv_decode_workspace_size", "pkv_d
             "pkv_update_pages", "pkv_compact_workspace_size", "pkv_compact_pages",
             "pkv_rotate", "pkv_latent_append", "pkv_latent_gather",
             "pkv_latent_decode_workspace_size", "pkv_latent_decode_attention",
-            "pkv_status_string",
+            "pkv_latent_prefill_attention", "pkv_status_string",
             "pkv_status_from_device_error", "pkv_last_cuda_error_string")
 
 
@@ -161,6 +161,10 @@ def load_library() -> ctypes.CDLL:
     lib.pkv_latent_decode_attention.argtypes = [desc_p, vp, i32p, vp, c_int, i32p, i32p, c_int,
                                                 c_int, c_float, vp, f32p, vp, c_size, i32p, vp]
     lib.pkv_latent_decode_attention.restype = c_int
+    lib.pkv_latent_prefill_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64,
+                                                 c_int, i32p, i32p, c_int, c_int, c_int, c_float, vp,
+                                                 f32p, i32p, vp]
+    lib.pkv_latent_prefill_attention.restype = c_int
     lib.pkv_status_string.argtypes = [c_int]
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error_string.argtypes = []
@@ -876,4 +880,37 @@ def pkv_latent_decode_attention(pool, page_table, q, batch_idx, seq_lens, page_s
     _run_with(workspace, lambda: lib.pkv_latent_decode_workspace_size(desc_p, B, n_q, H),
               "pkv_latent_decode_attention", dev, stream, _dev_err(dev_err, dev),
               lib.pkv_latent_decode_attention, desc_p, pool_p, table, *args, out_p, lse_p)
+    return out, lse
+
+
+def pkv_latent_prefill_attention(q, k_own, k_rot, v, q_starts, k_starts, scale: float, out=None,
+                                 lse=None, dev_err=None, stream=None):
+    """Causal attention of packed sequences in the expanded form of shared latents. q [Tq, H,
+    192], k_own and v [Tk, H, 128], k_rot [Tk, 64], bf16, views of any token and head stride
+    (multiples of 8): sequence s has the queries q_starts[s] : q_starts[s + 1] and the keys
+    k_starts[s] : k_starts[s + 1], a cached prefix first; its last query sees all of them.
+    Returns (out [Tq, H, 128] bf16, lse [Tq, H] fp32); rows of no sequence stay as they were."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != LATENT_KEY + LATENT_ROTATED:
+        raise ValueError(f"q must be a tensor [Tq, H, {LATENT_KEY + LATENT_ROTATED}]")
+    q_p = _strided("q", q, None)
+    dev = q.get_device()
+    Tq, H, _ = q.shape
+    if not isinstance(k_own, torch.Tensor) or k_own.dim() != 3:
+        raise ValueError(f"k_own must be a tensor [Tk, H, {LATENT_KEY}]")
+    Tk = k_own.shape[0]
+    k_p = _strided("k_own", k_own, dev, (Tk, H, LATENT_KEY))
+    r_p = _strided("k_rot", k_rot, dev, (Tk, LATENT_ROTATED))
+    v_p = _strided("v", v, dev, (Tk, H, LATENT_VALUE))
+    _need(q_starts, "q_starts", torch.int32, 1)
+    n = q_starts.shape[0] - 1
+    if n < 0:
+        raise ValueError("q_starts must be [n_seqs + 1]")
+    qs = _tensor("q_starts", q_starts, torch.int32, (n + 1,), dev)
+    ks = _tensor("k_starts", k_starts, torch.int32, (n + 1,), dev)
+    out, out_p = _result("out", out, q, dev, stream, (Tq, H, LATENT_VALUE), torch.bfloat16)
+    lse, lse_p = _result("lse", lse, q, dev, stream, (Tq, H), torch.float32)
+    _run("pkv_latent_prefill_attention", dev, stream, load_library().pkv_latent_prefill_attention, q_p,
+         q.stride(0), q.stride(1), k_p, k_own.stride(0), k_own.stride(1), r_p, k_rot.stride(0), v_p,
+         v.stride(0), v.stride(1), H, qs, ks, n, Tq, Tk, float(scale), out_p, lse_p,
+         _dev_err(dev_err, dev))
     return out, lse

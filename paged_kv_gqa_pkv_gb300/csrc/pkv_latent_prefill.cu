@@ -1,0 +1,663 @@
+// pkv_latent_prefill.cu - causal attention of packed sequences in the expanded form of
+// shared latents, on tcgen05 tensor cores: a head's key is its own 128 values and the
+// token's 64 rotated ones (which all heads share), its value 128.
+//
+// For query i of the n of a sequence with m keys, over the keys t <= m - n + i:
+//   x[t] = scale (q_own . k_own[t] + q_rot . k_rot[t]),
+//   lse = ln sum_t exp x[t],   out = sum_t exp(x[t] - lse) v[t].
+//
+// An item is 256 query rows of one sequence and head, as two tiles of 128 rows that read the
+// same keys. Per 128 keys the tensor cores take 2 x (12 + 8) MMAs of 128 x 128 x 16, 2560
+// cycles at their rate; the 65 536 exponentials take 1024 to 2048. So the tensor pipe is the
+// bound, if each tile's softmax is hidden behind the other's products.
+//
+// Roles of a CTA (one per SM, items dealt by cost): warp 0 loads keys and values by TMA into a
+// ring of eight 16 KB slots (K: three slots of 64 dims x 128 keys, V: two of 64 keys), warp 2
+// the queries, warp 1's one thread issues the MMAs, warps 4-7 and 8-11 are the softmax of the
+// two tiles, a query row per thread. Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each);
+// P_h, bf16, is written over S_h and read from there by the product with V.
+//
+// The two tiles' chains QK -> softmax -> PV -> QK .. are independent; the MMA thread polls which
+// of their next products is ready and issues it, so that neither waits for the other's barrier.
+#include <atomic>
+#include <cmath>
+
+#include "pkv_latent.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace latent;
+using namespace prefill_detail;
+
+constexpr int kSlots = 8;
+constexpr int kSlot = 128 * 128;              // 16 KB
+constexpr int kQChunks = (kOwnKey + kRotated) / 64;
+constexpr int kTileSlots = kQChunks + 2;      // slots of a tile's keys and values
+constexpr int kItemRows = 2 * kBM;
+constexpr int kExpThreads = 12 * 32;
+
+// shared memory, offsets from a 1024-aligned base
+constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks][128 rows]
+constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
+constexpr int kOffBar = kOffRing + kSlots * kSlot;
+// full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2], tail
+constexpr int kNumBars = 2 * kSlots + 13;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
+constexpr int kOffSched = kOffMisc + 8;
+constexpr int kExpSmem = kOffSched + kSchedBytes + 1024;  // + slack for the alignment
+static_assert(kExpSmem <= kMaxDynSmem, "shared memory above the opt-in limit");
+static_assert(kSlots * kSlot >= kSchedScratchBytes, "schedule scratch lives in the ring");
+
+constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, false);
+constexpr uint32_t kIdescO = idesc_bf16_f32(kBM, kValue, true);
+
+struct LatentPrefillParams {
+  const int32_t* q_starts;
+  const int32_t* k_starts;
+  __nv_bfloat16* out;   // [tq, heads, 128]
+  float* lse;           // [tq, heads]
+  int32_t* dev_err;
+  int n_seqs;
+  int heads;
+  int tq;
+  int tk;
+  int n_tiles;          // places for 256-row tiles: tq / 256 + n_seqs
+  float qscale;         // scale * log2(e)
+};
+
+// Four K-steps, operands in shared memory.
+__device__ __forceinline__ void umma4_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b64 a<4>, b<4>;\n\t.reg .b32 x<4>, y<4>;\n\t"
+      "setp.ne.b32 p0, %3, 0;\n\tsetp.eq.b32 p1, %3, %3;\n\t"
+      "add.u32 x1, %1, 2;\n\tadd.u32 x2, %1, 4;\n\tadd.u32 x3, %1, 6;\n\t"
+      "add.u32 y1, %2, 2;\n\tadd.u32 y2, %2, 4;\n\tadd.u32 y3, %2, 6;\n\t"
+      "mov.b64 a0, {%1, %5};\n\tmov.b64 b0, {%2, %5};\n\t"
+      "mov.b64 a1, {x1, %5};\n\tmov.b64 b1, {y1, %5};\n\t"
+      "mov.b64 a2, {x2, %5};\n\tmov.b64 b2, {y2, %5};\n\t"
+      "mov.b64 a3, {x3, %5};\n\tmov.b64 b3, {y3, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %4, p0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %4, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %4, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %4, p1;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(idesc), "n"(kDescHi)
+      : "memory");
+}
+// Four K-steps of 16 keys, P from tensor memory (8 columns a step), V from shared memory.
+__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b64 b<4>;\n\t.reg .b32 x<4>, y<4>;\n\t"
+      "setp.ne.b32 p0, %3, 0;\n\tsetp.eq.b32 p1, %3, %3;\n\t"
+      "add.u32 x1, %1, 8;\n\tadd.u32 x2, %1, 16;\n\tadd.u32 x3, %1, 24;\n\t"
+      "add.u32 y1, %2, 128;\n\tadd.u32 y2, %2, 256;\n\tadd.u32 y3, %2, 384;\n\t"
+      "mov.b64 b0, {%2, %5};\n\tmov.b64 b1, {y1, %5};\n\t"
+      "mov.b64 b2, {y2, %5};\n\tmov.b64 b3, {y3, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], b1, %4, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], b2, %4, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x3], b3, %4, p1;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "r"(idesc), "n"(kDescHi)
+      : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// 32 bytes to global memory in one instruction.
+__device__ __forceinline__ void st_global_v8(void* a, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// ------------------------------------------------------------------- items --
+
+// A place for a 256-row tile: sequence b owns the places q_starts[b] / 256 + b up to the next
+// sequence's first one, as many as its rows can need. Places without rows have rows = 0.
+struct Tile {
+  int q0;    // its first query's token
+  int rows;  // its queries
+  int k0;    // the sequence's first key
+  int nk;    // the sequence's keys
+  int see;   // keys that its first query sees (may be negative)
+};
+__device__ __forceinline__ Tile tile_at(const LatentPrefillParams& p, int place) {
+  Tile t;
+  t.q0 = t.rows = t.k0 = t.nk = t.see = 0;
+  int lo = 0, hi = p.n_seqs;  // the first sequence whose places begin past `place`
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((__ldg(p.q_starts + mid) >> 8) + mid <= place) lo = mid + 1;
+    else hi = mid;
+  }
+  const int b = lo - 1;
+  if (b < 0) return t;
+  const int q0 = __ldg(p.q_starts + b), q1 = __ldg(p.q_starts + b + 1);
+  const int k0 = __ldg(p.k_starts + b), k1 = __ldg(p.k_starts + b + 1);
+  if (q0 < 0 || q1 < q0 || q1 > p.tq || k0 < 0 || k1 < k0 || k1 > p.tk) return t;
+  const int i0 = (place - ((q0 >> 8) + b)) * kItemRows;
+  if (i0 < 0 || i0 >= q1 - q0) return t;
+  t.q0 = q0 + i0;
+  t.rows = min(kItemRows, q1 - q0 - i0);
+  t.k0 = k0;
+  t.nk = k1 - k0;
+  t.see = t.nk - (q1 - q0) + i0 + 1;
+  return t;
+}
+// Key tiles that row tile h of an item reads (0: none, or no rows).
+__device__ __forceinline__ int key_tiles(const Tile& t, int h) {
+  const int last = min(t.rows, kBM * (h + 1)) - 1;  // its last row
+  if (last < kBM * h) return 0;
+  const int see = min(t.see + last, t.nk);
+  return see > 0 ? (see + kBN - 1) / kBN : 0;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap rmap,
+                      const __grid_constant__ CUtensorMap vmap, const LatentPrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // [8]
+  uint64_t* empty = full + kSlots;                               // [8]
+  uint64_t* q_full = empty + kSlots;                             // [2]
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;   // P_h is there, O_h rescaled
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_free = pv_done + 2;  // the epilogue has read O_h
+  uint64_t* tail = o_free + 2;     // values of a tile past whose last key there are others' rows
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&q_full[h], 1);
+      mbar_init(&q_empty[h], 1);
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_full[h], 4);   // the tile's four warps
+      mbar_init(&pv_done[h], 1);
+      mbar_init(&o_free[h], 4);
+    }
+    mbar_init(tail, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&rmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    // starts have to ascend from 0 or more to the tokens there are
+    for (int i = threadIdx.x; i <= p.n_seqs; i += kExpThreads) {
+      const int q = __ldg(p.q_starts + i), k = __ldg(p.k_starts + i);
+      const int qb = i > 0 ? __ldg(p.q_starts + i - 1) : 0, kb = i > 0 ? __ldg(p.k_starts + i - 1) : 0;
+      if (q < qb || q > p.tq || k < kb || k > p.tk) set_dev_err(p.dev_err, PKV_DEV_ERR_LAYOUT);
+    }
+  }
+  const uint16_t* s_list = reinterpret_cast<const uint16_t*>(smem + kOffSched);
+  const ItemSched S = sched_build(
+      reinterpret_cast<uint16_t*>(smem + kOffSched), smem + kOffRing, p.n_tiles, p.heads,
+      [&](int t) -> int {
+        const Tile x = tile_at(p, t);
+        return x.rows == 0 ? 0 : key_tiles(x, 0) + key_tiles(x, 1) + 1;
+      },
+      [&](int t) -> bool {  // the next place goes on in the same sequence
+        const Tile x = tile_at(p, t), y = tile_at(p, t + 1);
+        return x.rows > 0 && y.rows > 0 && y.k0 == x.k0 && y.q0 == x.q0 + kItemRows;
+      });
+  fence_proxy_async_smem();  // (the scratch's place goes to TMA)
+  __syncthreads();
+
+  // 384 threads start with 168 registers each; the softmax warps need more, the others few.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ------------------------------------------ keys and values ----
+      uint32_t n = 0, tails = 0;  // slots filled, tiles with a tail
+      bool ok = true;
+      int item;
+      for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
+        const int place = item / p.heads, head = item - place * p.heads;
+        const Tile x = tile_at(p, place);
+        const int nt = max(key_tiles(x, 0), key_tiles(x, 1));
+        for (int t = 0; ok && t < nt; ++t) {
+          const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
+          for (int s = 0; ok && s < kTileSlots; ++s, ++n) {
+            const uint32_t slot = n % kSlots;
+            ok = n < kSlots || wait_or_abort(&empty[slot], ((n / kSlots) - 1) & 1, s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* dst = smem + kOffRing + slot * kSlot;
+            const int key = x.k0 + t * kBN;
+            if (s < kQChunks) {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], kSlot);
+                if (s < 2) tma_load_3d(dst, &kmap, &full[slot], 64 * s, head, key);
+                else tma_load_3d(dst, &rmap, &full[slot], 0, 0, key);
+              }
+            } else {
+              const int v = s - kQChunks;  // which 64 keys
+              const int valid = left - 64 * v;
+              const bool ragged = valid > 0 && valid < 64 && (valid & 15) != 0;
+              if (lane == 0) {
+                uint64_t* bar = ragged ? tail : &full[slot];
+                mbar_arrive_expect_tx(bar, kSlot);
+                tma_load_3d(dst, &vmap, bar, 0, head, key + 64 * v);
+                tma_load_3d(dst + kSlot / 2, &vmap, bar, 64, head, key + 64 * v);
+              }
+              if (ragged) {
+                // the rows past the sequence that share a 16-key step with its last ones: their
+                // weights are 0, but what stands there may be NaN
+                ok = __all_sync(0xffffffffu, wait_or_abort(tail, tails & 1, s_abort));
+                ++tails;
+                if (!ok) break;
+                const int z = 16 - (valid & 15);
+                for (int e = lane; e < z * 16; e += 32)
+                  *reinterpret_cast<uint4*>(dst + (e & 8) * (kSlot / 16) + (valid + (e >> 4)) * 128 +
+                                            (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+              }
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+    } else if (warp == 2) {
+      // ---------------------------------------------------- queries ----
+      if (lane == 0) {
+        uint32_t n[2] = {0u, 0u};
+        bool ok = true;
+        int item;
+        for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
+          const int place = item / p.heads, head = item - place * p.heads;
+          const Tile x = tile_at(p, place);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (key_tiles(x, h) == 0 || !ok) continue;
+            ok = n[h] == 0 || wait_or_abort(&q_empty[h], (n[h] - 1) & 1, s_abort);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
+            for (int c = 0; c < kQChunks; ++c)
+              tma_load_3d(smem + kOffQ + (h * kQChunks + c) * kSlot, &qmap, &q_full[h], 64 * c,
+                          head, x.q0 + kBM * h);
+            ++n[h];
+          }
+        }
+        if (!ok) *s_abort = 1;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------- MMAs ----
+      if (elect_one()) {
+        // One chain per row tile: its item, its next tile's number and whether QK or PV is next.
+        // `base` counts the key tiles of the items before; kq, vq: key tiles of all items that
+        // the chain needs no more of the keys, the values.
+        struct Chain {
+          int r, t, nt, item_nt, left0;
+          uint32_t base, n, items, kq, vq;
+          bool pv, done;
+        };
+        Chain ch[2];
+        auto next_item = [&](Chain& c, int h) {
+          for (;; ++c.r) {
+            const int item = sched_item(S, s_list, c.r);
+            if (item < 0) {
+              c.done = true;
+              c.kq = c.vq = 0xffffffffu;
+              return;
+            }
+            const Tile x = tile_at(p, item / p.heads);
+            c.nt = key_tiles(x, h);
+            c.item_nt = max(key_tiles(x, 0), key_tiles(x, 1));
+            c.left0 = x.nk;
+            c.kq = c.vq = c.base;
+            if (c.nt > 0) break;
+            c.base += static_cast<uint32_t>(c.item_nt);
+          }
+          c.t = 0;
+          c.pv = false;
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ch[h].r = 0;
+          ch[h].base = ch[h].n = ch[h].items = 0;
+          ch[h].done = false;
+          next_item(ch[h], h);
+        }
+        uint32_t k_rel = 0, v_rel = 0;  // key tiles whose slots have been given back
+        uint32_t landed = 0;            // slots that have been filled
+        const uint32_t ring_lo = desc_lo(smem_u32(smem + kOffRing), 0);
+        const uint32_t ring_v = desc_lo(smem_u32(smem + kOffRing), kSlot / 2);
+        uint64_t t0 = 0;
+        uint32_t idle = 0;
+        while (!(ch[0].done && ch[1].done)) {
+          bool worked = false;
+          // in order, so that no slot's barrier is asked for a phase ahead of its next one
+          if (mbar_test(&full[landed % kSlots], (landed / kSlots) & 1)) {
+            ++landed;
+            worked = true;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            Chain& c = ch[h];
+            if (c.done) continue;
+            const uint32_t tile = c.base + static_cast<uint32_t>(c.t);
+            const uint32_t first = tile * kTileSlots;  // its first slot's number
+            if (!c.pv) {
+              // S_h = Q_h K^T, over P_h once the last PV_h has read it
+              if (!(c.n == 0 || mbar_test(&pv_done[h], (c.n - 1) & 1))) continue;
+              if (c.t == 0 && !mbar_test(&q_full[h], c.items & 1)) continue;
+              if (landed < first + kQChunks) continue;
+              tc_fence_after();
+              const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ + h * kQChunks * kSlot), 0);
+#pragma unroll
+              for (int s = 0; s < kQChunks; ++s)
+                umma4_ss(tmem + kBN * h, q_lo + ((s * kSlot) >> 4),
+                         ring_lo + ((((first + s) % kSlots) * kSlot) >> 4), kIdescS, s > 0 ? 1u : 0u);
+              umma_commit(&s_full[h]);
+              c.pv = true;
+              if (c.t + 1 == c.nt) umma_commit(&q_empty[h]);
+              c.kq = c.t + 1 == c.nt ? c.base + static_cast<uint32_t>(c.item_nt) : tile + 1;
+            } else {
+              // O_h += P_h V
+              if (!mbar_test(&p_full[h], c.n & 1)) continue;
+              if (c.t == 0 && c.items > 0 && !mbar_test(&o_free[h], (c.items - 1) & 1)) continue;
+              if (landed < first + kTileSlots) continue;
+              const uint32_t v0 = first + kQChunks, v1 = v0 + 1;
+              tc_fence_after();
+              const int left = c.left0 - c.t * kBN;
+              const int steps = left >= kBN ? 8 : (left + 15) >> 4;
+              const uint32_t d = tmem + 256 + kValue * h, a = tmem + kBN * h;
+              const uint32_t b0 = ring_v + (((v0 % kSlots) * kSlot) >> 4);
+              const uint32_t b1 = ring_v + (((v1 % kSlots) * kSlot) >> 4);
+              const uint32_t acc = c.t > 0 ? 1u : 0u;
+              if (steps == 8) {
+                umma4_ts(d, a, b0, kIdescO, acc);
+                umma4_ts(d, a + 32, b1, kIdescO, 1u);
+              } else {
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) {
+                  const uint64_t bd = (static_cast<uint64_t>(kDescHi) << 32) |
+                                      ((k < 4 ? b0 : b1) + 128u * (k & 3));
+                  umma_bf16_ts(d, a + 8 * k, bd, kIdescO, acc | (k > 0 ? 1u : 0u));
+                }
+              }
+              umma_commit(&pv_done[h]);
+              ++c.n;
+              c.pv = false;
+              const bool last = ++c.t == c.nt;
+              c.vq = last ? c.base + static_cast<uint32_t>(c.item_nt) : tile + 1;
+              if (last) {
+                c.base += static_cast<uint32_t>(c.item_nt);
+                ++c.r;
+                ++c.items;
+                next_item(c, h);
+              }
+            }
+            worked = true;
+          }
+          if (ch[0].done && ch[1].done) break;
+          // slots that neither chain needs any more go back once the products issued are done
+          for (; k_rel < min(ch[0].kq, ch[1].kq); ++k_rel)
+            for (int s = 0; s < kQChunks; ++s) umma_commit(&empty[(k_rel * kTileSlots + s) % kSlots]);
+          for (; v_rel < min(ch[0].vq, ch[1].vq); ++v_rel)
+            for (int s = kQChunks; s < kTileSlots; ++s)
+              umma_commit(&empty[(v_rel * kTileSlots + s) % kSlots]);
+          if (worked) {
+            idle = 0;
+            continue;
+          }
+          if (idle++ == 0) t0 = global_timer_ns();
+          if ((idle & 63u) == 0 && (*s_abort || global_timer_ns() - t0 > kWaitLimitNs)) {
+            *s_abort = 1;
+            break;
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------ softmax and epilogue ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int h = (warp - 4) >> 2;
+    const int lane_base = 32 * (warp & 3);
+    const int row = lane_base + lane;  // of the tile
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(lane_base) << 16);
+    const uint32_t t_s = t_lane + kBN * h;
+    const uint32_t t_o = t_lane + 256 + kValue * h;
+    uint32_t n = 0;
+    bool ok = true;
+    int item;
+    for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
+      const int place = item / p.heads, head = item - place * p.heads;
+      const Tile x = tile_at(p, place);
+      const int nt = key_tiles(x, h);
+      const int i = kBM * h + row;  // of the item
+      const bool live = i < x.rows;
+      const int see = live ? min(x.see + i, x.nk) : 0;  // keys that the row sees
+      float m_run = -INFINITY;  // the maximum that the weights refer to, raw score units
+      float l_run = 0.f;
+      for (int t = 0; t < nt; ++t, ++n) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[h], n & 1, s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+        tmem_wait_ld();
+        const int c_hi = see - t * kBN;  // visible columns
+        if (c_hi < kBN) {
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (c >= c_hi) sr[c] = __float_as_uint(-INFINITY);
+        }
+        const float mx = row_max_full(sr);
+        // the maximum moves only when it has grown by more than 2^8: until then weights of up
+        // to 256 do no harm in bf16 and fp32, and O stays as it is
+        const float m_cand = fmaxf(m_run, mx);
+        const bool grow = m_run == -INFINITY ? m_cand != -INFINITY
+                                             : (m_cand - m_run) * p.qscale > kRescaleThreshold;
+        const float m_use = grow ? m_cand : m_run;
+        const float alpha = grow ? ex2((m_run - m_use) * p.qscale) : 1.f;  // 0 if m_run = -inf
+        const float neg_m = m_use == -INFINITY ? 0.f : -m_use * p.qscale;
+        // P over the first 64 columns of S_h, in bf16 (a weight off by at most 2^-8 of itself;
+        // the sum takes it unrounded)
+        const float psum = softmax_row_to_tmem(sr, p.qscale, neg_m, t_s);
+        l_run = l_run * alpha + psum;
+        m_run = m_use;
+        // (S_h of this tile was issued after the last PV_h had completed: O_h is at rest)
+        if (t > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int q = 0; q < kValue; q += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(t_o + q, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[h]);
+      }
+      // ---- O / l, LSE ----
+      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[h], (n - 1) & 1, s_abort));
+      if (!ok) break;
+      tc_fence_after();
+      const bool has = live && l_run > 0.f;
+      const float inv = has ? 1.f / l_run : 0.f;
+      const long long at = static_cast<long long>(x.q0 + i) * p.heads + head;
+      __nv_bfloat16* orow = p.out + at * kValue;
+#pragma unroll 1
+      for (int q = 0; q < kValue; q += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(t_o + q, o);
+          tmem_wait_ld();
+        }
+        if (live) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t wv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              wv[e] = has ? pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv,
+                                        __uint_as_float(o[16 * v + 2 * e + 1]) * inv)
+                          : 0u;
+            st_global_v8(orow + q + 16 * v, wv);
+          }
+        }
+      }
+      if (live)
+        p.lse[at] = has ? (m_run * p.qscale + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+      if (nt > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[h]);
+      }
+    }
+    if (!ok) *s_abort = 1;
+  }
+  __syncwarp();
+  if (*s_abort && threadIdx.x == 0) {
+    set_dev_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    // copies that are still in flight land before the CTA's shared memory goes back
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000) {}
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+namespace {
+
+// {values, heads, tokens} view with free strides (in values); a box is 64 values of one head of
+// `tokens` tokens, 128-byte swizzled.
+bool encode_heads_map(CUtensorMap* map, const void* base, int values, int heads, int tokens,
+                      int64_t token_stride, int64_t head_stride, int box_tokens) {
+  prefill_host::EncodeTiledFn enc = prefill_host::encode_fn();
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(values), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2,
+                                 static_cast<cuuint64_t>(token_stride) * 2};
+  const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+using namespace pkv::latent;
+
+extern "C" pkv_status pkv_latent_prefill_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_own,
+    int64_t k_token_stride, int64_t k_head_stride, const void* k_rot, int64_t r_token_stride,
+    const void* v, int64_t v_token_stride, int64_t v_head_stride, int num_heads,
+    const int32_t* q_starts, const int32_t* k_starts, int n_seqs, int n_queries, int n_keys,
+    float scale, void* out, float* lse, int32_t* dev_err, cudaStream_t stream) {
+  if (num_heads <= 0 || num_heads > 65535 || n_seqs < 0 || n_queries < 0 || n_keys < 0 ||
+      !std::isfinite(scale) || !(scale > 0.f))
+    return PKV_ERR_ARG;
+  constexpr int64_t kMaxStride = int64_t{1} << 38;  // a tensor map's limit, in values
+  for (const int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                          r_token_stride, v_token_stride, v_head_stride})
+    if (s < 0 || s >= kMaxStride) return PKV_ERR_ARG;
+  if (n_seqs == 0 || n_queries == 0) return PKV_OK;
+  const long long places = n_queries / 256 + static_cast<long long>(n_seqs);
+  if (places * num_heads > INT_MAX) return PKV_ERR_ARG;
+  if (!q || !q_starts || !k_starts || !out || !lse || (n_keys > 0 && (!k_own || !k_rot || !v)))
+    return PKV_ERR_ARG;
+  for (const int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                          r_token_stride, v_token_stride, v_head_stride})
+    if (s % 8 != 0) return PKV_ERR_ALIGN;
+  if (!is_aligned(q, 16) || !is_aligned(k_own, 16) || !is_aligned(k_rot, 16) || !is_aligned(v, 16) ||
+      !is_aligned(out, 32) || !is_aligned(lse, 4) || !is_aligned(q_starts, 4) ||
+      !is_aligned(k_starts, 4) || !is_aligned(dev_err, 4))
+    return PKV_ERR_ALIGN;
+  int sms = 0;
+  if (const pkv_status st = device_info(&sms); st != PKV_OK) return st;
+  CUtensorMap qmap, kmap, rmap, vmap;
+  // (without keys nothing is loaded: the queries' tensor stands in for what is not there)
+  const bool any = n_keys > 0;
+  if (!encode_heads_map(&qmap, q, kOwnKey + kRotated, num_heads, n_queries, q_token_stride,
+                        q_head_stride, kBM) ||
+      !encode_heads_map(&kmap, any ? k_own : q, kOwnKey, num_heads, any ? n_keys : n_queries,
+                        any ? k_token_stride : q_token_stride, any ? k_head_stride : q_head_stride,
+                        kBN) ||
+      !encode_heads_map(&rmap, any ? k_rot : q, kRotated, 1, any ? n_keys : n_queries,
+                        any ? r_token_stride : q_token_stride, any ? r_token_stride : q_token_stride,
+                        kBN) ||
+      !encode_heads_map(&vmap, any ? v : q, kValue, num_heads, any ? n_keys : n_queries,
+                        any ? v_token_stride : q_token_stride, any ? v_head_stride : q_head_stride, 64))
+    return PKV_ERR_ARG;
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return record_cuda_status(e);
+  static std::atomic<bool> attr_set[64] = {};  // per device; host threads may race to set it
+  if (dev < 0 || dev >= 64) return PKV_ERR_DEVICE;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpSmem);
+    if (e != cudaSuccess) return record_cuda_status(e);
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  LatentPrefillParams p;
+  p.q_starts = q_starts;
+  p.k_starts = k_starts;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.dev_err = dev_err;
+  p.n_seqs = n_seqs;
+  p.heads = num_heads;
+  p.tq = n_queries;
+  p.tk = n_keys;
+  p.n_tiles = static_cast<int>(places);
+  p.qscale = scale * 1.4426950408889634f;
+  const long long items = places * num_heads;
+  return record_cuda_status(launch_kernel(latent_prefill_kernel,
+                                          dim3(static_cast<unsigned>(items < sms ? items : sms)),
+                                          dim3(kExpThreads), kExpSmem, stream, true, qmap, kmap, rmap,
+                                          vmap, p));
+}

@@ -328,3 +328,139 @@ def test_decode_workspace():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     with pytest.raises(binding.PkvError):
         run_decode(pool, table, q, slots, lens, 64, workspace=ws[:n // 4 - 64])
+
+
+# ----------------------------------------------------------------- prefill --
+
+def prefill_case(seed, lens, H, before=0, after=0, q_scale=1.0):
+    """lens: (queries, keys) of each sequence; `before`/`after` rows of no sequence around them."""
+    g = C.gen(seed)
+    q_starts, k_starts = [before], [before]
+    for n, m in lens:
+        q_starts.append(q_starts[-1] + n)
+        k_starts.append(k_starts[-1] + m)
+    tq, tk = q_starts[-1] + after, k_starts[-1] + after
+    q = C.normal(g, tq, H, 192, scale=q_scale)
+    kv = C.normal(g, tk, H, 256)
+    rows = C.normal(g, tk, 576)
+    return q, kv, rows, C.i32(q_starts), C.i32(k_starts)
+
+
+def run_prefill(case, **kw):
+    q, kv, rows, q_starts, k_starts = case
+    kv, rows, err = kv.cuda(), rows.cuda(), new_err()
+    out, lse = binding.pkv_latent_prefill_attention(q.cuda(), kv[..., :128], rows[:, 512:], kv[..., 128:], q_starts.cuda(),
+                                                    k_starts.cuda(), C.SCALE, dev_err=err, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), lse.cpu(), err.item()
+
+
+def check_prefill(case, tag="", rows=None, **kw):
+    q, kv, lat, q_starts, k_starts = case
+    out, lse, err = run_prefill(case, **kw)
+    want = orl.prefill(C.bits(q), C.bits(kv[..., :128].contiguous()), C.bits(lat[:, 512:].contiguous()),
+                       C.bits(kv[..., 128:].contiguous()), q_starts.tolist(), k_starts.tolist(), C.SCALE)
+    a, b = int(q_starts[0]), int(q_starts[-1])
+    C.check_attention(out[a:b], lse[a:b], [w[a:b] for w in want], 192, tag)
+    return err
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300, 513])
+def test_prefill_lengths(n):
+    assert check_prefill(prefill_case(n, [(n, n)], 2)) == 0
+
+
+@pytest.mark.parametrize("n,m", [(1, 700), (3, 130), (130, 131), (128, 256), (100, 1000), (300, 333), (257, 640)])
+def test_prefill_behind_a_prefix(n, m):
+    assert check_prefill(prefill_case(n + m, [(n, m)], 2)) == 0
+
+
+@pytest.mark.parametrize("H", [1, 3, 8, 33])
+def test_prefill_heads(H):
+    assert check_prefill(prefill_case(H, [(70, 70), (5, 200)], H)) == 0
+
+
+def test_prefill_packed():
+    """Many sequences of all kinds, empty ones among them, rows of none before and behind."""
+    lens = [(1, 1), (0, 0), (130, 130), (5, 300), (0, 40), (64, 64), (256, 300), (17, 17), (0, 0), (300, 301), (2, 2)]
+    case = prefill_case(4, lens, 3, before=2, after=3)
+    out = torch.full((case[0].shape[0], 3, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((case[0].shape[0], 3), 7.0, device="cuda")
+    assert check_prefill(case, out=out, lse=lse) == 0
+    assert (out[:2] == 7).all() and (out[-3:] == 7).all() and (lse[:2] == 7).all() and (lse[-3:] == 7).all()
+
+
+def test_prefill_more_queries_than_keys():
+    """The first queries see nothing: 0 and -inf."""
+    assert check_prefill(prefill_case(5, [(10, 3), (300, 100), (200, 0), (4, 4)], 2)) == 0
+
+
+def test_prefill_items_of_very_different_cost():
+    """Items of one tile beside items of many, more items than SMs."""
+    lens = [(700, 2000)] + [(3, 3)] * 40 + [(130, 140)] * 3 + [(1, 1500)] * 5
+    assert check_prefill(prefill_case(6, lens, 4)) == 0
+
+
+def test_prefill_neighbours_are_not_read():
+    """NaN in every other sequence's rows, and in rows of none, reaches no result."""
+    case = prefill_case(7, [(50, 50), (77, 205), (40, 40)], 2, before=4, after=4)
+    q, kv, rows, qs, ks = case
+    nan = float("nan")
+    for s in range(3):
+        kv2, rows2, q2 = kv.clone(), rows.clone(), q.clone()
+        keep_k, keep_q = slice(int(ks[s]), int(ks[s + 1])), slice(int(qs[s]), int(qs[s + 1]))
+        for t, keep in ((kv2, keep_k), (rows2, keep_k), (q2, keep_q)):
+            saved = t[keep].clone()
+            t.fill_(nan)
+            t[keep] = saved
+        a, b = run_prefill(case), run_prefill((q2, kv2, rows2, qs, ks))
+        assert torch.equal(a[0][keep_q], b[0][keep_q]) and torch.equal(a[1][keep_q], b[1][keep_q])
+
+
+def test_prefill_large_scores():
+    """Scores in the hundreds whose maximum moves along the keys."""
+    q, kv, rows, qs, ks = prefill_case(8, [(300, 900)], 2, q_scale=30.0)
+    kv = (kv.float() * torch.linspace(0.2, 2.0, 900)[:, None, None]).to(torch.bfloat16)
+    assert check_prefill((q, kv, rows, qs, ks)) == 0
+
+
+def test_prefill_strides():
+    """Contiguous tensors, wide rows, heads outside the tokens: one result."""
+    case = prefill_case(9, [(140, 200), (30, 30)], 3)
+    q, kv, rows, qs, ks = case
+    a = run_prefill(case)
+    k, v, r = kv[..., :128], kv[..., 128:], rows[:, 512:]
+    forms = [(q.cuda(), k.contiguous().cuda(), r.contiguous().cuda(), v.contiguous().cuda()),
+             (q.transpose(0, 1).contiguous().cuda().transpose(0, 1), k.transpose(0, 1).contiguous().cuda().transpose(0, 1),
+              rows.cuda()[:, 512:], v.cuda())]
+    for qf, kf, rf, vf in forms:
+        out, lse = binding.pkv_latent_prefill_attention(qf, kf, rf, vf, qs.cuda(), ks.cuda(), C.SCALE)
+        assert torch.equal(out.cpu(), a[0]) and torch.equal(lse.cpu(), a[1])
+    # one head's keys and values for all heads (stride 0)
+    shared = prefill_case(10, [(60, 90)], 1)
+    q3 = C.normal(C.gen(11), 60, 3, 192)
+    k1, v1, r1 = shared[1][..., :128], shared[1][..., 128:], shared[2][:, 512:]
+    out, lse = binding.pkv_latent_prefill_attention(q3.cuda(), k1.cuda().expand(90, 3, 128), r1.cuda(),
+                                                    v1.cuda().expand(90, 3, 128), shared[3].cuda(), shared[4].cuda(), C.SCALE)
+    for h in range(3):
+        o, l = binding.pkv_latent_prefill_attention(q3[:, h:h + 1].cuda(), k1.cuda(), r1.cuda(), v1.cuda(),
+                                                    shared[3].cuda(), shared[4].cuda(), C.SCALE)
+        assert torch.equal(out[:, h], o[:, 0]) and torch.equal(lse[:, h], l[:, 0])
+
+
+def test_prefill_bad_starts():
+    """Starts that do not ascend or pass the tensors are told, and nothing outside is touched."""
+    case = prefill_case(12, [(40, 40), (60, 60), (20, 20)], 2)
+    q, kv, rows, qs, ks = case
+    for bad_q, bad_k in (([0, 100, 40, 120], None), ([0, 40, 100, 121], None), (None, [0, 40, 100, 121]), (None, [0, 100, 40, 120]),
+                         ([-1, 40, 100, 120], None), ([0, 1 << 30, 100, 120], None)):
+        c = (q, kv, rows, C.i32(bad_q) if bad_q else qs, C.i32(bad_k) if bad_k else ks)
+        assert run_prefill(c)[2] & LAYOUT
+
+
+def test_prefill_same_bits_every_time():
+    case = prefill_case(13, [(300, 700), (129, 129), (1, 900)], 4)
+    first = run_prefill(case)
+    for _ in range(5):
+        again = run_prefill(case)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
