@@ -136,18 +136,6 @@ __device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // One box of a tiled load whose bytes count on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
                                                  int x, int y, int z) {
@@ -488,7 +476,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       const int32_t* table = p.page_table + static_cast<long long>(w.slot) * p.max_blocks;
       if (keys) {
         if (lane == 0) {
-          ok = items == 0 || wait_or_abort(q_empty, (items - 1) & 1, s_abort);
+          ok = items == 0 || wait_phase(q_empty, (items - 1) & 1, s_abort);
           if (ok) {
             if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kChunks * kChunk);
             tma_load_3d_pair(smem + kOffQ, &qmap, q_full0, 0,
@@ -520,7 +508,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
           uint8_t* dst = smem + kOffK + (lane % per) * kChunk + (lane / per) * R * 128;
 #pragma unroll 1
           for (int g = 0; ok && g < kKGroups; ++g) {
-            ok = tc == 0 || wait_or_abort(&k_empty[g], (tc - 1) & 1, s_abort);
+            ok = tc == 0 || wait_phase(&k_empty[g], (tc - 1) & 1, s_abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * 3 * kChunk);
@@ -547,7 +535,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                          (lane / per - kh * half_boxes) * R * 128;
 #pragma unroll 1
           for (int g = 0; ok && g < kVGroups; ++g) {
-            ok = tc == 0 || wait_or_abort(&v_empty[g], (tc - 1) & 1, s_abort);
+            ok = tc == 0 || wait_phase(&v_empty[g], (tc - 1) & 1, s_abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             // the values of a ragged tile are announced to this CTA's softmax warps, which zero
@@ -601,8 +589,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       uint32_t tp = 0, p_items = 0, fv = 0;  // PV's; tiles whose values v_full announced
       int sj = ws.j0, pj = w.j0, sg = 0, pg = 0;
       bool q_there = false, p_there = false;
-      uint64_t t0 = 0;
-      uint32_t idle = 0;
+      WaitLimit idle;
       while (p_more) {
         // P of tile tp (before an item's first PV both epilogues have read the last item's O)
         if (!p_there)
@@ -641,7 +628,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
               pj = w.j0;
             }
           }
-          idle = 0;
+          idle.restart();
           continue;
         }
         // S of tile ts goes into buffer ts & 1, which P of tile ts - 2 has been read from
@@ -670,14 +657,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
               sj = ws.j0;
             }
           }
-          idle = 0;
+          idle.restart();
           continue;
         }
-        if (idle++ == 0) t0 = global_timer_ns();
-        if ((idle & 63u) == 0 && (*s_abort || global_timer_ns() - t0 > kWaitLimitNs)) {
-          *s_abort = 1;
-          break;
-        }
+        if (idle.over(s_abort)) break;
       }
     }
   } else {
@@ -703,7 +686,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       for (int j = w.j0; j < w.j1; ++j, ++tc) {
         // a wait that gave up is told to the other warps at their next common barrier, so
         // that all four leave at the same place
-        ok = ok && wait_or_abort(&s_full[tc & 1], (tc >> 1) & 1, s_abort);
+        ok = ok && wait_phase(&s_full[tc & 1], (tc >> 1) & 1, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         uint32_t s[64];
@@ -778,7 +761,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         l_run = l_run * alpha + psum;
         m_run = m_use;
         // P and O are free once the last PV is done
-        ok = tc == 0 || wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
+        ok = tc == 0 || wait_phase(pv_done, (tc - 1) & 1, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc_fence_after();
@@ -803,7 +786,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         // values of rows past the last key may hold any bits: their weights are 0, but
         // 0 * NaN is not, so the rows that share a 16-key step with live ones are zeroed
         if (ragged(w.n, j)) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(v_tail, tails & 1, s_abort));
+          ok = __all_sync(0xffffffffu, wait_phase(v_tail, tails & 1, s_abort));
           ++tails;
           if (!ok) continue;
           const int left = w.n - j * kKeys;
@@ -821,7 +804,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       }
       // ---- the segment's end: O and the row's maximum and sum ----
       if (left_together) break;
-      ok = ok && wait_or_abort(pv_done, (tc - 1) & 1, s_abort);
+      ok = ok && wait_phase(pv_done, (tc - 1) & 1, s_abort);
       float* const sums = s_max + 256;
       sums[tl] = l_run;
       ok = named_bar_all(1, 128, ok);

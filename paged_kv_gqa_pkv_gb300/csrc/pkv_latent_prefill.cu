@@ -13,12 +13,13 @@
 //
 // Roles of a CTA (one per SM, items dealt by cost): warp 0 loads keys and values by TMA into a
 // ring of eight 16 KB slots (K: three slots of 64 dims x 128 keys, V: two of 64 keys), warp 2
-// the queries, warp 1's one thread issues the MMAs, warps 4-7 and 8-11 are the softmax of the
-// two tiles, a query row per thread. Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each);
+// the queries, one thread each of warps 1 and 3 issues the MMAs of one tile, warps 4-7 and 8-11
+// are the softmax of the two tiles, a query row per thread. Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each);
 // P_h, bf16, is written over S_h and read from there by the product with V.
 //
-// The two tiles' chains QK -> softmax -> PV -> QK .. are independent; the MMA thread polls which
-// of their next products is ready and issues it, so that neither waits for the other's barrier.
+// The two tiles' chains QK -> softmax -> PV -> QK .. are independent, each with its own issuing
+// thread. (One thread that polled both chains' barriers took ~800 cycles a round beside the
+// softmax warps, whose code passes through the same instruction cache: 6000 cycles a key tile.)
 #include <atomic>
 #include <cmath>
 
@@ -41,8 +42,8 @@ constexpr int kExpThreads = 12 * 32;
 constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks][128 rows]
 constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-// full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2], tail
-constexpr int kNumBars = 2 * kSlots + 13;
+// full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_free[2], tail
+constexpr int kNumBars = 2 * kSlots + 15;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
 constexpr int kOffSched = kOffMisc + 8;
 constexpr int kExpSmem = kOffSched + kSchedBytes + 1024;  // + slack for the alignment
@@ -103,16 +104,36 @@ __device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a_tmem, uint32_t b
       : "memory");
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// exp2(s * qscale - m) of 64 columns, as bf16 pairs into 32 columns of this thread's TMEM lane;
+// their sum in fp32. Scale, shift and sum run two values per instruction.
+__device__ __forceinline__ float weights_to_tmem(const uint32_t (&s)[64], float qscale, float neg_m,
+                                                 uint32_t t_p) {
+  const unsigned long long qs2 = pack_f32x2(qscale, qscale);
+  const unsigned long long nm2 = pack_f32x2(neg_m, neg_m);
+  unsigned long long acc0 = 0ull, acc1 = 0ull;
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 64; c += 4) {
+    float e[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const unsigned long long x2 = ffma2(
+          pack_f32x2(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])), qs2, nm2);
+      float x0, x1;
+      unpack_f32x2(x2, x0, x1);
+      e[2 * u] = ex2(x0);
+      e[2 * u + 1] = ex2(x1);
+    }
+    acc0 = fadd2(acc0, pack_f32x2(e[0], e[1]));
+    acc1 = fadd2(acc1, pack_f32x2(e[2], e[3]));
+    pk[c / 2] = pack_bf16x2(e[0], e[1]);
+    pk[c / 2 + 1] = pack_bf16x2(e[2], e[3]);
+  }
+  tmem_st32(t_p, pk);
+  float a, b, c, d;
+  unpack_f32x2(acc0, a, b);
+  unpack_f32x2(acc1, c, d);
+  return (a + b) + (c + d);
 }
 
 // 32 bytes to global memory in one instruction.
@@ -179,8 +200,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* q_full = empty + kSlots;                             // [2]
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
-  uint64_t* p_full = s_full + 2;   // P_h is there, O_h rescaled
-  uint64_t* pv_done = p_full + 2;
+  uint64_t* p_full = s_full + 2;   // [tile][half of its keys]: P_h is there, O_h rescaled
+  uint64_t* pv_done = p_full + 4;
   uint64_t* o_free = pv_done + 2;  // the epilogue has read O_h
   uint64_t* tail = o_free + 2;     // values of a tile past whose last key there are others' rows
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -192,13 +213,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both row tiles'
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&q_full[h], 1);
       mbar_init(&q_empty[h], 1);
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], 4);   // the tile's four warps
+      mbar_init(&p_full[2 * h], 4);  // the tile's four warps
+      mbar_init(&p_full[2 * h + 1], 4);
       mbar_init(&pv_done[h], 1);
       mbar_init(&o_free[h], 4);
     }
@@ -230,7 +252,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       reinterpret_cast<uint16_t*>(smem + kOffSched), smem + kOffRing, p.n_tiles, p.heads,
       [&](int t) -> int {
         const Tile x = tile_at(p, t);
-        return x.rows == 0 ? 0 : key_tiles(x, 0) + key_tiles(x, 1) + 1;
+        // (an item's queries, first products and results take about 1.5 key tiles' time)
+        return x.rows == 0 ? 0 : 2 * max(key_tiles(x, 0), key_tiles(x, 1)) + 3;
       },
       [&](int t) -> bool {  // the next place goes on in the same sequence
         const Tile x = tile_at(p, t), y = tile_at(p, t + 1);
@@ -255,7 +278,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
           for (int s = 0; ok && s < kTileSlots; ++s, ++n) {
             const uint32_t slot = n % kSlots;
-            ok = n < kSlots || wait_or_abort(&empty[slot], ((n / kSlots) - 1) & 1, s_abort);
+            ok = n < kSlots || wait_phase(&empty[slot], ((n / kSlots) - 1) & 1, s_abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             uint8_t* dst = smem + kOffRing + slot * kSlot;
@@ -279,7 +302,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
               if (ragged) {
                 // the rows past the sequence that share a 16-key step with its last ones: their
                 // weights are 0, but what stands there may be NaN
-                ok = __all_sync(0xffffffffu, wait_or_abort(tail, tails & 1, s_abort));
+                ok = __all_sync(0xffffffffu, wait_phase(tail, tails & 1, s_abort));
                 ++tails;
                 if (!ok) break;
                 const int z = 16 - (valid & 15);
@@ -307,7 +330,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (key_tiles(x, h) == 0 || !ok) continue;
-            ok = n[h] == 0 || wait_or_abort(&q_empty[h], (n[h] - 1) & 1, s_abort);
+            ok = n[h] == 0 || wait_phase(&q_empty[h], (n[h] - 1) & 1, s_abort);
             if (!ok) break;
             mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
             for (int c = 0; c < kQChunks; ++c)
@@ -318,133 +341,86 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         if (!ok) *s_abort = 1;
       }
-    } else if (warp == 1) {
+    } else {
       // ------------------------------------------------------- MMAs ----
+      // Warp 1 for tile 0, warp 3 for tile 1: each waits for its own tile's barriers only, so
+      // that the tiles' products fill each other's gaps. Both wait for every slot of the ring and
+      // give it back, also for the key tiles that only the other needs.
       if (elect_one()) {
-        // One chain per row tile: its item, its next tile's number and whether QK or PV is next.
-        // `base` counts the key tiles of the items before; kq, vq: key tiles of all items that
-        // the chain needs no more of the keys, the values.
-        struct Chain {
-          int r, t, nt, item_nt, left0;
-          uint32_t base, n, items, kq, vq;
-          bool pv, done;
-        };
-        Chain ch[2];
-        auto next_item = [&](Chain& c, int h) {
-          for (;; ++c.r) {
-            const int item = sched_item(S, s_list, c.r);
-            if (item < 0) {
-              c.done = true;
-              c.kq = c.vq = 0xffffffffu;
-              return;
-            }
-            const Tile x = tile_at(p, item / p.heads);
-            c.nt = key_tiles(x, h);
-            c.item_nt = max(key_tiles(x, 0), key_tiles(x, 1));
-            c.left0 = x.nk;
-            c.kq = c.vq = c.base;
-            if (c.nt > 0) break;
-            c.base += static_cast<uint32_t>(c.item_nt);
-          }
-          c.t = 0;
-          c.pv = false;
-        };
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ch[h].r = 0;
-          ch[h].base = ch[h].n = ch[h].items = 0;
-          ch[h].done = false;
-          next_item(ch[h], h);
-        }
-        uint32_t k_rel = 0, v_rel = 0;  // key tiles whose slots have been given back
-        uint32_t landed = 0;            // slots that have been filled
-        const uint32_t ring_lo = desc_lo(smem_u32(smem + kOffRing), 0);
+        const int h = warp >> 1;
+        const uint32_t t_s = tmem + kBN * h, t_o = tmem + 256 + kValue * h;
+        const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ + h * kQChunks * kSlot), 0);
+        const uint32_t ring_k = desc_lo(smem_u32(smem + kOffRing), 0);
         const uint32_t ring_v = desc_lo(smem_u32(smem + kOffRing), kSlot / 2);
-        uint64_t t0 = 0;
-        uint32_t idle = 0;
-        while (!(ch[0].done && ch[1].done)) {
-          bool worked = false;
-          // in order, so that no slot's barrier is asked for a phase ahead of its next one
-          if (mbar_test(&full[landed % kSlots], (landed / kSlots) & 1)) {
-            ++landed;
-            worked = true;
-          }
+        uint32_t n = 0;             // key tiles of this row tile
+        uint32_t slot = 0, ph = 0;  // the ring's next slot and its phase
+        uint32_t items = 0;
+        bool ok = true;
+        auto next = [&]() {
+          if (++slot == kSlots) slot = 0, ph ^= 1;
+        };
+        int item;
+        for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
+          const Tile x = tile_at(p, item / p.heads);
+          const int nt = key_tiles(x, h), all = max(nt, key_tiles(x, 1 - h));
+          if (nt > 0) ok = wait_phase(&q_full[h], items & 1, s_abort);
+#pragma unroll 1
+          for (int t = 0; ok && t < all; ++t) {
+            if (t >= nt) {
+#pragma unroll 1
+              for (int s = 0; ok && s < kTileSlots; ++s) {
+                ok = wait_phase(&full[slot], ph, s_abort);
+                mbar_arrive(&empty[slot]);
+                next();
+              }
+              continue;
+            }
+            // S_h = Q_h K^T, over P_h once the last PV_h has read it
+            ok = n == 0 || wait_phase(&pv_done[h], (n - 1) & 1, s_abort);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            Chain& c = ch[h];
-            if (c.done) continue;
-            const uint32_t tile = c.base + static_cast<uint32_t>(c.t);
-            const uint32_t first = tile * kTileSlots;  // its first slot's number
-            if (!c.pv) {
-              // S_h = Q_h K^T, over P_h once the last PV_h has read it
-              if (!(c.n == 0 || mbar_test(&pv_done[h], (c.n - 1) & 1))) continue;
-              if (c.t == 0 && !mbar_test(&q_full[h], c.items & 1)) continue;
-              if (landed < first + kQChunks) continue;
+            for (int s = 0; s < kQChunks; ++s) {
+              ok = ok && wait_phase(&full[slot], ph, s_abort);
+              if (!ok) break;
               tc_fence_after();
-              const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ + h * kQChunks * kSlot), 0);
-#pragma unroll
-              for (int s = 0; s < kQChunks; ++s)
-                umma4_ss(tmem + kBN * h, q_lo + ((s * kSlot) >> 4),
-                         ring_lo + ((((first + s) % kSlots) * kSlot) >> 4), kIdescS, s > 0 ? 1u : 0u);
-              umma_commit(&s_full[h]);
-              c.pv = true;
-              if (c.t + 1 == c.nt) umma_commit(&q_empty[h]);
-              c.kq = c.t + 1 == c.nt ? c.base + static_cast<uint32_t>(c.item_nt) : tile + 1;
-            } else {
-              // O_h += P_h V
-              if (!mbar_test(&p_full[h], c.n & 1)) continue;
-              if (c.t == 0 && c.items > 0 && !mbar_test(&o_free[h], (c.items - 1) & 1)) continue;
-              if (landed < first + kTileSlots) continue;
-              const uint32_t v0 = first + kQChunks, v1 = v0 + 1;
+              umma4_ss(t_s, q_lo + ((s * kSlot) >> 4), ring_k + ((slot * kSlot) >> 4), kIdescS,
+                       s > 0 ? 1u : 0u);
+              umma_commit(&empty[slot]);
+              next();
+            }
+            if (!ok) break;
+            umma_commit(&s_full[h]);
+            if (t + 1 == nt) umma_commit(&q_empty[h]);
+            // O_h += P_h V
+            ok = t > 0 || items == 0 || wait_phase(&o_free[h], (items - 1) & 1, s_abort);
+            const int left = x.nk - t * kBN;
+            const int steps = left >= kBN ? 8 : (left + 15) >> 4;
+#pragma unroll 1
+            for (int v = 0; ok && v < 2; ++v) {
+              ok = wait_phase(&full[slot], ph, s_abort) &&
+                   wait_phase(&p_full[2 * h + v], n & 1, s_abort);
+              if (!ok) break;
               tc_fence_after();
-              const int left = c.left0 - c.t * kBN;
-              const int steps = left >= kBN ? 8 : (left + 15) >> 4;
-              const uint32_t d = tmem + 256 + kValue * h, a = tmem + kBN * h;
-              const uint32_t b0 = ring_v + (((v0 % kSlots) * kSlot) >> 4);
-              const uint32_t b1 = ring_v + (((v1 % kSlots) * kSlot) >> 4);
-              const uint32_t acc = c.t > 0 ? 1u : 0u;
-              if (steps == 8) {
-                umma4_ts(d, a, b0, kIdescO, acc);
-                umma4_ts(d, a + 32, b1, kIdescO, 1u);
+              const uint32_t b = ring_v + ((slot * kSlot) >> 4);
+              const uint32_t a = t_s + 32 * v;
+              const uint32_t acc = t > 0 || v > 0 ? 1u : 0u;
+              const int k_n = steps - 4 * v;
+              if (k_n >= 4) {
+                umma4_ts(t_o, a, b, kIdescO, acc);
               } else {
 #pragma unroll 1
-                for (int k = 0; k < steps; ++k) {
-                  const uint64_t bd = (static_cast<uint64_t>(kDescHi) << 32) |
-                                      ((k < 4 ? b0 : b1) + 128u * (k & 3));
-                  umma_bf16_ts(d, a + 8 * k, bd, kIdescO, acc | (k > 0 ? 1u : 0u));
-                }
+                for (int k = 0; k < k_n; ++k)
+                  umma_bf16_ts(t_o, a + 8 * k, (static_cast<uint64_t>(kDescHi) << 32) | (b + 128u * k),
+                               kIdescO, acc | (k > 0 ? 1u : 0u));
               }
-              umma_commit(&pv_done[h]);
-              ++c.n;
-              c.pv = false;
-              const bool last = ++c.t == c.nt;
-              c.vq = last ? c.base + static_cast<uint32_t>(c.item_nt) : tile + 1;
-              if (last) {
-                c.base += static_cast<uint32_t>(c.item_nt);
-                ++c.r;
-                ++c.items;
-                next_item(c, h);
-              }
+              umma_commit(&empty[slot]);
+              next();
             }
-            worked = true;
+            if (ok) umma_commit(&pv_done[h]);
+            ++n;
           }
-          if (ch[0].done && ch[1].done) break;
-          // slots that neither chain needs any more go back once the products issued are done
-          for (; k_rel < min(ch[0].kq, ch[1].kq); ++k_rel)
-            for (int s = 0; s < kQChunks; ++s) umma_commit(&empty[(k_rel * kTileSlots + s) % kSlots]);
-          for (; v_rel < min(ch[0].vq, ch[1].vq); ++v_rel)
-            for (int s = kQChunks; s < kTileSlots; ++s)
-              umma_commit(&empty[(v_rel * kTileSlots + s) % kSlots]);
-          if (worked) {
-            idle = 0;
-            continue;
-          }
-          if (idle++ == 0) t0 = global_timer_ns();
-          if ((idle & 63u) == 0 && (*s_abort || global_timer_ns() - t0 > kWaitLimitNs)) {
-            *s_abort = 1;
-            break;
-          }
+          if (nt > 0) ++items;
         }
+        if (!ok) *s_abort = 1;
       }
     }
   } else {
@@ -469,7 +445,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       float m_run = -INFINITY;  // the maximum that the weights refer to, raw score units
       float l_run = 0.f;
       for (int t = 0; t < nt; ++t, ++n) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[h], n & 1, s_abort));
+        ok = __all_sync(0xffffffffu, wait_phase(&s_full[h], n & 1, s_abort));
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[128];
@@ -492,11 +468,6 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         const float m_use = grow ? m_cand : m_run;
         const float alpha = grow ? ex2((m_run - m_use) * p.qscale) : 1.f;  // 0 if m_run = -inf
         const float neg_m = m_use == -INFINITY ? 0.f : -m_use * p.qscale;
-        // P over the first 64 columns of S_h, in bf16 (a weight off by at most 2^-8 of itself;
-        // the sum takes it unrounded)
-        const float psum = softmax_row_to_tmem(sr, p.qscale, neg_m, t_s);
-        l_run = l_run * alpha + psum;
-        m_run = m_use;
         // (S_h of this tile was issued after the last PV_h had completed: O_h is at rest)
         if (t > 0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
@@ -509,13 +480,23 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             tmem_st32(t_o + q, o);
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[h]);
+        // P over the first 64 columns of S_h, in bf16 (a weight off by at most 2^-8 of itself;
+        // the sum takes it unrounded), the first 64 keys' first: their product with V runs while
+        // the others' weights are computed.
+        l_run *= alpha;
+        m_run = m_use;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          l_run += weights_to_tmem(reinterpret_cast<const uint32_t(&)[64]>(sr[64 * v]), p.qscale, neg_m,
+                                   t_s + 32 * v);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * h + v]);
+        }
       }
       // ---- O / l, LSE ----
-      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[h], (n - 1) & 1, s_abort));
+      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_phase(&pv_done[h], (n - 1) & 1, s_abort));
       if (!ok) break;
       tc_fence_after();
       const bool has = live && l_run > 0.f;
