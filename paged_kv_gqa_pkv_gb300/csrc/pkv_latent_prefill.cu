@@ -43,9 +43,13 @@ constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks]
 constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
 // full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_free[2], tail
-constexpr int kNumBars = 2 * kSlots + 15;
+// item_full[4], item_free[4]
+constexpr int kAheadItems = 4;
+constexpr int kNumBars = 2 * kSlots + 15 + 2 * kAheadItems;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
-constexpr int kOffSched = kOffMisc + 8;
+constexpr int kOffItem = kOffMisc + 8;
+constexpr int kItemInts = 8;
+constexpr int kOffSched = kOffItem + kAheadItems * kItemInts * 4;
 constexpr int kExpSmem = kOffSched + kSchedBytes + 1024;  // + slack for the alignment
 static_assert(kExpSmem <= kMaxDynSmem, "shared memory above the opt-in limit");
 static_assert(kSlots * kSlot >= kSchedScratchBytes, "schedule scratch lives in the ring");
@@ -177,6 +181,35 @@ __device__ __forceinline__ Tile tile_at(const LatentPrefillParams& p, int place)
   t.see = t.nk - (q1 - q0) + i0 + 1;
   return t;
 }
+// Looking an item's tile up takes a bisection through global memory, ~1500 cycles beside the
+// softmax warps. Warp 2 does it for the items to come and leaves them in a ring in shared memory;
+// every role reads them there. readers: the loads, two issuing threads, eight softmax warps.
+constexpr int kItemReaders = 11;
+struct Item {
+  Tile x;
+  int head;  // -1: no more items
+};
+struct ItemReader {
+  const int* ring;
+  uint64_t* full;
+  uint64_t* free;
+  int r = 0;
+  // By a whole warp, or by one thread alone.
+  template <bool kWarp>
+  __device__ __forceinline__ bool next(Item* it, volatile int* abort_flag, bool* ok) {
+    const int at = r % kAheadItems;
+    *ok = wait_phase(&full[at], (r / kAheadItems) & 1, abort_flag);
+    if (kWarp) *ok = __all_sync(0xffffffffu, *ok);
+    if (!*ok) return false;
+    const int* v = ring + at * kItemInts;
+    it->x.q0 = v[0], it->x.rows = v[1], it->x.k0 = v[2], it->x.nk = v[3], it->x.see = v[4];
+    it->head = v[5];
+    if (kWarp) __syncwarp();
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&free[at]);
+    ++r;
+    return it->head >= 0;
+  }
+};
 // Key tiles that row tile h of an item reads (0: none, or no rows).
 __device__ __forceinline__ int key_tiles(const Tile& t, int h) {
   const int last = min(t.rows, kBM * (h + 1)) - 1;  // its last row
@@ -204,6 +237,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* pv_done = p_full + 4;
   uint64_t* o_free = pv_done + 2;  // the epilogue has read O_h
   uint64_t* tail = o_free + 2;     // values of a tile past whose last key there are others' rows
+  uint64_t* item_full = tail + 1;              // [4]
+  uint64_t* item_free = item_full + kAheadItems;  // [4]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
 
@@ -225,6 +260,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_init(&o_free[h], 4);
     }
     mbar_init(tail, 1);
+    for (int i = 0; i < kAheadItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_free[i], kItemReaders);
+    }
     *s_abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&qmap);
@@ -261,6 +300,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       });
   fence_proxy_async_smem();  // (the scratch's place goes to TMA)
   __syncthreads();
+  int* const s_items = reinterpret_cast<int*>(smem + kOffItem);
+  ItemReader items_ahead{s_items, item_full, item_free};
+  Item it;
 
   // 384 threads start with 168 registers each; the softmax warps need more, the others few.
   if (warp < 4) {
@@ -269,10 +311,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       // ------------------------------------------ keys and values ----
       uint32_t n = 0, tails = 0;  // slots filled, tiles with a tail
       bool ok = true;
-      int item;
-      for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
-        const int place = item / p.heads, head = item - place * p.heads;
-        const Tile x = tile_at(p, place);
+      while (items_ahead.next<true>(&it, s_abort, &ok)) {
+        const Tile& x = it.x;
+        const int head = it.head;
         const int nt = max(key_tiles(x, 0), key_tiles(x, 1));
         for (int t = 0; ok && t < nt; ++t) {
           const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
@@ -316,28 +357,50 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) *s_abort = 1;
     } else if (warp == 2) {
-      // ---------------------------------------------------- queries ----
+      // ------------------------------------- items to come, queries ----
       if (lane == 0) {
+        // an item's queries are loaded two items after it has been looked up
+        Item cur, one_back, two_back;
+        one_back.head = two_back.head = -1;
         uint32_t n[2] = {0u, 0u};
-        bool ok = true;
-        int item;
-        for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
-          const int place = item / p.heads, head = item - place * p.heads;
-          const Tile x = tile_at(p, place);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (key_tiles(x, h) == 0 || !ok) continue;
-            ok = n[h] == 0 || wait_phase(&q_empty[h], (n[h] - 1) & 1, s_abort);
+        bool ok = true, more = true;
+        for (int r = 0; ok && (more || one_back.head >= 0 || two_back.head >= 0); ++r) {
+          cur.head = -1;
+          if (more) {
+            const int at = r % kAheadItems;
+            ok = r < kAheadItems || wait_phase(&item_free[at], (r / kAheadItems - 1) & 1, s_abort);
             if (!ok) break;
-            mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
-            for (int c = 0; c < kQChunks; ++c)
-              tma_load_3d(smem + kOffQ + (h * kQChunks + c) * kSlot, &qmap, &q_full[h], 64 * c,
-                          head, x.q0 + kBM * h);
-            ++n[h];
+            const int item = sched_item(S, s_list, r);
+            int* v = s_items + at * kItemInts;
+            if (item >= 0) {
+              const int place = item / p.heads;
+              cur.head = item - place * p.heads;
+              cur.x = tile_at(p, place);
+              v[0] = cur.x.q0, v[1] = cur.x.rows, v[2] = cur.x.k0, v[3] = cur.x.nk, v[4] = cur.x.see;
+            }
+            v[5] = cur.head;
+            mbar_arrive(&item_full[at]);
+            more = item >= 0;
           }
+          if (two_back.head >= 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!ok || key_tiles(two_back.x, h) == 0) continue;
+              ok = n[h] == 0 || wait_phase(&q_empty[h], (n[h] - 1) & 1, s_abort);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
+              for (int c = 0; c < kQChunks; ++c)
+                tma_load_3d(smem + kOffQ + (h * kQChunks + c) * kSlot, &qmap, &q_full[h], 64 * c,
+                            two_back.head, two_back.x.q0 + kBM * h);
+              ++n[h];
+            }
+          }
+          two_back = one_back;
+          one_back = cur;
         }
         if (!ok) *s_abort = 1;
       }
@@ -359,9 +422,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         auto next = [&]() {
           if (++slot == kSlots) slot = 0, ph ^= 1;
         };
-        int item;
-        for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
-          const Tile x = tile_at(p, item / p.heads);
+        while (ok && items_ahead.next<false>(&it, s_abort, &ok)) {
+          const Tile& x = it.x;
           const int nt = key_tiles(x, h), all = max(nt, key_tiles(x, 1 - h));
           if (nt > 0) ok = wait_phase(&q_full[h], items & 1, s_abort);
 #pragma unroll 1
@@ -434,10 +496,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t t_o = t_lane + 256 + kValue * h;
     uint32_t n = 0;
     bool ok = true;
-    int item;
-    for (int r = 0; ok && (item = sched_item(S, s_list, r)) >= 0; ++r) {
-      const int place = item / p.heads, head = item - place * p.heads;
-      const Tile x = tile_at(p, place);
+    while (ok && items_ahead.next<true>(&it, s_abort, &ok)) {
+      const Tile& x = it.x;
+      const int head = it.head;
       const int nt = key_tiles(x, h);
       const int i = kBM * h + row;  // of the item
       const bool live = i < x.rows;
