@@ -11,7 +11,7 @@
 // cycles at their rate; the 65 536 exponentials take 1024 to 2048. So the tensor pipe is the
 // bound, if each tile's softmax is hidden behind the other's products.
 //
-// Roles of a CTA (one per SM, items dealt by cost): warp 0 loads keys and values by TMA into a
+// Roles of a CTA (one per SM; it takes item after item, the costly ones first): warp 0 loads keys and values by TMA into a
 // ring of eight 16 KB slots (K: three slots of 64 dims x 128 keys, V: two of 64 keys), warp 2
 // the queries, one thread each of warps 1 and 3 issues the MMAs of one tile, warps 4-7 and 8-11
 // are the softmax of the two tiles, a query row per thread. Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each);
@@ -43,16 +43,18 @@ constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks]
 constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
 // full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_free[2], tail
-// item_full[4], item_free[4]
+// item_full[4], item_free[4], claim
 constexpr int kAheadItems = 4;
-constexpr int kNumBars = 2 * kSlots + 15 + 2 * kAheadItems;
+constexpr int kNumBars = 2 * kSlots + 15 + 2 * kAheadItems + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
-constexpr int kOffItem = kOffMisc + 8;
+constexpr int kOffItem = kOffMisc + 16;
 constexpr int kItemInts = 8;
-constexpr int kOffSched = kOffItem + kAheadItems * kItemInts * 4;
-constexpr int kExpSmem = kOffSched + kSchedBytes + 1024;  // + slack for the alignment
+constexpr int kOffClaim = kOffItem + kAheadItems * kItemInts * 4;  // 16 bytes
+constexpr int kOffSched = kOffClaim + 16;
+constexpr int kExpSmem = kOffSched + kSchedMaxTiles * 2 + 1024;  // + slack for the alignment
 static_assert(kExpSmem <= kMaxDynSmem, "shared memory above the opt-in limit");
-static_assert(kSlots * kSlot >= kSchedScratchBytes, "schedule scratch lives in the ring");
+static_assert(kSlots * kSlot >= kSchedSortBytes, "the sort's scratch lives in the ring");
+static_assert(kOffClaim % 16 == 0, "a claim's answer is 16-byte aligned");
 
 constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kBM, kValue, true);
@@ -181,6 +183,30 @@ __device__ __forceinline__ Tile tile_at(const LatentPrefillParams& p, int place)
   t.see = t.nk - (q1 - q0) + i0 + 1;
   return t;
 }
+// Takes the item of a block that has not started yet: its index, or -1 if there is none (no claim
+// may follow that answer). answer: 16 bytes of shared memory.
+__device__ __forceinline__ int claim_block(void* answer, uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag, bool* ok) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+  *ok = wait_phase(bar, parity, abort_flag);
+  if (!*ok) return -1;
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tmov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  fence_proxy_async_smem();  // (the next answer is written by the async proxy)
+  return x;
+}
+
 // Looking an item's tile up takes a bisection through global memory, ~1500 cycles beside the
 // softmax warps. Warp 2 does it for the items to come and leaves them in a ring in shared memory;
 // every role reads them there. readers: the loads, two issuing threads, eight softmax warps.
@@ -239,6 +265,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* tail = o_free + 2;     // values of a tile past whose last key there are others' rows
   uint64_t* item_full = tail + 1;              // [4]
   uint64_t* item_free = item_full + kAheadItems;  // [4]
+  uint64_t* claim = item_free + kAheadItems;      // the answer to a claim has arrived
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
 
@@ -260,6 +287,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_init(&o_free[h], 4);
     }
     mbar_init(tail, 1);
+    mbar_init(claim, 1);
     for (int i = 0; i < kAheadItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_free[i], kItemReaders);
@@ -278,26 +306,28 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   const uint32_t tmem = *tmem_slot;
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (blockIdx.x == 0) {
-    // starts have to ascend from 0 or more to the tokens there are
-    for (int i = threadIdx.x; i <= p.n_seqs; i += kExpThreads) {
-      const int q = __ldg(p.q_starts + i), k = __ldg(p.k_starts + i);
-      const int qb = i > 0 ? __ldg(p.q_starts + i - 1) : 0, kb = i > 0 ? __ldg(p.k_starts + i - 1) : 0;
-      if (q < qb || q > p.tq || k < kb || k > p.tk) set_dev_err(p.dev_err, PKV_DEV_ERR_LAYOUT);
-    }
+  // starts have to ascend from 0 or more to the tokens there are (which blocks run is not known)
+  for (int i = threadIdx.x; i <= p.n_seqs; i += kExpThreads) {
+    const int q = __ldg(p.q_starts + i), k = __ldg(p.k_starts + i);
+    const int qb = i > 0 ? __ldg(p.q_starts + i - 1) : 0, kb = i > 0 ? __ldg(p.k_starts + i - 1) : 0;
+    if (q < qb || q > p.tq || k < kb || k > p.tk) set_dev_err(p.dev_err, PKV_DEV_ERR_LAYOUT);
   }
-  const uint16_t* s_list = reinterpret_cast<const uint16_t*>(smem + kOffSched);
-  const ItemSched S = sched_build(
-      reinterpret_cast<uint16_t*>(smem + kOffSched), smem + kOffRing, p.n_tiles, p.heads,
-      [&](int t) -> int {
-        const Tile x = tile_at(p, t);
-        // (an item's queries, first products and results take about 1.5 key tiles' time)
-        return x.rows == 0 ? 0 : 2 * max(key_tiles(x, 0), key_tiles(x, 1)) + 3;
-      },
-      [&](int t) -> bool {  // the next place goes on in the same sequence
-        const Tile x = tile_at(p, t), y = tile_at(p, t + 1);
-        return x.rows > 0 && y.rows > 0 && y.k0 == x.k0 && y.q0 == x.q0 + kItemRows;
-      });
+  // the places, the costly ones first, a sequence's together (as they stand where they are too
+  // many to sort)
+  uint16_t* const s_order = reinterpret_cast<uint16_t*>(smem + kOffSched);
+  const bool sorted = p.n_tiles > 1 && p.n_tiles <= kSchedMaxTiles;
+  if (sorted)
+    sched_sort(
+        s_order, smem + kOffRing, p.n_tiles,
+        [&](int t) -> int {
+          const Tile x = tile_at(p, t);
+          // (an item's queries, first products and results take about 1.5 key tiles' time)
+          return x.rows == 0 ? 0 : 2 * max(key_tiles(x, 0), key_tiles(x, 1)) + 3;
+        },
+        [&](int t) -> bool {  // the next place goes on in the same sequence
+          const Tile x = tile_at(p, t), y = tile_at(p, t + 1);
+          return x.rows > 0 && y.rows > 0 && y.k0 == x.k0 && y.q0 == x.q0 + kItemRows;
+        });
   fence_proxy_async_smem();  // (the scratch's place goes to TMA)
   __syncthreads();
   int* const s_items = reinterpret_cast<int*>(smem + kOffItem);
@@ -363,44 +393,39 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     } else if (warp == 2) {
       // ------------------------------------- items to come, queries ----
       if (lane == 0) {
-        // an item's queries are loaded two items after it has been looked up
-        Item cur, one_back, two_back;
-        one_back.head = two_back.head = -1;
+        // The grid has a block for every item; a CTA that is running takes the items of blocks
+        // that have not started, one when all its roles have begun the one before.
         uint32_t n[2] = {0u, 0u};
-        bool ok = true, more = true;
-        for (int r = 0; ok && (more || one_back.head >= 0 || two_back.head >= 0); ++r) {
-          cur.head = -1;
-          if (more) {
-            const int at = r % kAheadItems;
-            ok = r < kAheadItems || wait_phase(&item_free[at], (r / kAheadItems - 1) & 1, s_abort);
-            if (!ok) break;
-            const int item = sched_item(S, s_list, r);
-            int* v = s_items + at * kItemInts;
-            if (item >= 0) {
-              const int place = item / p.heads;
-              cur.head = item - place * p.heads;
-              cur.x = tile_at(p, place);
-              v[0] = cur.x.q0, v[1] = cur.x.rows, v[2] = cur.x.k0, v[3] = cur.x.nk, v[4] = cur.x.see;
-            }
-            v[5] = cur.head;
-            mbar_arrive(&item_full[at]);
-            more = item >= 0;
+        bool ok = true;
+        int item = blockIdx.x;
+        for (int r = 0; ok; ++r) {
+          const int at = r % kAheadItems;
+          int* v = s_items + at * kItemInts;
+          Tile x;
+          x.rows = 0;
+          int head = -1;
+          if (item >= 0) {
+            const int pos = item / p.heads;
+            head = item - pos * p.heads;
+            x = tile_at(p, sorted ? s_order[pos] : pos);
+            v[0] = x.q0, v[1] = x.rows, v[2] = x.k0, v[3] = x.nk, v[4] = x.see;
           }
-          if (two_back.head >= 0) {
+          v[5] = head;
+          mbar_arrive(&item_full[at]);
+          if (item < 0) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!ok || key_tiles(two_back.x, h) == 0) continue;
-              ok = n[h] == 0 || wait_phase(&q_empty[h], (n[h] - 1) & 1, s_abort);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
-              for (int c = 0; c < kQChunks; ++c)
-                tma_load_3d(smem + kOffQ + (h * kQChunks + c) * kSlot, &qmap, &q_full[h], 64 * c,
-                            two_back.head, two_back.x.q0 + kBM * h);
-              ++n[h];
-            }
+          for (int h = 0; h < 2; ++h) {
+            if (!ok || key_tiles(x, h) == 0) continue;
+            ok = n[h] == 0 || wait_phase(&q_empty[h], (n[h] - 1) & 1, s_abort);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[h], kQChunks * kSlot);
+            for (int c = 0; c < kQChunks; ++c)
+              tma_load_3d(smem + kOffQ + (h * kQChunks + c) * kSlot, &qmap, &q_full[h], 64 * c, head,
+                          x.q0 + kBM * h);
+            ++n[h];
           }
-          two_back = one_back;
-          one_back = cur;
+          ok = ok && wait_phase(&item_free[at], (r / kAheadItems) & 1, s_abort);
+          if (ok) item = claim_block(smem + kOffClaim, claim, r & 1, s_abort, &ok);
         }
         if (!ok) *s_abort = 1;
       }
@@ -699,7 +724,7 @@ extern "C" pkv_status pkv_latent_prefill_attention(
   p.qscale = scale * 1.4426950408889634f;
   const long long items = places * num_heads;
   return record_cuda_status(launch_kernel(latent_prefill_kernel,
-                                          dim3(static_cast<unsigned>(items < sms ? items : sms)),
+                                          dim3(static_cast<unsigned>(items)),
                                           dim3(kExpThreads), kExpSmem, stream, true, qmap, kmap, rmap,
                                           vmap, p));
 }

@@ -355,23 +355,19 @@ __device__ __forceinline__ void sched_fill_list(uint16_t* list, const uint16_t* 
   }
 }
 
-// Called by every thread of the CTA (it holds block barriers). cost(t) is the
-// estimated cost of tile t (clamped to [0, kSchedMaxCost]); link(t) says that
-// tile t + 1 continues tile t's last run (t + 1 < n_tiles). scratch holds
-// kSchedScratchBytes that nothing else uses until this returns; list gets
-// this CTA's items.
+// The tiles in that order: called by every thread of the CTA (it holds block barriers), 1 <
+// n_tiles <= kSchedMaxTiles. cost(t) is the estimated cost of tile t (clamped to [0,
+// kSchedMaxCost]); link(t) says that tile t + 1 continues tile t's last run (t + 1 < n_tiles).
+// scratch holds kSchedSortBytes that nothing else uses until this returns. Warp 0 has written
+// order[0..n_tiles) when it returns; the other warps see it behind another barrier.
+constexpr int kSchedSortBytes = 1024 + 3 * kSchedMaxTiles;
 template <class CostFn, class LinkFn>
-__device__ ItemSched sched_build(uint16_t* list, uint8_t* scratch, int n_tiles,
-                                 int items_per_tile, CostFn cost, LinkFn link) {
-  ItemSched s;
-  s.listed = false;
-  s.n_items = n_tiles * items_per_tile;
-  if (!sched_fits(n_tiles, s.n_items)) return s;
+__device__ void sched_sort(uint16_t* order, uint8_t* scratch, int n_tiles, CostFn cost,
+                           LinkFn link) {
   int* hist = reinterpret_cast<int*>(scratch);     // [256], bin = kSchedMaxCost - key
   uint8_t* tcost = scratch + 1024;                 // [n_tiles]
   uint8_t* tlink = tcost + kSchedMaxTiles;         // [n_tiles]
   uint8_t* bin = tlink + kSchedMaxTiles;           // [n_tiles]
-  uint16_t* order = reinterpret_cast<uint16_t*>(bin + kSchedMaxTiles);  // [n_tiles]
   for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
   for (int t = threadIdx.x; t < n_tiles; t += blockDim.x) {
     tcost[t] = static_cast<uint8_t>(min(max(cost(t), 0), kSchedMaxCost));
@@ -425,8 +421,22 @@ __device__ ItemSched sched_build(uint16_t* list, uint8_t* scratch, int n_tiles,
       if (valid && lane == leader) hist[k] = base + __popc(peers);
       __syncwarp();
     }
-    sched_fill_list(list, order, s.n_items, items_per_tile, lane);
   }
+}
+
+// Called by every thread of the CTA (it holds block barriers); cost and link as for sched_sort.
+// scratch holds kSchedScratchBytes that nothing else uses until this returns; list gets this
+// CTA's items.
+template <class CostFn, class LinkFn>
+__device__ ItemSched sched_build(uint16_t* list, uint8_t* scratch, int n_tiles,
+                                 int items_per_tile, CostFn cost, LinkFn link) {
+  ItemSched s;
+  s.listed = false;
+  s.n_items = n_tiles * items_per_tile;
+  if (!sched_fits(n_tiles, s.n_items)) return s;
+  uint16_t* order = reinterpret_cast<uint16_t*>(scratch + kSchedSortBytes);  // [n_tiles]
+  sched_sort(order, scratch, n_tiles, cost, link);
+  if (threadIdx.x < 32) sched_fill_list(list, order, s.n_items, items_per_tile, threadIdx.x);
   __syncthreads();
   s.listed = true;
   return s;
