@@ -25,6 +25,7 @@ Functions keep the names of the C entry points: ``pkv_append``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -524,8 +525,7 @@ def _result(name: str, t, like: torch.Tensor, dev: int, stream, shape=None, dtyp
     if stream is not None:
         with torch.cuda.stream(stream):
             return _result(name, None, like, dev, None, shape, dtype)
-    t = torch.empty_like(like) if shape is None else \
-        torch.empty(shape, dtype=dtype, device=like.device)
+    t = torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
     return t, t.data_ptr()
 
 
@@ -792,12 +792,18 @@ def pkv_rotate(x, positions, rope_cos, rope_sin, interleaved: bool = False, out=
     return out
 
 
-def latent_cache_desc(pool: torch.Tensor, page_table: torch.Tensor, page_size: int) -> CacheDesc:
-    """The descriptor of a paged cache of shared latents, pool [num_pages * page_size, 576]."""
-    rows, row = pool.shape
+@functools.lru_cache(maxsize=64)
+def _latent_desc(rows: int, row: int, page_size: int, max_batch: int, max_blocks: int):
+    """A latent cache's descriptor and its address, by the cache's sizes."""
     if page_size <= 0 or rows % page_size:
         raise ValueError("pool rows must be a multiple of page_size")
-    return CacheDesc(rows // page_size, page_size, 1, row, page_table.shape[0], page_table.shape[1])
+    desc = CacheDesc(rows // page_size, page_size, 1, row, max_batch, max_blocks)
+    return desc, ctypes.byref(desc)
+
+
+def latent_cache_desc(pool: torch.Tensor, page_table: torch.Tensor, page_size: int) -> CacheDesc:
+    """The descriptor of a paged cache of shared latents, pool [num_pages * page_size, 576]."""
+    return _latent_desc(*pool.shape, int(page_size), *page_table.shape)[0]
 
 
 def _latent_cache(pool, page_table, page_size: int):
@@ -807,7 +813,8 @@ def _latent_cache(pool, page_table, page_size: int):
     dev = pool.get_device()
     if page_table.get_device() != dev:
         raise ValueError(f"page_table: expected a tensor on cuda:{dev}, got {page_table.device}")
-    return dev, latent_cache_desc(pool, page_table, page_size), pool.data_ptr(), page_table.data_ptr()
+    desc_p = _latent_desc(*pool.shape, int(page_size), *page_table.shape)[1]
+    return dev, desc_p, pool.data_ptr(), page_table.data_ptr()
 
 
 def pkv_latent_append(pool, page_table, x_new, batch_idx, input_pos, page_size: int, rope_cos,
@@ -817,7 +824,7 @@ def pkv_latent_append(pool, page_table, x_new, batch_idx, input_pos, page_size: 
     then the position part) into the pool [num_pages * page_size, 576] through the page
     table: the latent normalised with ``norm_weight`` fp32 [512] if given, the position
     part rotated by the fp32 tables [L, 32] at input_pos [N]."""
-    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
+    dev, desc_p, pool_p, table = _latent_cache(pool, page_table, page_size)
     if not isinstance(x_new, torch.Tensor) or x_new.dim() != 2 or x_new.shape[1] != LATENT_ROW:
         raise ValueError(f"x_new must be a tensor [N, {LATENT_ROW}]")
     x_p = _strided("x_new", x_new, dev)
@@ -827,7 +834,7 @@ def pkv_latent_append(pool, page_table, x_new, batch_idx, input_pos, page_size: 
     cos, sin, L = _rope_tables(rope_cos, rope_sin, LATENT_ROTATED // 2, dev)
     w = None if norm_weight is None else \
         _tensor("norm_weight", norm_weight, torch.float32, (LATENT_DIM,), dev)
-    _run("pkv_latent_append", dev, stream, load_library().pkv_latent_append, ctypes.byref(desc),
+    _run("pkv_latent_append", dev, stream, load_library().pkv_latent_append, desc_p,
          pool_p, table, x_p, x_new.stride(0), b, pos, n, cos, sin, L, int(bool(interleaved)), w,
          float(norm_eps), _dev_err(dev_err, dev))
 
@@ -837,13 +844,13 @@ def pkv_latent_gather(pool, page_table, slots, starts, total: int, page_size: in
     """The cached rows of sequences, one after another: row starts[b] + t of the result
     [total, 576] is the row of position t of slot slots[b], t < starts[b + 1] - starts[b].
     Rows that no sequence covers stay as they were. Returns ``out`` (a new one if None)."""
-    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
+    dev, desc_p, pool_p, table = _latent_cache(pool, page_table, page_size)
     _need(slots, "slots", torch.int32, 1)
     n = slots.shape[0]
     slots_p = _tensor("slots", slots, torch.int32, (n,), dev)
     starts_p = _tensor("starts", starts, torch.int32, (n + 1,), dev)
     out, out_p = _result("out", out, pool, dev, stream, (int(total), pool.shape[1]), torch.bfloat16)
-    _run("pkv_latent_gather", dev, stream, load_library().pkv_latent_gather, ctypes.byref(desc), pool_p,
+    _run("pkv_latent_gather", dev, stream, load_library().pkv_latent_gather, desc_p, pool_p,
          table, slots_p, starts_p, n, int(total), out_p, _dev_err(dev_err, dev))
     return out
 
@@ -865,9 +872,9 @@ def pkv_latent_decode_attention(pool, page_table, q, batch_idx, seq_lens, page_s
     n_q of the seq_lens[b] positions of slot batch_idx[b], each sees the rows up to its own
     (appended first). Returns (out [B, n_q, H, 512] bf16, lse [B, n_q, H] fp32), without the
     n_q axis where q has none."""
-    dev, desc, pool_p, table = _latent_cache(pool, page_table, page_size)
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4) or q.shape[-1] != desc.head_dim:
-        raise ValueError(f"q must be a tensor [B, n_q, H, {desc.head_dim}] or [B, H, {desc.head_dim}]")
+    dev, desc_p, pool_p, table = _latent_cache(pool, page_table, page_size)
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4) or q.shape[-1] != LATENT_ROW:
+        raise ValueError(f"q must be a tensor [B, n_q, H, {LATENT_ROW}] or [B, H, {LATENT_ROW}]")
     q_p = _tensor("q", q, torch.bfloat16, q.shape, dev)
     B, H = q.shape[0], q.shape[-2]
     n_q = q.shape[1] if q.dim() == 4 else 1
@@ -876,7 +883,6 @@ def pkv_latent_decode_attention(pool, page_table, q, batch_idx, seq_lens, page_s
     out, out_p = _result("out", out, q, dev, stream, (*q.shape[:-1], LATENT_DIM), torch.bfloat16)
     lse, lse_p = _result("lse", lse, q, dev, stream, q.shape[:-1], torch.float32)
     lib = load_library()
-    desc_p = ctypes.byref(desc)
     _run_with(workspace, lambda: lib.pkv_latent_decode_workspace_size(desc_p, B, n_q, H),
               "pkv_latent_decode_attention", dev, stream, _dev_err(dev_err, dev),
               lib.pkv_latent_decode_attention, desc_p, pool_p, table, *args, out_p, lse_p)

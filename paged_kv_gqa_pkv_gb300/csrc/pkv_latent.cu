@@ -188,89 +188,113 @@ struct LatentAppendParams {
 
 constexpr int kAppendWarps = 8;
 
-// One warp a token: lane l holds the latent's 16-byte pieces l and l + 32, and lanes
-// 0..7 (interleaved) or 0..3 (halves, a piece and its partner) the position part. The
-// squares of all 512 values are summed in fp32 by shuffles; norm and rotation stay in
-// fp32 and each value is rounded to bf16 once.
-template <bool kInterleaved>
+// A warp takes kTokens tokens: lane l holds the latent's 16-byte pieces l and l + 32, and lanes
+// 0..7 (interleaved) or 0..3 (halves, a piece and its partner) the position part. The squares
+// of all 512 values are summed in fp32 by shuffles; norm and rotation stay in fp32 and each
+// value is rounded to bf16 once. What bounds it is the latency of two dependent reads (position,
+// then page and angles) and of the row's: all rows of the warp are read before any is used, and
+// two tokens a warp where there are more than the GPU holds warps (16384 tokens: see launch).
+template <bool kInterleaved, int kTokens>
 __global__ void __launch_bounds__(kAppendWarps * 32)
 latent_append_kernel(const LatentAppendParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  if (i >= p.n_tokens) return;
-  const uint4* src = reinterpret_cast<const uint4*>(p.x + i * p.x_token);
-  // the row's values and the addresses they go to are independent: all loads first
-  const int b = __ldg(p.batch_idx + i);
-  const int pos = __ldg(p.input_pos + i);
-  const uint4 v0 = __ldg(src + lane);
-  const uint4 v1 = __ldg(src + 32 + lane);
+  const int first = (blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * kTokens;
+  if (first >= p.n_tokens) return;
   constexpr int kTurners = kInterleaved ? 8 : 4;
-  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-  if (lane < kTurners) {
-    r0 = __ldg(src + 64 + lane);
-    if (!kInterleaved) r1 = __ldg(src + 68 + lane);
-  }
-  if (b == 0) return;  // padding
-  int err = 0;
-  if (b < 0 || b >= p.max_batch) err |= PKV_DEV_ERR_BAD_SLOT;
-  const int block = pos / p.page_size;
-  if (pos < 0 || block >= p.max_blocks || pos >= p.rope_len) err |= PKV_DEV_ERR_BAD_POS;
-  int page = -1;
-  if (!err) {
-    page = __ldg(p.page_table + static_cast<long long>(b) * p.max_blocks + block);
-    if (page < 0 || page >= p.num_pages) err |= PKV_DEV_ERR_BAD_PAGE;
-  }
-  if (err) {
-    if (lane == 0) set_dev_err(p.dev_err, err);
-    return;
-  }
-  uint4* dst = reinterpret_cast<uint4*>(
-      p.pool + (static_cast<long long>(page) * p.page_size + pos % p.page_size) * kRow);
-  if (p.norm_weight == nullptr) {
-    dst[lane] = v0;
-    dst[32 + lane] = v1;
-  } else {
-    float x[8], y[8];
-    unpack8(v0, x);
-    unpack8(v1, y);
-    float ss = 0.f;
+  int slot[kTokens], pos[kTokens];
+  uint4 v0[kTokens], v1[kTokens], r0[kTokens], r1[kTokens];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], fmaf(y[u], y[u], ss));
+  for (int k = 0; k < kTokens; ++k) {
+    const int i = min(first + k, p.n_tokens - 1);
+    slot[k] = __ldg(p.batch_idx + i);
+    pos[k] = __ldg(p.input_pos + i);
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + i * p.x_token);
+    v0[k] = __ldg(src + lane);
+    v1[k] = __ldg(src + 32 + lane);
+    r0[k] = r1[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < kTurners) {
+      r0[k] = __ldg(src + 64 + lane);
+      if (!kInterleaved) r1[k] = __ldg(src + 68 + lane);
+    }
+  }
+  int page[kTokens];
+  float4 c[kTokens][2], s[kTokens][2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(ss * (1.f / kLatent) + p.norm_eps);
+  for (int k = 0; k < kTokens; ++k) {
+    page[k] = -1;
+    if (first + k >= p.n_tokens || slot[k] == 0) continue;  // (slot 0: padding)
+    int err = 0;
+    if (slot[k] < 0 || slot[k] >= p.max_batch) err |= PKV_DEV_ERR_BAD_SLOT;
+    const int block = pos[k] / p.page_size;
+    if (pos[k] < 0 || block >= p.max_blocks || pos[k] >= p.rope_len) err |= PKV_DEV_ERR_BAD_POS;
+    if (!err) {
+      page[k] = __ldg(p.page_table + static_cast<long long>(slot[k]) * p.max_blocks + block);
+      if (lane < kTurners) {
+        const long long at = static_cast<long long>(pos[k]) * (kRotated / 2);
+        const float4* c4 = reinterpret_cast<const float4*>(p.rope_cos + at);
+        const float4* s4 = reinterpret_cast<const float4*>(p.rope_sin + at);
+        if (kInterleaved) {
+          c[k][0] = __ldg(c4 + lane);
+          s[k][0] = __ldg(s4 + lane);
+        } else {
+          c[k][0] = __ldg(c4 + 2 * lane), c[k][1] = __ldg(c4 + 2 * lane + 1);
+          s[k][0] = __ldg(s4 + 2 * lane), s[k][1] = __ldg(s4 + 2 * lane + 1);
+        }
+      }
+      if (page[k] < 0 || page[k] >= p.num_pages) {
+        err = PKV_DEV_ERR_BAD_PAGE;
+        page[k] = -1;
+      }
+    }
+    if (err && lane == 0) set_dev_err(p.dev_err, err);
+  }
+  if (p.norm_weight != nullptr) {
     const float4* w = reinterpret_cast<const float4*>(p.norm_weight);
     const float4 wa = __ldg(w + 2 * lane), wb = __ldg(w + 2 * lane + 1);
     const float4 wc = __ldg(w + 64 + 2 * lane), wd = __ldg(w + 64 + 2 * lane + 1);
     const float w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
     const float w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      x[u] = (x[u] * inv) * w0[u];
-      y[u] = (y[u] * inv) * w1[u];
+    for (int k = 0; k < kTokens; ++k) {
+      float x[8], y[8];
+      unpack8(v0[k], x);
+      unpack8(v1[k], y);
+      float ss = 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], fmaf(y[u], y[u], ss));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss * (1.f / kLatent) + p.norm_eps);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        x[u] = (x[u] * inv) * w0[u];
+        y[u] = (y[u] * inv) * w1[u];
+      }
+      v0[k] = pack8(x);
+      v1[k] = pack8(y);
     }
-    dst[lane] = pack8(x);
-    dst[32 + lane] = pack8(y);
   }
-  if (lane < kTurners) {
-    const float4* c4 =
-        reinterpret_cast<const float4*>(p.rope_cos + static_cast<long long>(pos) * (kRotated / 2));
-    const float4* s4 =
-        reinterpret_cast<const float4*>(p.rope_sin + static_cast<long long>(pos) * (kRotated / 2));
-    float x[8], y[8];
-    unpack8(r0, x);
-    if (kInterleaved) {
-      turn_pairs(x, __ldg(c4 + lane), __ldg(s4 + lane));
-      dst[64 + lane] = pack8(x);
-    } else {
-      unpack8(r1, y);
-      const float4 c[2] = {__ldg(c4 + 2 * lane), __ldg(c4 + 2 * lane + 1)};
-      const float4 s[2] = {__ldg(s4 + 2 * lane), __ldg(s4 + 2 * lane + 1)};
-      turn_halves(x, y, c, s);
-      dst[64 + lane] = pack8(x);
-      dst[68 + lane] = pack8(y);
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) {
+    if (page[k] < 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(
+        p.pool + (static_cast<long long>(page[k]) * p.page_size + pos[k] % p.page_size) * kRow);
+    dst[lane] = v0[k];
+    dst[32 + lane] = v1[k];
+    if (lane < kTurners) {
+      float x[8], y[8];
+      unpack8(r0[k], x);
+      if (kInterleaved) {
+        turn_pairs(x, c[k][0], s[k][0]);
+        dst[64 + lane] = pack8(x);
+      } else {
+        unpack8(r1[k], y);
+        turn_halves(x, y, c[k], s[k]);
+        dst[64 + lane] = pack8(x);
+        dst[68 + lane] = pack8(y);
+      }
     }
   }
 }
@@ -293,14 +317,18 @@ struct LatentGatherParams {
 };
 
 constexpr int kGatherWarps = 4;
-constexpr int kGatherRows = 8;                 // consecutive rows of out per warp
-constexpr int kRowPieces = kRow * 2 / 16;      // 72
-constexpr int kGatherSteps = kGatherRows * kRowPieces / 32;  // 18 pieces a lane
+constexpr int kRowPieces = kRow * 2 / 16;  // 72
 
-// Lane l < 8 finds row l's sequence by bisection of the starts and its page; then the
-// warp copies the eight rows, nine 16-byte pieces a lane in flight at a time.
+// A warp copies kRows consecutive rows of out. It finds the first one's sequence among the starts
+// (32 at a time, so that up to 1024 sequences take two reads); lane l < kRows steps on from there
+// to row l's and looks up its page. Then the rows go over nine 16-byte pieces a lane at a time,
+// all nine read before the first is written.
+template <int kRows>
 __global__ void __launch_bounds__(kGatherWarps * 32)
 latent_gather_kernel(const LatentGatherParams p) {
+  constexpr int kPerLane = 9;
+  constexpr int kParts = kRows * kRowPieces / (32 * kPerLane);
+  static_assert(kParts * 32 * kPerLane == kRows * kRowPieces, "whole parts");
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -312,22 +340,35 @@ latent_gather_kernel(const LatentGatherParams p) {
     const int before = i > 0 ? __ldg(p.starts + i - 1) : 0;
     if (s < before || s > p.total) set_dev_err(p.dev_err, PKV_DEV_ERR_LAYOUT);
   }
-  const long long row0 = warp * kGatherRows;
+  const long long row0 = warp * kRows;
   if (row0 >= p.total) return;
+  // the number of starts that are at most row0: the first `lo` are, those from `hi` on are not
+  int lo = 0, hi = p.n_seqs + 1;
+  while (hi - lo > 0) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && __ldg(p.starts + at) <= row0;
+    const int n = __popc(__ballot_sync(0xffffffffu, below));  // (ascending: the first n lanes)
+    if (n == 0) {
+      hi = lo;
+    } else {
+      const int last = lo + (n - 1) * step;  // at most row0; the next one looked at is not
+      hi = min(hi, last + step);
+      lo = last + 1;
+    }
+  }
   long long from = -1;  // the row's place in the pool, -1: the row is not written
   const long long t = row0 + lane;
-  if (lane < kGatherRows && t < p.total) {
-    int lo = 0, hi = p.n_seqs;  // the first index whose start is past t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.starts + mid) <= t) lo = mid + 1;
-      else hi = mid;
+  if (lane < kRows && t < p.total) {
+    int b = lo - 1;
+    while (b + 1 <= p.n_seqs && (b < 0 || __ldg(p.starts + b + 1) <= t)) {
+      if (b < 0 && __ldg(p.starts) > t) break;
+      ++b;
     }
-    const int b = lo - 1;
-    if (b >= 0 && t < __ldg(p.starts + b + 1)) {
+    if (b >= 0 && b < p.n_seqs) {
       const int slot = __ldg(p.slots + b);
       const long long pos = t - max(__ldg(p.starts + b), 0);
-      if (slot != 0) {
+      if (slot != 0 && pos >= 0) {
         const long long block = pos / p.page_size;
         int err = 0;
         if (slot < 0 || slot >= p.max_batch) err = PKV_DEV_ERR_BAD_SLOT;
@@ -341,22 +382,23 @@ latent_gather_kernel(const LatentGatherParams p) {
       }
     }
   }
+  __syncwarp();
   uint4* dst = p.out + row0 * kRowPieces;
+#pragma unroll 1
+  for (int part = 0; part < kParts; ++part) {
+    uint4 v[kPerLane];
+    bool have[kPerLane];
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    uint4 v[kGatherSteps / 2];
-    bool have[kGatherSteps / 2];
-#pragma unroll
-    for (int k = 0; k < kGatherSteps / 2; ++k) {
-      const int e = (part * (kGatherSteps / 2) + k) * 32 + lane;
+    for (int k = 0; k < kPerLane; ++k) {
+      const int e = (part * kPerLane + k) * 32 + lane;
       const int r = e / kRowPieces;
       const long long src = __shfl_sync(0xffffffffu, from, r);
       have[k] = src >= 0;
       if (have[k]) v[k] = __ldg(p.pool + src * kRowPieces + (e - r * kRowPieces));
     }
 #pragma unroll
-    for (int k = 0; k < kGatherSteps / 2; ++k)
-      if (have[k]) dst[(part * (kGatherSteps / 2) + k) * 32 + lane] = v[k];
+    for (int k = 0; k < kPerLane; ++k)
+      if (have[k]) dst[(part * kPerLane + k) * 32 + lane] = v[k];
   }
 }
 
@@ -474,7 +516,7 @@ extern "C" pkv_status pkv_latent_append(const pkv_cache_desc* cache, void* pool,
   p.max_blocks = cache->max_blocks;
   const int grid = n_tokens / kAppendWarps + (n_tokens % kAppendWarps != 0);
   return record_cuda_status(
-      launch_kernel(interleaved ? latent_append_kernel<true> : latent_append_kernel<false>,
+      launch_kernel(interleaved ? latent_append_kernel<true, 1> : latent_append_kernel<false, 1>,
                     dim3(grid), dim3(kAppendWarps * 32), 0, stream, true, p));
 }
 
@@ -503,8 +545,11 @@ extern "C" pkv_status pkv_latent_gather(const pkv_cache_desc* cache, const void*
   p.num_pages = cache->num_pages;
   p.max_batch = cache->max_batch;
   p.max_blocks = cache->max_blocks;
-  constexpr int kPerCta = kGatherWarps * kGatherRows;
-  const int grid = total / kPerCta + (total % kPerCta != 0);
-  return record_cuda_status(launch_kernel(latent_gather_kernel, dim3(grid),
-                                          dim3(kGatherWarps * 32), 0, stream, true, p));
+  // four rows a warp while all warps are on the GPU at once (28 an SM), else sixteen: the look-ups
+  // are the same for both
+  const bool few = total <= 152 * 28 * 4;
+  const int per_cta = kGatherWarps * (few ? 4 : 16);
+  const int grid = total / per_cta + (total % per_cta != 0);
+  return record_cuda_status(launch_kernel(few ? latent_gather_kernel<4> : latent_gather_kernel<16>,
+                                          dim3(grid), dim3(kGatherWarps * 32), 0, stream, true, p));
 }

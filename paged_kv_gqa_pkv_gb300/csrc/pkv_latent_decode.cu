@@ -49,7 +49,7 @@ constexpr int kChunks = kRow / 64;         // 9
 constexpr int kKGroups = 3;                // S's loads and barriers: three chunks at a time
 constexpr int kVGroups = 2;                // PV's: the CTA's dims 0-127 and 128-255
 constexpr int kLatThreads = 7 * 32;
-constexpr int kAhead = 3;                  // tiles whose rows are asked for in L2 ahead
+constexpr int kAhead = 1;                  // tiles whose rows are asked for in L2 ahead
 constexpr int kMaxRowsPerLaunch = 512;     // sequences of one launch
 
 // shared memory, offsets from a 1024-aligned base
@@ -225,20 +225,24 @@ __device__ __forceinline__ bool ragged(int n, int j) {
 // The schedule, from the sequences' tiles alone, so that it needs no other kernel's work.
 //
 // Up to as many items as workers: an item of nt tiles is cut into ceil(nt / S) equal parts, for the
-// smallest S (in steps of 1/16) at which all parts find a worker; every worker has one part, loads Q
+// smallest S (in steps of 1/32) at which all parts find a worker; every worker has one part, loads Q
 // once and has nothing to wait for between items. Where the longest item has at most kWholeSlack
 // tiles more than S nothing is cut at all: partial results are 256 KB each for 128 rows, written,
 // read and joined by a kernel that is otherwise done at once (a cut costs about two tiles' time).
 //
-// More items than workers: the tiles of all items stand in a row (at most 2^30, which the host sees
-// to), sequence by sequence, its row blocks one after another; worker w's range begins at tile
-// w * each + min(w, more). A cut inside an item moves to one of its ends if that is at most
-// kCutReach tiles away, and to the closer one.
+// More items than workers, or parts that are longer than an equal share by more than a quarter and
+// kRangeCost tiles (equal ranges cost the workers a second item, with its queries' loads and another
+// partial: 16 x ~20000 keys, parts of 37 tiles against ranges of 32: 77.7 us against 85.1): the tiles
+// of all items stand in a row (at most 2^30, which the host sees to), sequence by sequence, its row blocks one
+// after another; worker w's range begins at tile w * each + min(w, more). A cut inside an item moves
+// to one of its ends if that is at most kCutReach tiles away (one tile where ranges are long), and to
+// the closer one.
 constexpr int kWholeSlack = 1;
 constexpr int kCutReach = 3;
-__device__ __forceinline__ int move_cut(int x, int i0, int i1) {
-  if (x - i0 <= kCutReach && x - i0 <= i1 - x) return i0;
-  if (i1 - x <= kCutReach) return i1;
+constexpr int kRangeCost = 3;
+__device__ __forceinline__ int move_cut(int x, int i0, int i1, int reach) {
+  if (x - i0 <= reach && x - i0 <= i1 - x) return i0;
+  if (i1 - x <= reach) return i1;
   return x;
 }
 
@@ -363,10 +367,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     most = __reduce_max_sync(0xffffffffu, most);
     const int each = div_by(total, p.workers);
     const int more = total - each * p.workers.d;
-    const bool parts = items <= p.workers.d;
+    bool parts = items <= p.workers.d;
     int part_len = max(each + (more > 0), 1);
     if (parts) {
-      for (;; part_len += max(1, part_len >> 4)) {
+      for (;; part_len += max(1, part_len >> 5)) {
         if (most <= part_len + kWholeSlack) {
           part_len = max(most, 1);
           break;
@@ -377,7 +381,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
           n += (key_tiles(keys_of[b]) + part_len - 1) / part_len;
         if (__reduce_add_sync(0xffffffffu, n) * p.row_blocks.d <= p.workers.d) break;
       }
+      parts = part_len <= each + each / 4 + kRangeCost;
     }
+    const int reach = each >= 16 ? 1 : kCutReach;
     // what the scan counts: parts, or tiles
     const int x0 = parts ? worker : worker * each + min(worker, more);
     const int x1 = parts ? worker : x0 + each + (worker < more ? 1 : 0);
@@ -421,12 +427,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
           if (x >= base && x < base + span) {
             const int i0 = base + (p.row_blocks.d == 1 ? 0 : (x - base) / nt * nt);
             const int i1 = i0 + nt;
-            const int c = move_cut(x, i0, i1);
+            const int c = move_cut(x, i0, i1, reach);
             s_walk[k] = c;
-            if (k == 0 && c > i0 && c < i1 && move_cut(x1, i0, i1) >= i1) {
+            if (k == 0 && c > i0 && c < i1 && move_cut(x1, i0, i1, reach) >= i1) {
               // ends an item that it begins inside: as many workers before it as cuts in the item
               int u = worker;
-              while (move_cut((u - 1) * each + min(u - 1, more), i0, i1) > i0) --u;
+              while (move_cut((u - 1) * each + min(u - 1, more), i0, i1, reach) > i0) --u;
               s_walk[6] = worker - u + 2;
             }
           }
@@ -517,8 +523,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
               tma_load_3d_pair(dst + 3 * g * kChunk, &kmap, full0 + 8 * g, 0, src,
                                3 * g + lane % per);
           }
-          // The rows of a tile come from memory into L2 some tiles before they are loaded: what
-          // shared memory holds in flight (72 KB) does not cover the latency under load.
+          // The rows of a tile come from memory into L2 a tile before they are loaded: what shared
+          // memory holds in flight (72 KB) does not cover the latency under load. (64 x ~768 keys,
+          // none / 1 / 2 / 3 / 6 tiles ahead: 28.6 / 26.5 / 27.5 / 28.6 / 29.8 us; 76 x 2048: 45.9 /
+          // 41.4 / 42.8 / 45.3 / 54.0.)
           const int ahead = in + kAhead;
           const int at = lane >> box_sh;
           if (row > 0 && (at == ahead || (in == 0 && at > 0 && at < ahead)))
@@ -909,7 +917,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  // (neither CTA leaves while the other's MMAs may read its shared memory; no data is handed over,
+  // so nothing waits for the results' stores)
+  asm volatile(
+      "barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
