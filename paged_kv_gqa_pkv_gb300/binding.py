@@ -525,7 +525,8 @@ def _result(name: str, t, like: torch.Tensor, dev: int, stream, shape=None, dtyp
     if stream is not None:
         with torch.cuda.stream(stream):
             return _result(name, None, like, dev, None, shape, dtype)
-    t = torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
+    t = torch.empty_like(like) if shape is None else \
+        torch.empty(shape, dtype=dtype, device=like.device)
     return t, t.data_ptr()
 
 
