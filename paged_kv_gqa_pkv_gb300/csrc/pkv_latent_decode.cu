@@ -23,8 +23,8 @@
 // of 8 KB in flight: 6.76 TB/s of distinct cache rows, 12.8 TB/s into the SMs; the copy
 // bandwidth is 6.78.) The MMAs of a tile take ~2200-2500 cycles, its bytes ~3300.
 //
-// Roles per CTA: warps 0 and 6 load (TMA through the page table); warp 1 issues the MMAs (of
-// the pair: CTA 0's only); warps 2-5 are softmax and epilogue, lanes l and l + 64 sharing row l.
+// Roles per CTA: warps 0 and 6 load (TMA through the page table); warps 1 and 7 issue the MMAs
+// (CTA 0's, for the pair); warps 2-5 are softmax and epilogue, lanes l and l + 64 sharing row l.
 //
 // Work: where the (sequence, 128-row block) items are no more than the pairs of CTAs, each pair
 // takes one item or an equal part of one; the parts are as short as their number allows, unless
@@ -48,7 +48,7 @@ constexpr int kChunk = 64 * 128;           // [64 rows x 64 values], 128-byte sw
 constexpr int kChunks = kRow / 64;         // 9
 constexpr int kKGroups = 3;                // S's loads and barriers: three chunks at a time
 constexpr int kVGroups = 2;                // PV's: the CTA's dims 0-127 and 128-255
-constexpr int kLatThreads = 7 * 32;
+constexpr int kLatThreads = 8 * 32;
 constexpr int kAhead = 1;                  // tiles whose rows are asked for in L2 ahead
 constexpr int kMaxRowsPerLaunch = 512;     // sequences of one launch
 
@@ -58,9 +58,9 @@ constexpr int kOffK = kOffQ + kChunks * kChunk;       // [9 chunks][64 own keys]
 constexpr int kOffV = kOffK + kChunks * kChunk;       // [2 key halves][4 own chunks][64 keys]
 constexpr int kOffP = kOffV + 8 * kChunk;             // [2 key halves][64 query rows]
 constexpr int kOffBar = kOffP + 2 * kChunk;
-constexpr int kNumBars = 2 * kKGroups + 2 * kVGroups + 8;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;      // tmem slot, abort flag, first segment
-constexpr int kOffMax = kOffMisc + 32;                // [2][128] row maxima, [128] sums
+constexpr int kNumBars = 2 * kKGroups + 2 * kVGroups + 9;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;      // tmem slot, abort flag, 7 of the schedule
+constexpr int kOffMax = kOffMisc + 36;                // [2][128] row maxima, [128] sums
 constexpr int kLatSmem = kOffMax + 3 * 128 * 4 + 1024;  // + slack for the alignment
 static_assert(kLatSmem <= kMaxDynSmem, "shared memory above the opt-in limit");
 
@@ -290,13 +290,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* q_full = v_empty + kVGroups;      // CTA 0
   uint64_t* q_empty = q_full + 1;             // both: the item's last S is done
   uint64_t* s_full = q_empty + 1;             // [2] both
-  uint64_t* p_full = s_full + 2;              // CTA 0: both CTAs' P is there
-  uint64_t* pv_done = p_full + 1;             // both
+  uint64_t* p_full = s_full + 2;              // [2] CTA 0: both CTAs' P is there, S has been read
+  uint64_t* pv_done = p_full + 2;             // both
   uint64_t* o_free = pv_done + 1;             // CTA 0: both epilogues have read O
   uint64_t* v_tail = o_free + 1;              // each CTA: the values of a ragged tile
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* s_walk = reinterpret_cast<int*>(smem + kOffMisc + 8);  // the first segment
+  int* s_walk = reinterpret_cast<int*>(smem + kOffMisc + 8);  // [7]: the range and its first segment
   float* s_max = reinterpret_cast<float*>(smem + kOffMax);
 
   const int warp = threadIdx.x >> 5;
@@ -317,7 +317,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     mbar_init(q_empty, 1);
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(p_full, 8);   // the four softmax warps of both CTAs
+    mbar_init(&p_full[0], 8);   // the four softmax warps of both CTAs
+    mbar_init(&p_full[1], 8);
     mbar_init(pv_done, 1);
     mbar_init(o_free, 8);
     mbar_init(v_tail, 1);
@@ -564,112 +565,102 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
       }
     }
     if (!ok && lane == 0) *s_abort = 1;
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 7) {
     // ----------------------------------------------------- MMAs ----
-    // Two streams of products share the tensor pipe: S of the tiles, three chunks of the
-    // keys at a time, and PV. Whichever is ready is issued, PV first: S waits for rows from
-    // memory, and P for a softmax, and neither should hold up the other.
+    // Two streams of products share the tensor pipe, each with its own issuing thread of CTA 0
+    // (both in one thread, that polled for whichever was ready, took 200 cycles a round beside the
+    // softmax warps, whose code passes through the same instruction cache): S of the tiles waits for
+    // rows from memory, PV for a softmax, and neither holds up the other. (64 x ~768
+    // keys, 128 heads: 26.5 -> 24.6 us; 16 x ~20000, 128 rows: 77.7 -> 74.6 us.)
     if (rank == 1) {
-      // The other CTA's warp issues for both. This one notes for the join whether the worker's
+      // The other CTA's threads issue for both. Here warp 1 notes for the join whether the worker's
       // range ends an item of several parts, and writes the rows of sequences without keys.
-      if (lane == 0) {
-        p.part_item[worker] = make_int4(s_walk[6], w.b, w.rb, 0);
-      }
+      if (warp == 1) {
+        if (lane == 0) p.part_item[worker] = make_int4(s_walk[6], w.b, w.rb, 0);
 #pragma unroll 1
-      for (int b = worker; b < p.batch; b += p.workers.d) {
-        int err, slot;
-        if (seq_keys(p, b, &err, &slot) > 0) continue;
-        if (err && lane == 0) set_dev_err(p.dev_err, err);
-        const long long at = static_cast<long long>(b) * p.rows;
-        uint4* o = reinterpret_cast<uint4*>(p.out + at * kLatent);
-        for (long long e = lane; e < static_cast<long long>(p.rows) * (kLatent / 8); e += 32)
-          o[e] = make_uint4(0u, 0u, 0u, 0u);
-        for (int e = lane; e < p.rows; e += 32) p.lse[at + e] = -INFINITY;
+        for (int b = worker; b < p.batch; b += p.workers.d) {
+          int err, slot;
+          if (seq_keys(p, b, &err, &slot) > 0) continue;
+          if (err && lane == 0) set_dev_err(p.dev_err, err);
+          const long long at = static_cast<long long>(b) * p.rows;
+          uint4* o = reinterpret_cast<uint4*>(p.out + at * kLatent);
+          for (long long e = lane; e < static_cast<long long>(p.rows) * (kLatent / 8); e += 32)
+            o[e] = make_uint4(0u, 0u, 0u, 0u);
+          for (int e = lane; e < p.rows; e += 32) p.lse[at + e] = -INFINITY;
+        }
       }
     } else if (elect_one()) {
-      const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ), 0);
-      const uint32_t k_lo = desc_lo(smem_u32(smem + kOffK), 0);
-      const uint32_t p_lo = desc_lo(smem_u32(smem + kOffP), 0);
-      const uint32_t v_lo = desc_lo(smem_u32(smem + kOffV), kChunk);
-      Walk ws = w;                           // S's segment
-      bool s_more = more, p_more = more;
-      uint32_t ts = 0, s_items = 0;          // S's tile, items begun
-      uint32_t tp = 0, p_items = 0, fv = 0;  // PV's; tiles whose values v_full announced
-      int sj = ws.j0, pj = w.j0, sg = 0, pg = 0;
-      bool q_there = false, p_there = false;
-      WaitLimit idle;
-      while (p_more) {
-        // P of tile tp (before an item's first PV both epilogues have read the last item's O)
-        if (!p_there)
-          p_there = mbar_test(p_full, tp & 1) &&
-                    (pj > w.j0 || p_items == 0 || mbar_test(o_free, (p_items - 1) & 1));
-        const bool tail = ragged(w.n, pj);
-        if (p_there && (tail || mbar_test(&v_full[pg], fv & 1))) {
-          tc_fence_after();
-          const int left = w.n - pj * kKeys;
-          const int steps = left >= kKeys ? 8 : (left + 15) >> 4;  // of 16 keys
-          const uint32_t b = v_lo + ((2 * pg * kChunk) >> 4);
-          const uint32_t acc = pj > w.j0 ? 1u : 0u;
-          const uint32_t d = tmem + 128 * pg;
-          if (steps == 8) {
-            umma4_pair<32, 2048>(d, p_lo, b, kIdescO, acc);
-            umma4_pair<32, 2048>(d, p_lo + (kChunk >> 4), b + ((4 * kChunk) >> 4), kIdescO, 1u);
-          } else {
+      bool ok = true;
+      uint32_t tc = 0, items = 0;  // tiles, items issued
+      if (warp == 1) {
+        const uint32_t q_lo = desc_lo(smem_u32(smem + kOffQ), 0);
+        const uint32_t k_lo = desc_lo(smem_u32(smem + kOffK), 0);
+        for (; ok && more; more = walk_next(p, w)) {
+          ok = wait_phase(q_full, items & 1, s_abort);
+          ++items;
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k) {
-              const int kh = k >> 2, ks = k & 3;
-              umma1_pair(d, p_lo + ((kh * kChunk) >> 4) + 2 * ks,
-                         b + ((kh * 4 * kChunk) >> 4) + 128 * ks, kIdescO,
-                         acc | (k > 0 ? 1u : 0u));
-            }
-          }
-          commit_pair(&v_empty[pg]);
-          if (++pg == kVGroups) {
-            commit_pair(pv_done);
-            pg = 0;
-            p_there = false;
-            ++tp;
-            if (!tail) ++fv;
-            if (++pj == w.j1) {
-              ++p_items;
-              p_more = walk_next(p, w);
-              pj = w.j0;
-            }
-          }
-          idle.restart();
-          continue;
-        }
-        // S of tile ts goes into buffer ts & 1, which P of tile ts - 2 has been read from
-        bool s = s_more && ts <= tp + 1;
-        if (s) {
-          if (!q_there) q_there = mbar_test(q_full, s_items & 1);
-          s = q_there && mbar_test(&k_full[sg], ts & 1);
-        }
-        if (s) {
-          tc_fence_after();
+          for (int j = w.j0; ok && j < w.j1; ++j, ++tc) {
+            // S goes into buffer tc & 1, which P of tile tc - 2 has been read from. (A barrier for
+            // each buffer: this thread may come late, for it waits for Q too, and a barrier that two
+            // tiles have completed in the meantime looks as if none had.)
+            ok = tc < 2 || wait_phase(&p_full[tc & 1], ((tc >> 1) - 1) & 1, s_abort);
+#pragma unroll 1
+            for (int g = 0; ok && g < kKGroups; ++g) {
+              ok = wait_phase(&k_full[g], tc & 1, s_abort);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 3; ++c)
-            umma4_pair<32, 32>(tmem + kColS + 64 * (ts & 1), q_lo + (((3 * sg + c) * kChunk) >> 4),
-                               k_lo + (((3 * sg + c) * kChunk) >> 4), kIdescS,
-                               sg + c > 0 ? 1u : 0u);
-          commit_pair(&k_empty[sg]);
-          if (++sg == kKGroups) {
-            commit_pair(&s_full[ts & 1]);
-            sg = 0;
-            ++ts;
-            if (++sj == ws.j1) {
-              commit_pair(q_empty);
-              ++s_items;
-              q_there = false;
-              s_more = walk_next(p, ws);
-              sj = ws.j0;
+              for (int c = 0; c < 3; ++c)
+                umma4_pair<32, 32>(tmem + kColS + 64 * (tc & 1),
+                                   q_lo + (((3 * g + c) * kChunk) >> 4),
+                                   k_lo + (((3 * g + c) * kChunk) >> 4), kIdescS, g + c > 0 ? 1u : 0u);
+              commit_pair(&k_empty[g]);
             }
+            if (ok) commit_pair(&s_full[tc & 1]);
           }
-          idle.restart();
-          continue;
+          if (ok) commit_pair(q_empty);
         }
-        if (idle.over(s_abort)) break;
+      } else {
+        const uint32_t p_lo = desc_lo(smem_u32(smem + kOffP), 0);
+        const uint32_t v_lo = desc_lo(smem_u32(smem + kOffV), kChunk);
+        uint32_t fv = 0;  // tiles whose values v_full announced
+        for (; ok && more; more = walk_next(p, w)) {
+#pragma unroll 1
+          for (int j = w.j0; ok && j < w.j1; ++j, ++tc) {
+            // (before an item's first PV both epilogues have read the last item's O)
+            ok = wait_phase(&p_full[tc & 1], (tc >> 1) & 1, s_abort) &&
+                 (j > w.j0 || items == 0 || wait_phase(o_free, (items - 1) & 1, s_abort));
+            const bool tail = ragged(w.n, j);
+            const int left = w.n - j * kKeys;
+            const int steps = left >= kKeys ? 8 : (left + 15) >> 4;  // of 16 keys
+            const uint32_t acc = j > w.j0 ? 1u : 0u;
+#pragma unroll 1
+            for (int g = 0; ok && g < kVGroups; ++g) {
+              ok = tail || wait_phase(&v_full[g], fv & 1, s_abort);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t b = v_lo + ((2 * g * kChunk) >> 4);
+              const uint32_t d = tmem + 128 * g;
+              if (steps == 8) {
+                umma4_pair<32, 2048>(d, p_lo, b, kIdescO, acc);
+                umma4_pair<32, 2048>(d, p_lo + (kChunk >> 4), b + ((4 * kChunk) >> 4), kIdescO, 1u);
+              } else {
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) {
+                  const int kh = k >> 2, ks = k & 3;
+                  umma1_pair(d, p_lo + ((kh * kChunk) >> 4) + 2 * ks,
+                             b + ((kh * 4 * kChunk) >> 4) + 128 * ks, kIdescO, acc | (k > 0 ? 1u : 0u));
+                }
+              }
+              commit_pair(&v_empty[g]);
+            }
+            if (ok) commit_pair(pv_done);
+            if (!tail) ++fv;
+          }
+          ++items;
+        }
       }
+      if (!ok) *s_abort = 1;
     }
   } else {
     // ---------------------------------------- softmax and epilogue ----
@@ -808,7 +799,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_full0);
+        if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * (tc & 1));
       }
       // ---- the segment's end: O and the row's maximum and sum ----
       if (left_together) break;
