@@ -754,7 +754,7 @@ def _rope_tables(cos, sin, half: int, dev: int):
             _tensor("rope_sin", sin, torch.float32, cos.shape, dev), cos.shape[0])
 
 
-def _strided(name: str, t, dev, shape=None, inner: int = 1) -> int:
+def _strided(name: str, t, dev, shape=None) -> int:
     """The address of a bf16 CUDA tensor whose last dim is contiguous and whose other strides
     are free (of length-1 dims they do not matter)."""
     if not isinstance(t, torch.Tensor):
