@@ -20,6 +20,10 @@
 // The two tiles' chains QK -> softmax -> PV -> QK .. are independent, each with its own issuing
 // thread. (One thread that polled both chains' barriers took ~800 cycles a round beside the
 // softmax warps, whose code passes through the same instruction cache: 6000 cycles a key tile.)
+// Beside a softmax each barrier instruction of an issuing thread takes ~100-250 cycles, for it
+// queues behind exponentials; so there are few (one barrier for a tile's keys, one for its values;
+// packed prompts 137 -> 126 us, chunks 196 -> 182 us), and what has landed earlier is waited for
+// before P.
 #include <atomic>
 #include <cmath>
 
@@ -34,7 +38,6 @@ using namespace prefill_detail;
 constexpr int kSlots = 8;
 constexpr int kSlot = 128 * 128;              // 16 KB
 constexpr int kQChunks = (kOwnKey + kRotated) / 64;
-constexpr int kTileSlots = kQChunks + 2;      // slots of a tile's keys and values
 constexpr int kItemRows = 2 * kBM;
 constexpr int kExpThreads = 12 * 32;
 
@@ -42,10 +45,10 @@ constexpr int kExpThreads = 12 * 32;
 constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks][128 rows]
 constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-// full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_free[2], tail
-// item_full[4], item_free[4], claim
+// k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+// pv_done[2], o_free[2], tail, item_full[4], item_free[4], claim
 constexpr int kAheadItems = 4;
-constexpr int kNumBars = 2 * kSlots + 15 + 2 * kAheadItems + 1;
+constexpr int kNumBars = 8 + 15 + 2 * kAheadItems + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
 constexpr int kOffItem = kOffMisc + 16;
 constexpr int kItemInts = 8;
@@ -254,9 +257,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // [8]
-  uint64_t* empty = full + kSlots;                               // [8]
-  uint64_t* q_full = empty + kSlots;                             // [2]
+  // [2], a key tile's by its number's parity: its keys (values) are there; both row tiles'
+  // products have read them
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* q_full = v_empty + 2;  // [2]
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;   // [tile][half of its keys]: P_h is there, O_h rescaled
@@ -273,11 +280,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // both row tiles'
-    }
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&k_full[h], 1);
+      mbar_init(&k_empty[h], 2);  // both row tiles'
+      mbar_init(&v_full[h], 1);
+      mbar_init(&v_empty[h], 2);
       mbar_init(&q_full[h], 1);
       mbar_init(&q_empty[h], 1);
       mbar_init(&s_full[h], 1);
@@ -339,53 +346,61 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ------------------------------------------ keys and values ----
-      uint32_t n = 0, tails = 0;  // slots filled, tiles with a tail
+      // Tile n's keys take the ring's slots 5n .. 5n + 2 (mod 8), its values the next two: where
+      // the keys go, tile n - 2's values were read last, where the values go, tile n - 1's keys.
+      uint32_t n = 0, slot = 0, tails = 0;  // tiles, the next slot, tiles with a tail
       bool ok = true;
       while (items_ahead.next<true>(&it, s_abort, &ok)) {
         const Tile& x = it.x;
         const int head = it.head;
         const int nt = max(key_tiles(x, 0), key_tiles(x, 1));
-        for (int t = 0; ok && t < nt; ++t) {
+        for (int t = 0; t < nt; ++t, ++n) {
+          const uint32_t at = n & 1;
+          const int key = x.k0 + t * kBN;
           const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
-          for (int s = 0; ok && s < kTileSlots; ++s, ++n) {
-            const uint32_t slot = n % kSlots;
-            ok = n < kSlots || wait_phase(&empty[slot], ((n / kSlots) - 1) & 1, s_abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t* dst = smem + kOffRing + slot * kSlot;
-            const int key = x.k0 + t * kBN;
-            if (s < kQChunks) {
-              if (lane == 0) {
-                mbar_arrive_expect_tx(&full[slot], kSlot);
-                if (s < 2) tma_load_3d(dst, &kmap, &full[slot], 64 * s, head, key);
-                else tma_load_3d(dst, &rmap, &full[slot], 0, 0, key);
-              }
-            } else {
-              const int v = s - kQChunks;  // which 64 keys
-              const int valid = left - 64 * v;
-              const bool ragged = valid > 0 && valid < 64 && (valid & 15) != 0;
-              if (lane == 0) {
-                uint64_t* bar = ragged ? tail : &full[slot];
-                mbar_arrive_expect_tx(bar, kSlot);
-                tma_load_3d(dst, &vmap, bar, 0, head, key + 64 * v);
-                tma_load_3d(dst + kSlot / 2, &vmap, bar, 64, head, key + 64 * v);
-              }
-              if (ragged) {
-                // the rows past the sequence that share a 16-key step with its last ones: their
-                // weights are 0, but what stands there may be NaN
-                ok = __all_sync(0xffffffffu, wait_phase(tail, tails & 1, s_abort));
-                ++tails;
-                if (!ok) break;
-                const int z = 16 - (valid & 15);
-                for (int e = lane; e < z * 16; e += 32)
-                  *reinterpret_cast<uint4*>(dst + (e & 8) * (kSlot / 16) + (valid + (e >> 4)) * 128 +
-                                            (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
-              }
+          ok = n < 2 || wait_phase(&v_empty[at], ((n >> 1) - 1) & 1, s_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&k_full[at], kQChunks * kSlot);
+#pragma unroll 1
+            for (int s = 0; s < kQChunks; ++s) {
+              uint8_t* dst = smem + kOffRing + ((slot + s) % kSlots) * kSlot;
+              if (s < 2) tma_load_3d(dst, &kmap, &k_full[at], 64 * s, head, key);
+              else tma_load_3d(dst, &rmap, &k_full[at], 0, 0, key);
             }
           }
+          slot = (slot + kQChunks) % kSlots;
+          ok = n < 1 || wait_phase(&k_empty[at ^ 1], ((n - 1) >> 1) & 1, s_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const bool ragged = left < kBN && (left & 15) != 0;
+          if (lane == 0) {
+            uint64_t* bar = ragged ? tail : &v_full[at];
+            mbar_arrive_expect_tx(bar, 2 * kSlot);
+#pragma unroll 1
+            for (int v = 0; v < 4; ++v)  // 64 keys, 64 dims at a time
+              tma_load_3d(smem + kOffRing + ((slot + (v >> 1)) % kSlots) * kSlot +
+                              (v & 1) * (kSlot / 2),
+                          &vmap, bar, 64 * (v & 1), head, key + 64 * (v >> 1));
+          }
+          if (ragged) {
+            // the rows past the sequence that share a 16-key step with its last ones: their
+            // weights are 0, but what stands there may be NaN
+            ok = __all_sync(0xffffffffu, wait_phase(tail, tails & 1, s_abort));
+            ++tails;
+            if (!ok) break;
+            uint8_t* dst = smem + kOffRing + ((slot + (left >> 6)) % kSlots) * kSlot;
+            const int z = 16 - (left & 15);
+            for (int e = lane; e < z * 16; e += 32)
+              *reinterpret_cast<uint4*>(dst + (e & 8) * (kSlot / 16) +
+                                        ((left & 63) + (e >> 4)) * 128 + (e & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[at]);
+          }
+          slot = (slot + 2) % kSlots;
         }
         if (!ok) break;
       }
@@ -441,69 +456,70 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         const uint32_t ring_k = desc_lo(smem_u32(smem + kOffRing), 0);
         const uint32_t ring_v = desc_lo(smem_u32(smem + kOffRing), kSlot / 2);
         uint32_t n = 0;             // key tiles of this row tile
-        uint32_t slot = 0, ph = 0;  // the ring's next slot and its phase
+        uint32_t tc = 0, slot = 0;  // key tiles of the ring, its next slot
         uint32_t items = 0;
         bool ok = true;
-        auto next = [&]() {
-          if (++slot == kSlots) slot = 0, ph ^= 1;
+        // gives a tile's slots back: when the MMAs so far are done, or at once
+        auto give_back = [&](uint64_t* bar, bool mine) {
+          if (mine) umma_commit(bar);
+          else mbar_arrive(bar);
         };
         while (ok && items_ahead.next<false>(&it, s_abort, &ok)) {
           const Tile& x = it.x;
           const int nt = key_tiles(x, h), all = max(nt, key_tiles(x, 1 - h));
+          if (all == 0) continue;
           if (nt > 0) ok = wait_phase(&q_full[h], items & 1, s_abort);
 #pragma unroll 1
-          for (int t = 0; ok && t < all; ++t) {
-            if (t >= nt) {
-#pragma unroll 1
-              for (int s = 0; ok && s < kTileSlots; ++s) {
-                ok = wait_phase(&full[slot], ph, s_abort);
-                mbar_arrive(&empty[slot]);
-                next();
-              }
-              continue;
-            }
-            // S_h = Q_h K^T, over P_h once the last PV_h has read it
-            ok = n == 0 || wait_phase(&pv_done[h], (n - 1) & 1, s_abort);
+          for (int t = 0; ok && t < all; ++t, ++tc) {
+            const bool mine = t < nt;
+            const uint32_t at = tc & 1, ph = (tc >> 1) & 1;
+            ok = wait_phase(&k_full[at], ph, s_abort);
+            if (mine && ok) {
+              // S_h = Q_h K^T, over P_h once the last PV_h has read it
+              ok = n == 0 || wait_phase(&pv_done[h], (n - 1) & 1, s_abort);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < kQChunks; ++s) {
-              ok = ok && wait_phase(&full[slot], ph, s_abort);
-              if (!ok) break;
-              tc_fence_after();
-              umma4_ss(t_s, q_lo + ((s * kSlot) >> 4), ring_k + ((slot * kSlot) >> 4), kIdescS,
-                       s > 0 ? 1u : 0u);
-              umma_commit(&empty[slot]);
-              next();
+              for (uint32_t s = 0; s < kQChunks; ++s)
+                umma4_ss(t_s, q_lo + ((s * kSlot) >> 4),
+                         ring_k + ((((slot + s) % kSlots) * kSlot) >> 4), kIdescS, s > 0 ? 1u : 0u);
+              umma_commit(&s_full[h]);
+              if (t + 1 == nt) umma_commit(&q_empty[h]);
             }
-            if (!ok) break;
-            umma_commit(&s_full[h]);
-            if (t + 1 == nt) umma_commit(&q_empty[h]);
-            // O_h += P_h V
-            ok = t > 0 || items == 0 || wait_phase(&o_free[h], (items - 1) & 1, s_abort);
-            const int left = x.nk - t * kBN;
-            const int steps = left >= kBN ? 8 : (left + 15) >> 4;
+            give_back(&k_empty[at], mine);
+            slot = (slot + kQChunks) % kSlots;
+            // (what has been there long before P is waited for first)
+            ok = ok && wait_phase(&v_full[at], ph, s_abort);
+            if (mine) {
+              // O_h += P_h V
+              ok = ok && (t > 0 || items == 0 || wait_phase(&o_free[h], (items - 1) & 1, s_abort));
+              const int left = x.nk - t * kBN;
+              const int steps = left >= kBN ? 8 : (left + 15) >> 4;
 #pragma unroll 1
-            for (int v = 0; ok && v < 2; ++v) {
-              ok = wait_phase(&full[slot], ph, s_abort) &&
-                   wait_phase(&p_full[2 * h + v], n & 1, s_abort);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t b = ring_v + ((slot * kSlot) >> 4);
-              const uint32_t a = t_s + 32 * v;
-              const uint32_t acc = t > 0 || v > 0 ? 1u : 0u;
-              const int k_n = steps - 4 * v;
-              if (k_n >= 4) {
-                umma4_ts(t_o, a, b, kIdescO, acc);
-              } else {
+              for (int v = 0; ok && v < 2; ++v) {
+                const uint32_t b = ring_v + ((((slot + v) % kSlots) * kSlot) >> 4);
+                const uint32_t a = t_s + 32 * v;
+                const uint32_t acc = t > 0 || v > 0 ? 1u : 0u;
+                const int k_n = steps - 4 * v;
+                ok = wait_phase(&p_full[2 * h + v], n & 1, s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (k_n >= 4) {
+                  umma4_ts(t_o, a, b, kIdescO, acc);
+                } else {
 #pragma unroll 1
-                for (int k = 0; k < k_n; ++k)
-                  umma_bf16_ts(t_o, a + 8 * k, (static_cast<uint64_t>(kDescHi) << 32) | (b + 128u * k),
-                               kIdescO, acc | (k > 0 ? 1u : 0u));
+                  for (int k = 0; k < k_n; ++k)
+                    umma_bf16_ts(t_o, a + 8 * k,
+                                 (static_cast<uint64_t>(kDescHi) << 32) | (b + 128u * k), kIdescO,
+                                 acc | (k > 0 ? 1u : 0u));
+                }
               }
-              umma_commit(&empty[slot]);
-              next();
+              if (!ok) break;
+              umma_commit(&pv_done[h]);
+              ++n;
             }
-            if (ok) umma_commit(&pv_done[h]);
-            ++n;
+            give_back(&v_empty[at], mine);
+            slot = (slot + 2) % kSlots;
           }
           if (nt > 0) ++items;
         }
@@ -552,10 +568,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         const bool grow = m_run == -INFINITY ? m_cand != -INFINITY
                                              : (m_cand - m_run) * p.qscale > kRescaleThreshold;
         const float m_use = grow ? m_cand : m_run;
-        const float alpha = grow ? ex2((m_run - m_use) * p.qscale) : 1.f;  // 0 if m_run = -inf
         const float neg_m = m_use == -INFINITY ? 0.f : -m_use * p.qscale;
         // (S_h of this tile was issued after the last PV_h had completed: O_h is at rest)
         if (t > 0 && __any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? ex2((m_run - m_use) * p.qscale) : 1.f;  // 0 if m_run = -inf
+          l_run *= alpha;
 #pragma unroll 1
           for (int q = 0; q < kValue; q += 32) {
             uint32_t o[32];
@@ -569,7 +586,6 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // P over the first 64 columns of S_h, in bf16 (a weight off by at most 2^-8 of itself;
         // the sum takes it unrounded), the first 64 keys' first: their product with V runs while
         // the others' weights are computed.
-        l_run *= alpha;
         m_run = m_use;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
