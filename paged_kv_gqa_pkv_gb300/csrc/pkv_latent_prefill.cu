@@ -11,19 +11,25 @@
 // cycles at their rate; the 65 536 exponentials take 1024 to 2048. So the tensor pipe is the
 // bound, if each tile's softmax is hidden behind the other's products.
 //
-// Roles of a CTA (one per SM; it takes item after item, the costly ones first): warp 0 loads keys and values by TMA into a
-// ring of eight 16 KB slots (K: three slots of 64 dims x 128 keys, V: two of 64 keys), warp 2
-// the queries, one thread each of warps 1 and 3 issues the MMAs of one tile, warps 4-7 and 8-11
-// are the softmax of the two tiles, a query row per thread. Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each);
-// P_h, bf16, is written over S_h and read from there by the product with V.
+// Roles of a CTA (one per SM; it takes item after item, the costly ones first): warp 0 loads keys
+// and values by TMA into a ring of eight 16 KB slots (K: three slots of 64 dims x 128 keys, V: two
+// of 64 keys), warp 2 the queries, one thread each of warps 1 and 3 issues the MMAs of one tile,
+// warps 4-7 and 8-11 are the softmax of the two tiles, a query row per thread. Tensor memory holds
+// S_0, S_1, O_0, O_1 (128 columns each); P_h, bf16, is written over S_h and read from there by the
+// product with V.
 //
 // The two tiles' chains QK -> softmax -> PV -> QK .. are independent, each with its own issuing
 // thread. (One thread that polled both chains' barriers took ~800 cycles a round beside the
-// softmax warps, whose code passes through the same instruction cache: 6000 cycles a key tile.)
-// Beside a softmax each barrier instruction of an issuing thread takes ~100-250 cycles, for it
-// queues behind exponentials; so there are few (one barrier for a tile's keys, one for its values;
-// packed prompts 137 -> 126 us, chunks 196 -> 182 us), and what has landed earlier is waited for
-// before P.
+// softmax warps: 6000 cycles a key tile.) A chain takes ~3600 cycles a key tile, of which its
+// products run 1280: QK ~1000 from issue to S, softmax ~1500 (reading S twice, 64 columns at a
+// time, in loops: with all 128 in registers the unrolled code does not stay in the instruction
+// cache, 4 % slower), P's arrival to PV's end ~600, and so on. Beside a softmax each barrier
+// instruction of an issuing thread takes ~100-250 cycles, for it queues behind exponentials; so
+// there are few (a tile's keys have one barrier), and those that need not be waited for last are
+// waited for before P. Measured with 32 heads: 24 prompts of 64 .. 1024 tokens 124 us (0.74
+// PFLOP/s; the floor of their bytes is 71), 8 chunks of 512 behind 512 .. 4096 170 us (1.26
+// PFLOP/s of 1.99). Tiles forced half a period apart by a barrier: 176 us (what each gains, the
+// ring's eight slots take back: a tile's keys land where the slower tile has read values).
 #include <atomic>
 #include <cmath>
 
@@ -45,10 +51,10 @@ constexpr int kExpThreads = 12 * 32;
 constexpr int kOffQ = 0;                                  // [2 tiles][3 chunks][128 rows]
 constexpr int kOffRing = kOffQ + 2 * kQChunks * kSlot;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-// k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+// k_full[2], k_empty[2], v_full[2], v_empty[2][2], q_full[2], q_empty[2], s_full[2], p_full[2][2],
 // pv_done[2], o_free[2], tail, item_full[4], item_free[4], claim
 constexpr int kAheadItems = 4;
-constexpr int kNumBars = 8 + 15 + 2 * kAheadItems + 1;
+constexpr int kNumBars = 10 + 15 + 2 * kAheadItems + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;          // tmem slot, abort flag
 constexpr int kOffItem = kOffMisc + 16;
 constexpr int kItemInts = 8;
@@ -143,6 +149,13 @@ __device__ __forceinline__ float weights_to_tmem(const uint32_t (&s)[64], float 
   unpack_f32x2(acc0, a, b);
   unpack_f32x2(acc1, c, d);
   return (a + b) + (c + d);
+}
+
+// 64 scores of a row.
+__device__ __forceinline__ void load_half(uint32_t t_s, uint32_t (&s)[64]) {
+  tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+  tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+  tmem_wait_ld();
 }
 
 // 32 bytes to global memory in one instruction.
@@ -258,12 +271,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   // [2], a key tile's by its number's parity: its keys (values) are there; both row tiles'
-  // products have read them
+  // products have read them (the values: [2][2], the first and the last 64)
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* k_empty = k_full + 2;
   uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + 2;
-  uint64_t* q_full = v_empty + 2;  // [2]
+  uint64_t* q_full = v_empty + 4;  // [2]
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;   // [tile][half of its keys]: P_h is there, O_h rescaled
@@ -285,6 +298,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_init(&k_empty[h], 2);  // both row tiles'
       mbar_init(&v_full[h], 1);
       mbar_init(&v_empty[h], 2);
+      mbar_init(&v_empty[2 + h], 2);
       mbar_init(&q_full[h], 1);
       mbar_init(&q_empty[h], 1);
       mbar_init(&s_full[h], 1);
@@ -346,8 +360,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ------------------------------------------ keys and values ----
-      // Tile n's keys take the ring's slots 5n .. 5n + 2 (mod 8), its values the next two: where
-      // the keys go, tile n - 2's values were read last, where the values go, tile n - 1's keys.
+      // Tile n's keys take the ring's slots 5n .. 5n + 2 (mod 8), its values the next two: the
+      // first 64 dims of the keys go where tile n - 2's last ones were (the load of tile n - 1's
+      // values has waited for them), the others where its values were, half by half, and the
+      // values where tile n - 1's keys were.
       uint32_t n = 0, slot = 0, tails = 0;  // tiles, the next slot, tiles with a tail
       bool ok = true;
       while (items_ahead.next<true>(&it, s_abort, &ok)) {
@@ -358,18 +374,20 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           const uint32_t at = n & 1;
           const int key = x.k0 + t * kBN;
           const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
-          ok = n < 2 || wait_phase(&v_empty[at], ((n >> 1) - 1) & 1, s_abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&k_full[at], kQChunks * kSlot);
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[at], kQChunks * kSlot);
 #pragma unroll 1
-            for (int s = 0; s < kQChunks; ++s) {
-              uint8_t* dst = smem + kOffRing + ((slot + s) % kSlots) * kSlot;
+          for (int s = 0; s < kQChunks; ++s) {
+            if (s > 0 && n >= 2)
+              ok = wait_phase(&v_empty[2 * (s - 1) + at], ((n >> 1) - 1) & 1, s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* dst = smem + kOffRing + ((slot + s) % kSlots) * kSlot;
+            if (lane == 0) {
               if (s < 2) tma_load_3d(dst, &kmap, &k_full[at], 64 * s, head, key);
               else tma_load_3d(dst, &rmap, &k_full[at], 0, 0, key);
             }
           }
+          if (!ok) break;
           slot = (slot + kQChunks) % kSlots;
           ok = n < 1 || wait_phase(&k_empty[at ^ 1], ((n - 1) >> 1) & 1, s_abort);
           ok = __all_sync(0xffffffffu, ok);
@@ -473,7 +491,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           for (int t = 0; ok && t < all; ++t, ++tc) {
             const bool mine = t < nt;
             const uint32_t at = tc & 1, ph = (tc >> 1) & 1;
-            ok = wait_phase(&k_full[at], ph, s_abort);
+            if (t == 0 || !mine) ok = wait_phase(&k_full[at], ph, s_abort);
             if (mine && ok) {
               // S_h = Q_h K^T, over P_h once the last PV_h has read it
               ok = n == 0 || wait_phase(&pv_done[h], (n - 1) & 1, s_abort);
@@ -501,7 +519,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                 const uint32_t a = t_s + 32 * v;
                 const uint32_t acc = t > 0 || v > 0 ? 1u : 0u;
                 const int k_n = steps - 4 * v;
-                ok = wait_phase(&p_full[2 * h + v], n & 1, s_abort);
+                // (the next product's keys, whose wait costs nothing here)
+                if (v == 1 && t + 1 < nt)
+                  ok = wait_phase(&k_full[at ^ 1], ((tc + 1) >> 1) & 1, s_abort);
+                ok = ok && wait_phase(&p_full[2 * h + v], n & 1, s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 if (k_n >= 4) {
@@ -513,12 +534,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                                  (static_cast<uint64_t>(kDescHi) << 32) | (b + 128u * k), kIdescO,
                                  acc | (k > 0 ? 1u : 0u));
                 }
+                if (v == 0) umma_commit(&v_empty[at]);
               }
               if (!ok) break;
               umma_commit(&pv_done[h]);
               ++n;
             }
-            give_back(&v_empty[at], mine);
+            if (!mine) mbar_arrive(&v_empty[at]);
+            give_back(&v_empty[2 + at], mine);
             slot = (slot + 2) % kSlots;
           }
           if (nt > 0) ++items;
@@ -550,18 +573,32 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         ok = __all_sync(0xffffffffu, wait_phase(&s_full[h], n & 1, s_abort));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        tmem_wait_ld();
         const int c_hi = see - t * kBN;  // visible columns
-        if (c_hi < kBN) {
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          uint32_t sr[64];
+          load_half(t_s + 64 * v, sr);
+          if (__any_sync(0xffffffffu, c_hi < 64 * v + 64)) {
+            // hidden keys' scores go back as -inf
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c >= c_hi) sr[c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 64; ++c)
+              if (c >= c_hi - 64 * v) sr[c] = __float_as_uint(-INFINITY);
+            tmem_st32(t_s + 64 * v, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            tmem_st32(t_s + 64 * v + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            tmem_wait_st();
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              m4[k] = fmax3(m4[k], __uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1]));
+          }
+          mx = fmax3(fmax3(m4[0], m4[1], mx), m4[2], m4[3]);
         }
-        const float mx = row_max_full(sr);
+        // (P will take S's columns 0-63, and a half of S is read just before its half of P is written:
+        // P's first 32 columns lie over what has been read, its last 32 too)
         // the maximum moves only when it has grown by more than 2^8: until then weights of up
         // to 256 do no harm in bf16 and fp32, and O stays as it is
         const float m_cand = fmaxf(m_run, mx);
@@ -587,10 +624,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // the sum takes it unrounded), the first 64 keys' first: their product with V runs while
         // the others' weights are computed.
         m_run = m_use;
-#pragma unroll
+#pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-          l_run += weights_to_tmem(reinterpret_cast<const uint32_t(&)[64]>(sr[64 * v]), p.qscale, neg_m,
-                                   t_s + 32 * v);
+          uint32_t sr[64];
+          load_half(t_s + 64 * v, sr);
+          l_run += weights_to_tmem(sr, p.qscale, neg_m, t_s + 32 * v);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
