@@ -306,8 +306,8 @@ constexpr int kRowPieces = kRow * 2 / 16;  // 72
 // A warp copies kRows consecutive rows of out. It finds the first one's sequence among the starts
 // (32 at a time, so that up to 1024 sequences take two reads); lane l < kRows steps on from there
 // to row l's and looks up its page. Then the rows go over nine 16-byte pieces a lane at a time,
-// all nine read before the first is written. Memory bounds it: 82 000 rows of 17 sequences in
-// 34.0 us (189 MB, 5.6 TB/s); the chain of starts, slot, page and row bounds few rows (777: 2.7 us).
+// all nine read before the first is written. Memory bounds it: 82 000 rows of 16 sequences in
+// 33.8 us (189 MB, 5.6 TB/s); the chain of starts, slot, page and row bounds few rows (777: 2.7 us).
 template <int kRows>
 __global__ void __launch_bounds__(kGatherWarps * 32)
 latent_gather_kernel(const LatentGatherParams p) {
