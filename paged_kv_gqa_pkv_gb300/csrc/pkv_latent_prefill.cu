@@ -27,8 +27,8 @@
 // instruction of an issuing thread takes ~100-250 cycles, for it queues behind exponentials; so
 // there are few (a tile's keys have one barrier), and those that need not be waited for last are
 // waited for before P. Measured with 32 heads: 24 prompts of 64 .. 1024 tokens 124 us (0.74
-// PFLOP/s; the floor of their bytes is 71), 8 chunks of 512 behind 512 .. 4096 170 us (1.26
-// PFLOP/s of 1.99). Tiles forced half a period apart by a barrier: 176 us (what each gains, the
+// PFLOP/s; the floor of their bytes is 71), 8 chunks of 512 behind 512 .. 4096 164 us (1.31
+// PFLOP/s of 1.99). Tiles forced half a period apart by a barrier: 3 % slower (what each gains, the
 // ring's eight slots take back: a tile's keys land where the slower tile has read values).
 #include <atomic>
 #include <cmath>
@@ -236,8 +236,9 @@ struct ItemReader {
   uint64_t* full;
   uint64_t* free;
   int r = 0;
-  // By a whole warp, or by one thread alone.
-  template <bool kWarp>
+  // By a whole warp, or by one thread alone. kFree: the reader needs no more of it; else it says
+  // so itself.
+  template <bool kWarp, bool kFree = true>
   __device__ __forceinline__ bool next(Item* it, volatile int* abort_flag, bool* ok) {
     const int at = r % kAheadItems;
     *ok = wait_phase(&full[at], (r / kAheadItems) & 1, abort_flag);
@@ -247,7 +248,7 @@ struct ItemReader {
     it->x.q0 = v[0], it->x.rows = v[1], it->x.k0 = v[2], it->x.nk = v[3], it->x.see = v[4];
     it->head = v[5];
     if (kWarp) __syncwarp();
-    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&free[at]);
+    if (kFree && (!kWarp || (threadIdx.x & 31) == 0)) mbar_arrive(&free[at]);
     ++r;
     return it->head >= 0;
   }
@@ -366,11 +367,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       // values where tile n - 1's keys were.
       uint32_t n = 0, slot = 0, tails = 0;  // tiles, the next slot, tiles with a tail
       bool ok = true;
-      while (items_ahead.next<true>(&it, s_abort, &ok)) {
+      while (items_ahead.next<true, false>(&it, s_abort, &ok)) {
         const Tile& x = it.x;
         const int head = it.head;
         const int nt = max(key_tiles(x, 0), key_tiles(x, 1));
+        // The next item is claimed on this word: late, so that no CTA holds one that another could
+        // begin earlier (claimed when an item begins, chunks took 170 us instead of 164), but with
+        // time to look it up.
+        const int claim_at = max(nt - 2, 0);
+        uint64_t* const claimed = &item_free[(items_ahead.r - 1) % kAheadItems];
+        if (nt == 0 && lane == 0) mbar_arrive(claimed);
         for (int t = 0; t < nt; ++t, ++n) {
+          if (t == claim_at && lane == 0) mbar_arrive(claimed);
           const uint32_t at = n & 1;
           const int key = x.k0 + t * kBN;
           const int left = x.nk - t * kBN;  // keys of the sequence from this tile on
