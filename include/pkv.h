@@ -654,7 +654,7 @@ pkv_status pkv_compact_pages(const pkv_cache_desc* cache, void* k_pool, void* v_
  * same strides; otherwise no value of out may lie on one of x that the call
  * reads. Values of out must not lie on one another: strides for which the inner
  * axis's rows do not end before the outer one's next are PKV_ERR_ARG (x may
- * repeat values: a stride of 0). A token whose position is outside [0, rope_len)
+ * repeat values: a stride of 0). The stride of an axis of length 1 is ignored. A token whose position is outside [0, rope_len)
  * is not written and sets PKV_DEV_ERR_BAD_POS. Pointers need 2-byte (x, out) and
  * 4-byte alignment; with 16-byte alignment of all four tensors, strides that are
  * multiples of 8 and dims of 16 (8 if interleaved) the call moves 16 bytes at a
@@ -761,7 +761,8 @@ pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, const void* 
  *   out[i, h] = sum_t exp(x[t] - lse) v[t, h]
  * A query that sees no key gives out 0, lse -inf. q: bf16, 192 values a head; k_own,
  * v: bf16, 128 a head; k_rot: bf16, 64 a token; strides of tokens and heads in values,
- * multiples of 8, >= 0 and below 2^38 (so slices of wider rows and stride-0 heads do);
+ * multiples of 8, >= 0 and below 2^38 (so slices of wider rows and stride-0 heads do;
+ * those of an axis of length 1 are ignored);
  * the four tensors 16-byte aligned. out: bf16 [n_queries, num_heads, 128], 32-byte
  * aligned; lse: fp32 [n_queries, num_heads]. q_starts, k_starts: int32 [n_seqs + 1], ascending
  * (equal neighbours: no queries, no keys) from 0 or more to at most n_queries and

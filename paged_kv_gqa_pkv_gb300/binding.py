@@ -756,7 +756,7 @@ def _rope_tables(cos, sin, half: int, dev: int):
 
 def _strided(name: str, t, dev, shape=None) -> int:
     """The address of a bf16 CUDA tensor whose last dim is contiguous and whose other strides
-    are free (of length-1 dims they do not matter)."""
+    are free."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16 or not t.is_cuda or (dev is not None and t.get_device() != dev) or \

@@ -406,6 +406,8 @@ extern "C" pkv_status pkv_rotate(const void* x, int64_t x_token_stride, int64_t 
                                  const float* rope_sin, int rope_len, int32_t* dev_err,
                                  cudaStream_t stream) {
   constexpr int64_t kMaxStride = int64_t{1} << 40;
+  if (n_tokens == 1) x_token_stride = out_token_stride = 0;  // (no second token to step to)
+  if (num_heads == 1) x_head_stride = out_head_stride = 0;
   if (n_tokens < 0 || num_heads <= 0 || dims <= 0 || dims % 2 != 0 || rope_len <= 0)
     return PKV_ERR_ARG;
   if (interleaved != 0 && interleaved != 1) return PKV_ERR_ARG;

@@ -731,6 +731,10 @@ extern "C" pkv_status pkv_latent_prefill_attention(
       !std::isfinite(scale) || !(scale > 0.f))
     return PKV_ERR_ARG;
   constexpr int64_t kMaxStride = int64_t{1} << 38;  // a tensor map's limit, in values
+  // (an axis of length 1 has no second place to step to)
+  if (num_heads == 1) q_head_stride = k_head_stride = v_head_stride = 0;
+  if (n_queries == 1) q_token_stride = 0;
+  if (n_keys == 1) k_token_stride = r_token_stride = v_token_stride = 0;
   for (const int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
                           r_token_stride, v_token_stride, v_head_stride})
     if (s < 0 || s >= kMaxStride) return PKV_ERR_ARG;

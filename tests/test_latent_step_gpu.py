@@ -303,3 +303,26 @@ def test_binding_refusals_on_the_gpu():
     kv = torch.zeros(3, H, 128, dtype=bf, device="cuda")
     with pytest.raises(pkv.PkvError):
         pkv.pkv_latent_prefill_attention(wide, kv, torch.zeros(3, 64, dtype=bf, device="cuda"), kv, i32([0, 3]), i32([0, 3]), 0.1)
+
+
+def test_strides_of_single_tokens_and_heads():
+    """The strides of an axis of length 1 are whatever the view left there."""
+    g = C.gen(5)
+    layer = Layer(2, 40, 16)
+    odd = lambda t, k: t.as_strided(t.shape, tuple(3 if i == k else s for i, s in enumerate(t.stride())))  # noqa: E731
+    x, pos = C.normal(g, 1, 4, 64).cuda(), i32([7])
+    want = pkv.pkv_rotate(x, pos, layer.cos, layer.sin)
+    assert torch.equal(pkv.pkv_rotate(odd(x, 0), pos, layer.cos, layer.sin), want)
+    y = x.clone()
+    pkv.pkv_rotate(odd(y, 0), pos, layer.cos, layer.sin, out=y)
+    assert torch.equal(y, want)
+    assert torch.equal(pkv.pkv_rotate(odd(x[:, :1], 1), pos, layer.cos, layer.sin), want[:, :1])
+    q, k, r = C.normal(g, 5, 1, 192).cuda(), C.normal(g, 5, 1, 128).cuda(), C.normal(g, 5, 64).cuda()
+    for n in (5, 1):
+        a = (q[:n], k[:n], r[:n], k[:n])
+        want = pkv.pkv_latent_prefill_attention(*a, i32([0, n]), i32([0, n]), C.SCALE)
+        b = [odd(t, 1) if t.dim() == 3 else t for t in a]
+        if n == 1:
+            b = [odd(t, 0) for t in b]
+        got = pkv.pkv_latent_prefill_attention(*b, i32([0, n]), i32([0, n]), C.SCALE)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
