@@ -81,17 +81,18 @@ struct RotateParams {
   int head_groups;  // ceil(num_heads / kRotateHeads)
 };
 
-constexpr int kRotateThreads = 256;
+constexpr int kRotateThreads = 128;
 // Heads per thread: they share the position's cosines and sines, which are read once
 // into registers, and their loads are all in flight together.
-constexpr int kRotateHeads = 4;
+constexpr int kRotateHeads = 2;
 
 enum RotateForm { kPairs16, kHalves16, kPairs1, kHalves1 };
 
 // A thread turns one unit of kRotateHeads heads of one token. The 16-byte forms take
 // 8 values (interleaved) or 8 values and their 8 partners (halves); where an address,
 // a stride or the number of dims does not allow that, a unit is one pair of values.
-// Memory bounds it: 8191 tokens of 32 heads (69 MB) in 13.4 us, 5.2 TB/s with the launch.
+// Memory bounds it: 8191 tokens of 32 heads (69 MB) in 12.3 us, 5.6 TB/s with the launch (one head
+// a thread 13.9, four 12.4; CTAs of 256 threads, which come to 2.3 waves, 13.4).
 template <RotateForm kForm>
 __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateParams p) {
   pdl_wait_primary();
@@ -301,19 +302,19 @@ struct LatentGatherParams {
 };
 
 constexpr int kGatherWarps = 4;
+constexpr int kGatherRows = 4;  // of a warp: nine 16-byte pieces a lane
 constexpr int kRowPieces = kRow * 2 / 16;  // 72
 
-// A warp copies kRows consecutive rows of out. It finds the first one's sequence among the starts
-// (32 at a time, so that up to 1024 sequences take two reads); lane l < kRows steps on from there
-// to row l's and looks up its page. Then the rows go over nine 16-byte pieces a lane at a time,
-// all nine read before the first is written. Memory bounds it: 82 000 rows of 16 sequences in
-// 33.8 us (189 MB, 5.6 TB/s); the chain of starts, slot, page and row bounds few rows (777: 2.7 us).
-template <int kRows>
+// A warp copies kGatherRows consecutive rows of out. It finds the first one's sequence among the
+// starts (32 at a time, so that up to 1024 sequences take two reads); lane l < kGatherRows steps on from
+// there to row l's and looks up its page. Then all pieces of the rows are read before the first is
+// written. Memory bounds it: 82 000 rows of 16 sequences in 30.8 us (189 MB, 6.1 TB/s; 8 rows a warp
+// 31.8 us, 16 rows 33.9, the look-ups being cheap); the chain of starts, slot, page and row bounds
+// few rows (777: 2.7 us, with 8 rows a warp 3.6).
 __global__ void __launch_bounds__(kGatherWarps * 32)
 latent_gather_kernel(const LatentGatherParams p) {
   constexpr int kPerLane = 9;
-  constexpr int kParts = kRows * kRowPieces / (32 * kPerLane);
-  static_assert(kParts * 32 * kPerLane == kRows * kRowPieces, "whole parts");
+  static_assert(32 * kPerLane == kGatherRows * kRowPieces, "nine pieces a lane");
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -325,7 +326,7 @@ latent_gather_kernel(const LatentGatherParams p) {
     const int before = i > 0 ? __ldg(p.starts + i - 1) : 0;
     if (s < before || s > p.total) set_dev_err(p.dev_err, PKV_DEV_ERR_LAYOUT);
   }
-  const long long row0 = warp * kRows;
+  const long long row0 = warp * kGatherRows;
   if (row0 >= p.total) return;
   // the number of starts that are at most row0: the first `lo` are, those from `hi` on are not
   int lo = 0, hi = p.n_seqs + 1;
@@ -344,7 +345,7 @@ latent_gather_kernel(const LatentGatherParams p) {
   }
   long long from = -1;  // the row's place in the pool, -1: the row is not written
   const long long t = row0 + lane;
-  if (lane < kRows && t < p.total) {
+  if (lane < kGatherRows && t < p.total) {
     int b = lo - 1;
     while (b + 1 <= p.n_seqs && (b < 0 || __ldg(p.starts + b + 1) <= t)) {
       if (b < 0 && __ldg(p.starts) > t) break;
@@ -369,22 +370,19 @@ latent_gather_kernel(const LatentGatherParams p) {
   }
   __syncwarp();
   uint4* dst = p.out + row0 * kRowPieces;
-#pragma unroll 1
-  for (int part = 0; part < kParts; ++part) {
-    uint4 v[kPerLane];
-    bool have[kPerLane];
+  uint4 v[kPerLane];
+  bool have[kPerLane];
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int e = (part * kPerLane + k) * 32 + lane;
-      const int r = e / kRowPieces;
-      const long long src = __shfl_sync(0xffffffffu, from, r);
-      have[k] = src >= 0;
-      if (have[k]) v[k] = __ldg(p.pool + src * kRowPieces + (e - r * kRowPieces));
-    }
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k)
-      if (have[k]) dst[(part * kPerLane + k) * 32 + lane] = v[k];
+  for (int k = 0; k < kPerLane; ++k) {
+    const int e = k * 32 + lane;
+    const int r = e / kRowPieces;
+    const long long src = __shfl_sync(0xffffffffu, from, r);
+    have[k] = src >= 0;
+    if (have[k]) v[k] = __ldg(p.pool + src * kRowPieces + (e - r * kRowPieces));
   }
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k)
+    if (have[k]) dst[k * 32 + lane] = v[k];
 }
 
 // PKV_OK on an sm_103 device.
@@ -532,11 +530,8 @@ extern "C" pkv_status pkv_latent_gather(const pkv_cache_desc* cache, const void*
   p.num_pages = cache->num_pages;
   p.max_batch = cache->max_batch;
   p.max_blocks = cache->max_blocks;
-  // four rows a warp while all warps are on the GPU at once (28 an SM), else sixteen: the look-ups
-  // are the same for both
-  const bool few = total <= 152 * 28 * 4;
-  const int per_cta = kGatherWarps * (few ? 4 : 16);
+  constexpr int per_cta = kGatherWarps * kGatherRows;
   const int grid = total / per_cta + (total % per_cta != 0);
-  return record_cuda_status(launch_kernel(few ? latent_gather_kernel<4> : latent_gather_kernel<16>,
-                                          dim3(grid), dim3(kGatherWarps * 32), 0, stream, true, p));
+  return record_cuda_status(launch_kernel(latent_gather_kernel, dim3(grid),
+                                          dim3(kGatherWarps * 32), 0, stream, true, p));
 }
