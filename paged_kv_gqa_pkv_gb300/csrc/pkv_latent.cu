@@ -190,13 +190,14 @@ struct LatentAppendParams {
 
 constexpr int kAppendWarps = 4;
 
-// A warp takes a token: lane l holds the latent's 16-byte pieces l and l + 32, and lanes 0..7
-// (interleaved) or 0..3 (halves, a piece and its partner) the position part. The squares of all
+// A warp takes a token: lane l holds the latent's 16-byte pieces l and l + 32, and lanes 0..7 four
+// pairs each of the position part. The squares of all
 // 512 values are summed in fp32 by shuffles; norm and rotation stay in fp32 and each value is
 // rounded to bf16 once. What bounds it is the latency of two dependent reads (position, then page
 // and angles) before the writes: the row is read beside the first of them, and norm and weights do
-// not wait for the page. Measured in a graph: 128 tokens 1.9 us, 16384 tokens 10.8 us (37.9 MB,
-// 3.5 TB/s; CTAs of eight warps 11.5, two tokens a warp 13.1, the page looked at first 13.8).
+// not wait for the page. Measured in a graph: 128 tokens 1.9 us, 16384 tokens 10.1 us (37.9 MB,
+// 3.8 TB/s; eight pairs a lane, for more registers and fewer warps, 10.8; CTAs of eight warps 11.5;
+// two tokens a warp 13.1; the page looked at first 13.8).
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kAppendWarps * 32)
 latent_append_kernel(const LatentAppendParams p) {
@@ -205,15 +206,20 @@ latent_append_kernel(const LatentAppendParams p) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   if (i >= p.n_tokens) return;
-  constexpr int kTurners = kInterleaved ? 8 : 4;
+  constexpr int kTurners = 8;  // lanes
   const int slot = __ldg(p.batch_idx + i);
   const int pos = __ldg(p.input_pos + i);
   const uint4* src = reinterpret_cast<const uint4*>(p.x + i * p.x_token);
   uint4 v0 = __ldg(src + lane), v1 = __ldg(src + 32 + lane);
-  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);  // four pairs: neighbours, or four values and their partners
   if (lane < kTurners) {
-    r0 = __ldg(src + 64 + lane);
-    if (!kInterleaved) r1 = __ldg(src + 68 + lane);
+    if (kInterleaved) {
+      r = __ldg(src + 64 + lane);
+    } else {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(src + 64) + lane);
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(src + 68) + lane);
+      r = make_uint4(a.x, a.y, b.x, b.y);
+    }
   }
   if (slot == 0) return;  // padding
   const int block = pos / p.page_size;
@@ -221,20 +227,13 @@ latent_append_kernel(const LatentAppendParams p) {
   if (slot < 0 || slot >= p.max_batch) err |= PKV_DEV_ERR_BAD_SLOT;
   if (pos < 0 || block >= p.max_blocks || pos >= p.rope_len) err |= PKV_DEV_ERR_BAD_POS;
   int page = -1;
-  float4 c[2], s[2];
+  float4 c, s;
   if (!err) {
     page = __ldg(p.page_table + static_cast<long long>(slot) * p.max_blocks + block);
     if (lane < kTurners) {
       const long long at = static_cast<long long>(pos) * (kRotated / 2);
-      const float4* c4 = reinterpret_cast<const float4*>(p.rope_cos + at);
-      const float4* s4 = reinterpret_cast<const float4*>(p.rope_sin + at);
-      if (kInterleaved) {
-        c[0] = __ldg(c4 + lane);
-        s[0] = __ldg(s4 + lane);
-      } else {
-        c[0] = __ldg(c4 + 2 * lane), c[1] = __ldg(c4 + 2 * lane + 1);
-        s[0] = __ldg(s4 + 2 * lane), s[1] = __ldg(s4 + 2 * lane + 1);
-      }
+      c = __ldg(reinterpret_cast<const float4*>(p.rope_cos + at) + lane);
+      s = __ldg(reinterpret_cast<const float4*>(p.rope_sin + at) + lane);
     }
   }
   if (p.norm_weight != nullptr) {
@@ -270,16 +269,22 @@ latent_append_kernel(const LatentAppendParams p) {
   dst[lane] = v0;
   dst[32 + lane] = v1;
   if (lane < kTurners) {
-    float x[8], y[8];
-    unpack8(r0, x);
+    float x[8];
+    unpack8(r, x);
     if (kInterleaved) {
-      turn_pairs(x, c[0], s[0]);
+      turn_pairs(x, c, s);
       dst[64 + lane] = pack8(x);
     } else {
-      unpack8(r1, y);
-      turn_halves(x, y, c, s);
-      dst[64 + lane] = pack8(x);
-      dst[68 + lane] = pack8(y);
+      const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float a = x[u], b = x[u + 4];
+        x[u] = turn_diff(a, cv[u], b, sv[u]);
+        x[u + 4] = turn_sum(b, cv[u], a, sv[u]);
+      }
+      const uint4 w = pack8(x);
+      reinterpret_cast<uint2*>(dst + 64)[lane] = make_uint2(w.x, w.y);
+      reinterpret_cast<uint2*>(dst + 68)[lane] = make_uint2(w.z, w.w);
     }
   }
 }
