@@ -1,6 +1,5 @@
 // pkv_latent.cuh - what the operators of a paged cache of shared latents have in
-// common: the row's sizes, the cache's checks, and the two-CTA forms of the
-// tcgen05 instructions.
+// common: the row's sizes, the cache's checks, and waits with a limit.
 //
 // A cache row is one token's latent (kLatent values, key and value of every head)
 // and its rotated position part (kRotated values, key only), bf16.
@@ -35,25 +34,11 @@ inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// Whether the barrier's phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // The limit of a wait. Reading the global timer takes hundreds of cycles, so it is read only
 // every 256th time that there is nothing to do.
 struct WaitLimit {
   uint64_t since = 0;
   uint32_t n = 0;
-  __device__ __forceinline__ void restart() { since = 0, n = 0; }
   __device__ __forceinline__ bool over(volatile int* abort_flag) {
     if ((++n & 255u) != 0) return false;
     const uint64_t now = global_timer_ns();

@@ -20,8 +20,8 @@
 //
 // The two tiles' chains QK -> softmax -> PV -> QK .. are independent, each with its own issuing
 // thread. (One thread that polled both chains' barriers took ~800 cycles a round beside the
-// softmax warps: 6000 cycles a key tile.) A chain takes ~3600 cycles a key tile, of which its
-// products run 1280: QK ~1000 from issue to S, softmax ~1500 (reading S twice, 64 columns at a
+// softmax warps: 6000 cycles a key tile.) A chain takes 3600 to 4200 cycles a key tile, of which
+// its products run 1280: QK 1000 to 1300 from issue to S, softmax 1500 to 1900 (reading S twice, 64 columns at a
 // time, in loops: with all 128 in registers the unrolled code does not stay in the instruction
 // cache, 4 % slower), P's arrival to PV's end ~600, and so on. Beside a softmax each barrier
 // instruction of an issuing thread takes ~100-250 cycles, for it queues behind exponentials; so
