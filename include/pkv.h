@@ -771,8 +771,10 @@ pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, const void* 
  * they were. Scores, sums and products are held in fp32; the weights are rounded to
  * bf16 for the product (their sum takes them unrounded) and out is rounded once. A NaN
  * or infinity in a sequence's k or v may reach any query of that sequence and head,
- * never another's. num_heads 1 .. 65535; scale finite and > 0. The same inputs give the
- * same bits on every run.
+ * never another's. num_heads 1 .. 65535; scale finite and > 0. A sequence has at most
+ * 2^26 keys (with more, an item of work may pass the kernel's limit on waits, which sets
+ * PKV_DEV_ERR_TIMEOUT and leaves rows unspecified). The same inputs give the same bits on
+ * every run.
  */
 pkv_status pkv_latent_prefill_attention(
     const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_own,
