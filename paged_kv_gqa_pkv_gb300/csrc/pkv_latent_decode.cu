@@ -128,13 +128,34 @@ __device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-// Arrives on a barrier of either CTA. What the barriers of the pair order is shared memory
-// that its own CTA's threads wrote (behind a proxy fence) or TMA filled, and tensor memory;
-// no thread reads what a thread of the other CTA wrote. So the default, CTA-scope semantics
-// do: a release or acquire at cluster scope waits for the thread's whole memory traffic
-// (arriving took 1000-3400 cycles a tile).
+// What CTA 1's softmax threads hand over to the MMAs (P and zeroed values in its shared memory; S
+// that they have read and O that they have rescaled, behind tcgen05 fences) is waited for by threads
+// of CTA 0. Arrives and waits have CTA scope by default and order nothing between threads of two
+// CTAs, so here both have cluster scope. The release is a fence of this CTA's shared memory alone:
+// an arrive with .release.cluster waits for all of the SM's memory traffic, loads by TMA included
+// (64 x ~768 keys, 128 heads: 24.7 us with the fence, 30.1 with that; 16 x ~20000, 128 rows: 75.4
+// and 91.6; 64 x 4096, 16 heads: 57.3 and 89.1). With CTA scope on both sides it is 24.7 and 75.5.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity,
+                                                   volatile int* abort_flag) {
+  WaitLimit limit;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (limit.over(abort_flag)) return false;
+  }
 }
 // One box of a tiled load whose bytes count on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
@@ -603,7 +624,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
             // S goes into buffer tc & 1, which P of tile tc - 2 has been read from. (A barrier for
             // each buffer: this thread may come late, for it waits for Q too, and a barrier that two
             // tiles have completed in the meantime looks as if none had.)
-            ok = tc < 2 || wait_phase(&p_full[tc & 1], ((tc >> 1) - 1) & 1, s_abort);
+            ok = tc < 2 || wait_phase_cluster(&p_full[tc & 1], ((tc >> 1) - 1) & 1, s_abort);
 #pragma unroll 1
             for (int g = 0; ok && g < kKGroups; ++g) {
               ok = wait_phase(&k_full[g], tc & 1, s_abort);
@@ -628,8 +649,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll 1
           for (int j = w.j0; ok && j < w.j1; ++j, ++tc) {
             // (before an item's first PV both epilogues have read the last item's O)
-            ok = wait_phase(&p_full[tc & 1], (tc >> 1) & 1, s_abort) &&
-                 (j > w.j0 || items == 0 || wait_phase(o_free, (items - 1) & 1, s_abort));
+            ok = wait_phase_cluster(&p_full[tc & 1], (tc >> 1) & 1, s_abort) &&
+                 (j > w.j0 || items == 0 || wait_phase_cluster(o_free, (items - 1) & 1, s_abort));
             const bool tail = ragged(w.n, j);
             const int left = w.n - j * kKeys;
             const int steps = left >= kKeys ? 8 : (left + 15) >> 4;  // of 16 keys

@@ -318,6 +318,23 @@ def test_decode_same_bits_every_time():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_decode_both_ctas_of_a_pair():
+    """Heads h and h + 64 with one query: their rows lie in different CTAs of a pair and run through
+    the same steps, so one that took weights or values before they were there would differ. Every
+    pair busy with several tiles, maxima that move, ragged ends; many calls."""
+    g = C.gen(31)
+    B, n = 90, 700
+    pool, table = C.cache(g, 12, n, 64)
+    pool *= torch.rand(pool.shape[0], 1, generator=g).to(torch.bfloat16) * 3
+    q = C.normal(g, B, 1, 64, 576, scale=4.0).repeat(1, 1, 2, 1)
+    slots = C.i32([1 + b % 12 for b in range(B)])
+    lens = torch.randint(n // 2, n + 1, (B,), generator=g).to(torch.int32)
+    args = pool.cuda(), table.cuda(), q.cuda(), slots.cuda(), lens.cuda(), 64, C.SCALE
+    for _ in range(20):
+        out, lse = binding.pkv_latent_decode_attention(*args)
+        assert torch.equal(out[:, :, :64], out[:, :, 64:]) and torch.equal(lse[:, :, :64], lse[:, :, 64:])
+
+
 def test_decode_workspace():
     """A caller's workspace full of NaN; one that is too small is refused."""
     pool, table, q, slots, lens = decode_case(22, [900, 130], 1, 16, 64, marker=0.0)
