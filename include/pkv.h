@@ -732,8 +732,10 @@ size_t pkv_latent_decode_workspace_size(const pkv_cache_desc* cache, int batch, 
  * max_batch) sets PKV_DEV_ERR_BAD_SLOT, an n < 0 or past the table
  * PKV_DEV_ERR_BAD_POS: the row gives 0 / -inf. A page entry out of range within the
  * first n rows sets PKV_DEV_ERR_BAD_PAGE and leaves the row unspecified. The pool is
- * only read; rows past n may hold any bits. A NaN or infinity in a row below n
- * reaches every query of the sequence.
+ * only read; rows past n may hold any bits. A query among whose scores there is a NaN
+ * or +infinity gives NaN for out and lse, never 0 / -inf; one all of whose scores are
+ * -infinity gives 0 / -inf. Of the tokens that do not see a row below n, lse is as
+ * without it, but a NaN or infinity in its latent may reach their out in that dim.
  * n_q 1 .. 64; num_heads 1 .. 1024; batch any count >= 0 (above 512 rows the call runs
  * as equal launches that share the workspace); page_size any multiple of 16; scale
  * finite and > 0. workspace: at least pkv_latent_decode_workspace_size() bytes,

@@ -32,6 +32,7 @@
 // of an item leave unnormalised partials, which a second kernel joins.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 
 #include "pkv_latent.cuh"
@@ -835,7 +836,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
         const int first = w.rb * kRows + static_cast<int>(rank) * 64;  // row of this CTA's row 0
         const int live_rows = min(64, p.rows - first);
         if (live_rows > 0) {
-          const bool has = live && l > 0.f;
+          const bool has = live && l != 0.f;  // (a NaN among its scores: NaN)
           const float inv = has ? 1.f / l : 0.f;
           const long long at = static_cast<long long>(w.b) * p.rows + first;
           const int part = 2 * worker + (w.j0 == 0 ? 1 : 0);
@@ -845,7 +846,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
               p.lse[at + r] =
                   has ? (m_run * p.qscale + __log2f(l)) * 0.69314718055994531f : -INFINITY;
             } else {
-              p.part_ml[2 * (pat + r)] = m_run;
+              // (-inf says that the row sees no key of the part)
+              p.part_ml[2 * (pat + r)] =
+                  m_run == -INFINITY && lim > w.j0 * kKeys ? -FLT_MAX : m_run;
               p.part_ml[2 * (pat + r) + 1] = l;
             }
           }
@@ -972,10 +975,10 @@ __device__ __forceinline__ void join_row(const LatentDecodeParams& p, const int4
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float mn = fmaxf(m, mx);
-    // (a range none of whose keys the row sees adds nothing)
-    const float take = mi == -INFINITY ? 0.f : ex2((mi - mn) * p.qscale);
+    // (-1: a range none of whose keys the row sees, which adds nothing, whatever the keys hold)
+    const float take = mi == -INFINITY ? -1.f : ex2((mi - mn) * p.qscale);
     const float keep = m == -INFINITY ? 0.f : ex2((m - mn) * p.qscale);
-    float ls = take * li;
+    float ls = mi == -INFINITY ? 0.f : take * li;
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
     l = l * keep + ls;
@@ -990,7 +993,7 @@ __device__ __forceinline__ void join_row(const LatentDecodeParams& p, const int4
       float4 v[kVecs];
 #pragma unroll
       for (int e = 0; e < kVecs; ++e) v[e] = __ldcg(src + piece + 32 * e);
-      if (t > 0.f) {
+      if (t >= 0.f) {
 #pragma unroll
         for (int e = 0; e < kVecs; ++e) {
           o[e].x = fmaf(v[e].x, t, o[e].x);
@@ -1002,7 +1005,7 @@ __device__ __forceinline__ void join_row(const LatentDecodeParams& p, const int4
     }
     m = mn;
   }
-  const bool has = l > 0.f;
+  const bool has = l != 0.f;
   const float inv = has ? 1.f / l : 0.f;
   const long long at = static_cast<long long>(item.y) * p.rows + row;
 #pragma unroll

@@ -77,5 +77,40 @@ def check_attention(out_gpu, lse_gpu, want, dims, tag=""):
         assert worst <= 1, f"{tag}: lse {worst:.3g} times the bound"
 
 
+def attend_beside(q, k, v, end, scale, at, place):
+    """What one query has to give that sees the keys before `end` of k, of which key `at` holds a
+    value that is not finite at k[at, place[0]] and v[at, place[1]] (None: not there). Returns the
+    oracle's tuple and which of out's values are NaN; all, and lse too, where the key's score is NaN
+    or +inf, and, of queries that see it with score -inf, the one that its weight of 0 multiplies."""
+    n = v.shape[1]
+    if at >= end:
+        return (*orl.attend(q, k[:end], v[:end], scale), np.zeros(n, bool))
+    with np.errstate(invalid="ignore"):
+        x = 0.0 if place[0] is None else q[place[0]] * k[at, place[0]]
+    if not x < math.inf:
+        return np.zeros(n), math.nan, np.zeros(n), 0.0, np.ones(n, bool)
+    keep = [t for t in range(end) if t != at or x != -math.inf]
+    nan = np.zeros(n, bool)
+    v = v.copy()
+    if place[1] is not None:
+        nan[place[1]] = True
+        v[at, place[1]] = 0
+    return (*orl.attend(q, k[keep], v[keep], scale), nan)
+
+
+def check_beside(out, lse, want, dims, free, tag=""):
+    """out [n, d], lse [n] of a kernel against the rows of attend_beside. free: [n, d], values that may
+    be anything (of queries that do not see the key, where the products meet what it holds)."""
+    o, l = out.double().numpy().copy(), lse.double().numpy().copy()
+    w = [np.stack([np.asarray(r[i]) for r in want]) for i in range(5)]
+    none = np.isnan(w[1])
+    assert np.array_equal(np.isnan(l), none), f"{tag}: lse is NaN at the wrong places"
+    assert np.array_equal(np.isnan(o) | free, w[4] | free), f"{tag}: out is NaN at the wrong places"
+    o[w[4] | free] = 0
+    w[0][w[4] | free] = 0
+    if not none.all():
+        check_attention(torch.from_numpy(o[~none]), torch.from_numpy(l[~none]), [a[~none] for a in w[:4]], dims, tag)
+
+
 def bits(t):
     return bf16_bits(t)

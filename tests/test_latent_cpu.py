@@ -244,3 +244,21 @@ def test_bounds_catch_a_mistake():
         wrong = orl.decode(C.bits(q), C.bits(pool), table.numpy(), np.array([1]), np.array([n]), 16, C.SCALE)
         with pytest.raises(AssertionError):
             C.check_attention(*as_gpu(wrong), want, 576)
+
+
+def test_attend_beside_a_value_that_is_not_finite():
+    """The helper of the GPU tests against numpy's own arithmetic."""
+    rng = np.random.default_rng(8)
+    q, k, v = rng.standard_normal(4), rng.standard_normal((5, 4)), rng.standard_normal((5, 3))
+    for value in (math.nan, math.inf, -math.inf):
+        for end in (2, 3, 5):
+            k2, v2 = k.copy(), v.copy()
+            k2[2, 1] = v2[2, 0] = value
+            out, lse, _, _, nan = C.attend_beside(q, k2, v2, end, 0.5, 2, (1, 0))
+            with np.errstate(invalid="ignore"):
+                x = 0.5 * (k2[:end] @ q)
+                w = np.exp(x - x.max())
+                plain, plain_lse = (w / w.sum()) @ v2[:end], x.max() + np.log(w.sum())
+            assert np.array_equal(np.isnan(plain), nan) and np.isnan(plain_lse) == np.isnan(lse)
+            assert np.allclose(plain[~nan], out[~nan], rtol=0, atol=1e-12)
+            assert np.isnan(lse) or math.isclose(lse, plain_lse, rel_tol=0, abs_tol=1e-12)

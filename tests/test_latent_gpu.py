@@ -318,6 +318,52 @@ def test_decode_same_bits_every_time():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+# a whole item; an item of several parts; ranges that begin and end inside items
+@pytest.mark.parametrize("lens", [[300, 129, 40], [5000], [700, 90, 800] * 30], ids=["whole", "parts", "ranges"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("back,dim", [(1, 3), (2, 540), (3, 511), (39, 300), (40, 575)])
+def test_decode_non_finite_row(lens, value, back, dim):
+    """A value of a cached row that is not finite, `back` rows before the end: queries that see it
+    tell so (NaN where its score is NaN or +inf), the others' lse and all other sequences are as
+    without it."""
+    n_q, H = 3, 2
+    case = decode_case(len(lens) + dim, lens, n_q, H, 64, marker=0.0)
+    pool, table, q, slots, ln = case
+    clean = run_decode(*case, 64)
+    b = len(lens) // 2
+    at = lens[b] - back
+    rows = [orl.pool_row(table.numpy(), b + 1, t, 64, pool.shape[0] // 64) for t in range(lens[b])]
+    bad = pool.clone()
+    bad[rows[at], dim] = value
+    out, lse, err = run_decode(bad, table, q, slots, ln, 64)
+    assert err == 0
+    others = [i for i in range(len(lens)) if i != b]
+    assert torch.equal(out[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
+    c, qb = orl.bf16_bits_to_f64(C.bits(bad[rows])), orl.bf16_bits_to_f64(C.bits(q[b]))
+    want, free = [], np.zeros((n_q * H, 512), bool)
+    for j in range(n_q):
+        for h in range(H):
+            end = lens[b] - (n_q - 1 - j)
+            want.append(C.attend_beside(qb[j, h], c, c[:, :512], end, C.SCALE, at, (dim, dim if dim < 512 else None)))
+            if at >= end and dim < 512:
+                free[j * H + h, dim] = True
+    C.check_beside(out[b].view(-1, 512), lse[b].view(-1), want, 576, free)
+
+
+@pytest.mark.parametrize("lens", [[300, 40], [5000]])
+def test_decode_non_finite_query(lens):
+    """One head's query is NaN, one's infinite: their rows are NaN and no other is touched."""
+    case = decode_case(4, lens, 2, 5, 64, marker=0.0)
+    clean = run_decode(*case, 64)
+    q = case[2].clone()
+    q[-1, 1, 3, 100], q[-1, 0, 2, 570] = float("nan"), float("inf")  # (rows of both signs: +inf among the scores)
+    out, lse, _ = run_decode(case[0], case[1], q, *case[3:], 64)
+    for j, h in ((1, 3), (0, 2)):
+        assert out[-1, j, h].isnan().all() and lse[-1, j, h].isnan()
+        out[-1, j, h], lse[-1, j, h] = clean[0][-1, j, h], clean[1][-1, j, h]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
 def test_decode_both_ctas_of_a_pair():
     """Heads h and h + 64 with one query: their rows lie in different CTAs of a pair and run through
     the same steps, so one that took weights or values before they were there would differ. Every
