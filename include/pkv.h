@@ -771,9 +771,11 @@ pkv_status pkv_latent_decode_attention(const pkv_cache_desc* cache, const void* 
  * n_keys, else PKV_DEV_ERR_LAYOUT is set and rows are unspecified (nothing is read or
  * written outside the tensors). Rows of out and lse outside all sequences stay as
  * they were. Scores, sums and products are held in fp32; the weights are rounded to
- * bf16 for the product (their sum takes them unrounded) and out is rounded once. A NaN
- * or infinity in a sequence's k or v may reach any query of that sequence and head,
- * never another's. num_heads 1 .. 65535; scale finite and > 0. A sequence has at most
+ * bf16 for the product (their sum takes them unrounded) and out is rounded once. A query
+ * among whose scores there is a NaN or +infinity gives NaN for out and lse, never 0 / -inf;
+ * one all of whose scores are -infinity gives 0 / -inf. A NaN or infinity in v may reach,
+ * in its dim, out of any query of that sequence and head, also of those before the key; one
+ * in k reaches only queries that see it. Other sequences are never reached. num_heads 1 .. 65535; scale finite and > 0. A sequence has at most
  * 2^26 keys (with more, an item of work may pass the kernel's limit on waits, which sets
  * PKV_DEV_ERR_TIMEOUT and leaves rows unspecified). The same inputs give the same bits on
  * every run.

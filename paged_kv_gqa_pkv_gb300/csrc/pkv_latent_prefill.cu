@@ -647,7 +647,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_phase(&pv_done[h], (n - 1) & 1, s_abort));
       if (!ok) break;
       tc_fence_after();
-      const bool has = live && l_run > 0.f;
+      const bool has = live && l_run != 0.f;  // (a NaN among its scores: NaN)
       const float inv = has ? 1.f / l_run : 0.f;
       const long long at = static_cast<long long>(x.q0 + i) * p.heads + head;
       __nv_bfloat16* orow = p.out + at * kValue;

@@ -79,37 +79,38 @@ def check_attention(out_gpu, lse_gpu, want, dims, tag=""):
 
 def attend_beside(q, k, v, end, scale, at, place):
     """What one query has to give that sees the keys before `end` of k, of which key `at` holds a
-    value that is not finite at k[at, place[0]] and v[at, place[1]] (None: not there). Returns the
-    oracle's tuple and which of out's values are NaN; all, and lse too, where the key's score is NaN
-    or +inf, and, of queries that see it with score -inf, the one that its weight of 0 multiplies."""
+    value that is not finite at k[at, place[0]] and v[at, place[1]] (None: not there): the oracle's
+    tuple, with NaN everywhere where the key's score is NaN or +inf, and with the value's product with
+    the key's weight (NaN if that is 0) in its place of out."""
     n = v.shape[1]
     if at >= end:
-        return (*orl.attend(q, k[:end], v[:end], scale), np.zeros(n, bool))
+        return orl.attend(q, k[:end], v[:end], scale)
     with np.errstate(invalid="ignore"):
         x = 0.0 if place[0] is None else q[place[0]] * k[at, place[0]]
     if not x < math.inf:
-        return np.zeros(n), math.nan, np.zeros(n), 0.0, np.ones(n, bool)
-    keep = [t for t in range(end) if t != at or x != -math.inf]
-    nan = np.zeros(n, bool)
-    v = v.copy()
+        return np.full(n, math.nan), math.nan, np.zeros(n), 0.0
+    finite = v.copy()
     if place[1] is not None:
-        nan[place[1]] = True
-        v[at, place[1]] = 0
-    return (*orl.attend(q, k[keep], v[keep], scale), nan)
+        finite[at, place[1]] = 0
+    keep = [t for t in range(end) if t != at or x != -math.inf]
+    out, lse, mass, size = orl.attend(q, k[keep], finite[keep], scale)
+    if place[1] is not None:
+        out[place[1]] = math.nan if x == -math.inf else v[at, place[1]]
+    return out, lse, mass, size
 
 
 def check_beside(out, lse, want, dims, free, tag=""):
     """out [n, d], lse [n] of a kernel against the rows of attend_beside. free: [n, d], values that may
     be anything (of queries that do not see the key, where the products meet what it holds)."""
     o, l = out.double().numpy().copy(), lse.double().numpy().copy()
-    w = [np.stack([np.asarray(r[i]) for r in want]) for i in range(5)]
-    none = np.isnan(w[1])
+    w = [np.stack([np.asarray(r[i]) for r in want]) for i in range(4)]
+    o[free] = w[0][free] = 0
+    none, odd = np.isnan(w[1]), ~np.isfinite(w[0])
     assert np.array_equal(np.isnan(l), none), f"{tag}: lse is NaN at the wrong places"
-    assert np.array_equal(np.isnan(o) | free, w[4] | free), f"{tag}: out is NaN at the wrong places"
-    o[w[4] | free] = 0
-    w[0][w[4] | free] = 0
+    assert np.array_equal(o[odd], w[0][odd], equal_nan=True), f"{tag}: out's values that are not finite"
+    o[odd] = w[0][odd] = 0
     if not none.all():
-        check_attention(torch.from_numpy(o[~none]), torch.from_numpy(l[~none]), [a[~none] for a in w[:4]], dims, tag)
+        check_attention(torch.from_numpy(o[~none]), torch.from_numpy(l[~none]), [a[~none] for a in w], dims, tag)
 
 
 def bits(t):

@@ -246,19 +246,22 @@ def test_bounds_catch_a_mistake():
             C.check_attention(*as_gpu(wrong), want, 576)
 
 
-def test_attend_beside_a_value_that_is_not_finite():
+@pytest.mark.parametrize("place", [(1, 0), (1, None), (None, 2)])
+def test_attend_beside_a_value_that_is_not_finite(place):
     """The helper of the GPU tests against numpy's own arithmetic."""
     rng = np.random.default_rng(8)
     q, k, v = rng.standard_normal(4), rng.standard_normal((5, 4)), rng.standard_normal((5, 3))
     for value in (math.nan, math.inf, -math.inf):
         for end in (2, 3, 5):
             k2, v2 = k.copy(), v.copy()
-            k2[2, 1] = v2[2, 0] = value
-            out, lse, _, _, nan = C.attend_beside(q, k2, v2, end, 0.5, 2, (1, 0))
+            if place[0] is not None:
+                k2[2, place[0]] = value
+            if place[1] is not None:
+                v2[2, place[1]] = value
+            out, lse, _, _ = C.attend_beside(q, k2, v2, end, 0.5, 2, place)
             with np.errstate(invalid="ignore"):
                 x = 0.5 * (k2[:end] @ q)
                 w = np.exp(x - x.max())
                 plain, plain_lse = (w / w.sum()) @ v2[:end], x.max() + np.log(w.sum())
-            assert np.array_equal(np.isnan(plain), nan) and np.isnan(plain_lse) == np.isnan(lse)
-            assert np.allclose(plain[~nan], out[~nan], rtol=0, atol=1e-12)
-            assert np.isnan(lse) or math.isclose(lse, plain_lse, rel_tol=0, abs_tol=1e-12)
+            assert np.allclose(plain, out, rtol=0, atol=1e-12, equal_nan=True)
+            assert np.allclose(lse, plain_lse, rtol=0, atol=1e-12, equal_nan=True)

@@ -480,6 +480,63 @@ def test_prefill_neighbours_are_not_read():
         assert torch.equal(a[0][keep_q], b[0][keep_q]) and torch.equal(a[1][keep_q], b[1][keep_q])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["own", "rotated", "v"])
+@pytest.mark.parametrize("n,m,at", [(5, 5, 2), (140, 300, 170), (300, 300, 0), (300, 300, 299), (130, 400, 128), (1, 140, 139)])
+def test_prefill_non_finite_key(n, m, at, where, value):
+    """One key's or value's entry is not finite: queries that see it tell so, those before it have the
+    same bits as without it (for a value: all but its dim, and lse), and so have other sequences."""
+    case = prefill_case(n + m + at, [(20, 30), (n, m), (9, 9)], 2)
+    q, kv, rows, qs, ks = case
+    clean = run_prefill(case)
+    kv2, rows2 = kv.clone(), rows.clone()
+    key, dim = int(ks[1]) + at, 37
+    if where == "own":
+        kv2[key, 1, dim] = value
+    elif where == "rotated":
+        rows2[key, 512 + dim] = value
+    else:
+        kv2[key, 1, 128 + dim] = value
+    out, lse, err = run_prefill((q, kv2, rows2, qs, ks))
+    assert err == 0
+    q0, q1, k0, k1 = int(qs[1]), int(qs[2]), int(ks[1]), int(ks[2])
+    place = dict(own=(dim, None), rotated=(128 + dim, None), v=(None, dim))[where]
+    for h in range(2):
+        if where != "rotated" and h == 0:
+            assert torch.equal(out[:, h], clean[0][:, h]) and torch.equal(lse[:, h], clean[1][:, h])
+            continue
+        k = orl.bf16_bits_to_f64(np.concatenate([C.bits(kv2[k0:k1, h, :128].contiguous()),
+                                                 C.bits(rows2[k0:k1, 512:].contiguous())], 1))
+        v = orl.bf16_bits_to_f64(C.bits(kv2[k0:k1, h, 128:].contiguous()))
+        qh = orl.bf16_bits_to_f64(C.bits(q[q0:q1, h].contiguous()))
+        want, free = [], np.zeros((n, 128), bool)
+        for i in range(n):
+            end = m - n + i + 1
+            want.append(C.attend_beside(qh[i], k, v, end, C.SCALE, at, place))
+            if at >= end:
+                same = torch.ones(128, dtype=torch.bool)
+                if where == "v":
+                    free[i, dim], same[dim] = True, False
+                assert torch.equal(out[q0 + i, h, same], clean[0][q0 + i, h, same])
+                assert torch.equal(lse[q0 + i, h], clean[1][q0 + i, h])
+        C.check_beside(out[q0:q1, h], lse[q0:q1, h], want, 192, free)
+    keep = [i for i in range(len(out)) if not q0 <= i < q1]
+    assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
+def test_prefill_non_finite_query():
+    """A query that is NaN and one that is infinite: their rows are NaN and no other is touched."""
+    case = prefill_case(17, [(140, 150), (20, 20)], 3)
+    clean = run_prefill(case)
+    q = case[0].clone()
+    q[70, 2, 5], q[131, 0, 150] = float("nan"), float("inf")  # (keys of both signs: +inf among the scores)
+    out, lse, _ = run_prefill((q, *case[1:]))
+    for i, h in ((70, 2), (131, 0)):
+        assert out[i, h].isnan().all() and lse[i, h].isnan()
+        out[i, h], lse[i, h] = clean[0][i, h], clean[1][i, h]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
 def test_prefill_large_scores():
     """Scores in the hundreds whose maximum moves along the keys."""
     q, kv, rows, qs, ks = prefill_case(8, [(300, 900)], 2, q_scale=30.0)
