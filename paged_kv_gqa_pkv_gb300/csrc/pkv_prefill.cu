@@ -547,7 +547,7 @@ prefill_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap,
       }
       tc_fence_after();
       const bool in_range = i < p.n_tokens;
-      const bool has = in_range && valid && ok && l_run > 0.f;
+      const bool has = in_range && valid && ok && l_run != 0.f;  // (a NaN among the scores stays one)
       const float inv = has ? 1.f / l_run : 0.f;
       if (n_kv > 0 && ok) {
         // O / l as bf16 into this head's P buffer (same swizzled layout; the

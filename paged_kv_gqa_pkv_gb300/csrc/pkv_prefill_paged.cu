@@ -722,7 +722,7 @@ prefill_paged_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap,
       // tokens served by another kernel are not written here
       const bool in_range =
           mine && i < p.n_tokens && !(p.skip != nullptr && __ldg(p.skip + i) != 0);
-      const bool has = in_range && my_b != 0 && ok && l_run > 0.f;
+      const bool has = in_range && my_b != 0 && ok && l_run != 0.f;  // (a NaN stays one)
       const float inv = has ? 1.f / l_run : 0.f;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                             (static_cast<int64_t>(i) * p.num_q_heads + head) * kHeadDim;

@@ -177,3 +177,23 @@ def test_item_schedule_one_head_items():
     rows = _sampled_rows(c, 400, 300)
     ro, rl = _oracle(c, rows=rows)
     assert_attention_close(out, lse, ro, rl, rows=rows, tag="G=1")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("doc,at", [(0, 0), (2, 100), (2, 299), (3, 1)])
+def test_a_key_that_is_not_finite(doc, at, value):
+    """Tokens that see a NaN or infinite key give NaN (with an infinite one: where the score is not
+    -inf), not a padding row's 0 / -inf; all others have the bits that they have without it."""
+    lens, hq, hkv = [5, 130, 300, 2], 8, 2
+    c = W.packed_prefill(7, doc_lens=lens, hq=hq, hkv=hkv)
+    clean = _run(c)
+    c.k[sum(lens[:doc]) + at, 1, 11] = value
+    out, lse, err = _run(c)
+    assert err == 0
+    sees = torch.zeros_like(lse, dtype=torch.bool)
+    sees[sum(lens[:doc]) + at:sum(lens[:doc + 1]), hq // hkv:] = True
+    # (of an infinite key's scores, those of queries that are negative in its dim are -inf)
+    hit = sees if np.isnan(value) else sees & (c.q[..., 11].float() > 0)
+    assert hit.any() and out[hit].isnan().all() and lse[hit].isnan().all()
+    assert not out[~hit].isnan().any() and not lse[~hit].isnan().any()
+    assert torch.equal(out[~sees], clean[0][~sees]) and torch.equal(lse[~sees], clean[1][~sees])

@@ -230,3 +230,23 @@ def test_item_schedule_one_head_items():
     ro, rl, bad_tok, bad = oracle_chunked(c, rows=rows)
     assert not bad_tok and not bad
     assert_attention_close(out, lse, ro, rl, rows=rows, tag="G=1 chunks")
+
+
+@pytest.mark.parametrize("slot_of,t", [(0, 0), (1, 39), (1, 100)])
+def test_a_cached_key_that_is_nan(slot_of, t):
+    """Tokens that see a NaN key give NaN, not a padding row's 0 / -inf; all others have the bits that
+    they have without it."""
+    c = W.chunked_prefill(9, prefix_lens=[40, 128, 30], chunk_lens=[90, 140, 3], hq=8, hkv=2,
+                          page_size=128)
+    clean = run_chunked(c)
+    slot = sorted(set(c.batch_idx.tolist()) - {0})[slot_of]
+    row = int(c.page_table[slot, t // 128]) * 128 + t % 128
+    held = bool(((c.batch_idx == slot) & (c.input_pos == t)).any())
+    assert not held  # (a prefix's key: the append does not write it)
+    c.k_pool[row, 1, 5] = float("nan")
+    _, _, out, lse, err = run_chunked(c)
+    assert err == clean[4] == 0
+    sees = torch.zeros_like(lse, dtype=torch.bool)
+    sees[(c.batch_idx == slot) & (c.input_pos >= t), 4:] = True
+    assert sees.any() and out[sees].isnan().all() and lse[sees].isnan().all()
+    assert torch.equal(out[~sees], clean[2][~sees]) and torch.equal(lse[~sees], clean[3][~sees])
