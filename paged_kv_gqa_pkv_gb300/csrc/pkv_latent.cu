@@ -4,6 +4,7 @@
 // All three move every byte once and compute next to nothing, so memory bounds them:
 // 16-byte accesses, several independent ones in flight per thread, and no more than
 // one launch.
+#include <cfloat>
 #include <cmath>
 
 #include "pkv_latent.cuh"
@@ -15,16 +16,18 @@ using namespace latent;
 
 // a*c - b*s and a*c + b*s to about one fp32 ulp of the result even where the two
 // products nearly cancel: the rounding error of b*s is kept exactly (an FMA) and
-// folded back in after the fused multiply-add.
+// folded back in after the fused multiply-add. (Of an infinite b*s the error is
+// inf - inf. The sum is infinite or NaN there, so any finite number will do.)
+__device__ __forceinline__ float product_error(float b, float s, float p) {
+  return fmaxf(fmaf(b, s, -p), -FLT_MAX);
+}
 __device__ __forceinline__ float turn_diff(float a, float c, float b, float s) {
   const float p = b * s;
-  const float e = fmaf(b, s, -p);
-  return fmaf(a, c, -p) - e;
+  return fmaf(a, c, -p) - product_error(b, s, p);
 }
 __device__ __forceinline__ float turn_sum(float a, float c, float b, float s) {
   const float p = b * s;
-  const float e = fmaf(b, s, -p);
-  return fmaf(a, c, p) + e;
+  return fmaf(a, c, p) + product_error(b, s, p);
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {

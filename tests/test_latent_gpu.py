@@ -87,6 +87,43 @@ def test_rotate_cancellation():
     check_rotated(y, x, pos, cos, sin, False)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dims", [64, 8, 10])
+def test_rotated_infinities(dims, inter):
+    """Infinite values give what the formula gives (infinities, NaN where it has inf - inf or inf * 0),
+    in the rotation and in the append's position part; a NaN stays in its pair."""
+    g = C.gen(dims)
+    T, inf = 40, float("inf")
+    x = C.normal(g, T, 3, dims)
+    at = torch.randint(0, dims, (T, 3), generator=g)
+    for i in range(1, T):
+        x[i, 0, at[i, 0]] = (inf, -inf, float("nan"))[i % 3]
+        x[i, 1, at[i, 1]] = x[i, 1, (at[i, 1] + (1 if inter else dims // 2)) % dims] = (inf, -inf)[i % 2]
+    pos = torch.arange(T, dtype=torch.int32)
+    cos, sin = C.rope_tables(T, dims)
+    with np.errstate(invalid="ignore"):
+        want = orl.rotate(x.double().numpy(), cos.double().numpy()[:, None], sin.double().numpy()[:, None], inter)
+    odd = ~np.isfinite(want)
+
+    def check(y, want, odd):
+        y = y.double().cpu().numpy()
+        assert np.array_equal(y[odd], want[odd], equal_nan=True)
+        ok = np.abs(y[~odd] - want[~odd]) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want[~odd]) + 1e-38
+        assert ok.all()
+
+    check(binding.pkv_rotate(x.cuda(), pos.cuda(), cos.cuda(), sin.cuda(), interleaved=inter), want, odd)
+    if dims != 64:
+        return
+    for h in range(3):
+        new = torch.cat((C.normal(g, T, 512), x[:, h]), 1)
+        pool, table = C.cache(g, 1, T, 16)
+        got = pool.cuda()
+        binding.pkv_latent_append(got, table.cuda(), new.cuda(), torch.ones_like(pos).cuda(), pos.cuda(), 16, cos.cuda(),
+                                  sin.cuda(), interleaved=inter)
+        rows = [orl.pool_row(table.numpy(), 1, t, 16, pool.shape[0] // 16) for t in range(T)]
+        check(got[rows, 512:], want[:, h], odd[:, h])
+
+
 def test_rotate_bad_positions():
     g = C.gen(5)
     x = C.normal(g, 4, 3, 64)
