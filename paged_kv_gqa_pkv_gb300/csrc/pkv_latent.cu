@@ -193,6 +193,12 @@ struct LatentAppendParams {
 
 constexpr int kAppendWarps = 4;
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // A warp takes a token: lane l holds the latent's 16-byte pieces l and l + 32, and lanes 0..7 four
 // pairs each of the position part. The squares of all
 // 512 values are summed in fp32 by shuffles; norm and rotation stay in fp32 and each value is
@@ -240,24 +246,37 @@ latent_append_kernel(const LatentAppendParams p) {
     }
   }
   if (p.norm_weight != nullptr) {
-    const float4* w = reinterpret_cast<const float4*>(p.norm_weight);
-    const float4 wa = __ldg(w + 2 * lane), wb = __ldg(w + 2 * lane + 1);
-    const float4 wc = __ldg(w + 64 + 2 * lane), wd = __ldg(w + 64 + 2 * lane + 1);
-    const float w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-    const float w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
     float x[8], y[8];
     unpack8(v0, x);
     unpack8(v1, y);
     float ss = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], fmaf(y[u], y[u], ss));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(ss * (1.f / kLatent) + p.norm_eps);
+    float ms = warp_sum(ss) * (1.f / kLatent) + p.norm_eps;
+    float f = 1.f;
+    if (!(ms >= 0x1p-100f && ms <= FLT_MAX)) {
+      // Squares that left fp32's range, or are about to: once more with the values times a power of
+      // two. (Every lane has the same sum. The row is read again: few registers for a rare case.)
+      f = ms < 1.f ? 0x1p80f : 0x1p-70f;
+      const __nv_bfloat16* own = p.x + i * p.x_token + 8 * lane;
+      ss = 0.f;
+#pragma unroll 1
+      for (int u = 0; u < 16; ++u) {
+        const float v = __bfloat162float(own[u < 8 ? u : 248 + u]) * f;
+        ss = fmaf(v, v, ss);
+      }
+      ms = warp_sum(ss) * (1.f / kLatent) + p.norm_eps * f * f;
+    }
+    const float inv = rsqrtf(ms);
+    const float4* w = reinterpret_cast<const float4*>(p.norm_weight);
+    const float4 wa = __ldg(w + 2 * lane), wb = __ldg(w + 2 * lane + 1);
+    const float4 wc = __ldg(w + 64 + 2 * lane), wd = __ldg(w + 64 + 2 * lane + 1);
+    const float w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+    const float w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      x[u] = (x[u] * inv) * w0[u];
-      y[u] = (y[u] * inv) * w1[u];
+      x[u] = ((x[u] * f) * inv) * w0[u];
+      y[u] = ((y[u] * f) * inv) * w1[u];
     }
     v0 = pack8(x);
     v1 = pack8(y);

@@ -171,6 +171,32 @@ def test_append(n, ps, stride, inter, norm):
         assert np.array_equal(got[:, :512], want[:, :512])
 
 
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_append_norm_of_very_large_and_small_latents(eps):
+    """Latents whose squares leave fp32's range have their norm all the same."""
+    g = C.gen(14)
+    sizes = [1e18, 1e19, 1e25, 1e37, 1e-5, 1e-14, 1e-15, 1e-16, 1e-20, 1e-30, 1e-37]
+    n = len(sizes)
+    x = torch.cat(((torch.randn(n, 512, generator=g) * torch.tensor(sizes)[:, None]), torch.randn(n, 64, generator=g)), 1)
+    x[3] = x[3].clamp(-3e38, 3e38)
+    x[2, 7] = 3e38  # one value far ahead of the others
+    x = x.to(torch.bfloat16)
+    pool, table = C.cache(g, 1, n, 16)
+    weight = 1 + 0.2 * torch.randn(512, generator=g)
+    cos, sin = C.rope_tables(n, 64)
+    pos, slot = torch.arange(n, dtype=torch.int32), torch.ones(n, dtype=torch.int32)
+    want, _ = orl.append(orl.bf16_bits_to_f64(C.bits(pool)), table.numpy(), C.bits(x), slot.numpy(), pos.numpy(), 16,
+                         cos.numpy(), sin.numpy(), weight=weight.numpy(), eps=eps)
+    got = pool.cuda()
+    binding.pkv_latent_append(got, table.cuda(), x.cuda(), slot.cuda(), pos.cuda(), 16, cos.cuda(), sin.cuda(),
+                              norm_weight=weight.cuda(), norm_eps=eps)
+    got = got.cpu().double().numpy()
+    assert np.isfinite(want).all()
+    # (a value that 2^-70 brings below 2^-126 is off by up to 2^-150, and the root of the mean square that divides
+    # it is at least 2^-6: 2^-144, below 1e-38)
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(want) + 1e-38).all()
+
+
 def test_append_errors():
     g = C.gen(9)
     pool, table = C.cache(g, 2, 64, 16)
