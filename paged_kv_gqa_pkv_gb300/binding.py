@@ -804,7 +804,8 @@ def _latent_desc(rows: int, row: int, page_size: int, max_batch: int, max_blocks
 
 def latent_cache_desc(pool: torch.Tensor, page_table: torch.Tensor, page_size: int) -> CacheDesc:
     """The descriptor of a paged cache of shared latents, pool [num_pages * page_size, 576]."""
-    return _latent_desc(*pool.shape, int(page_size), *page_table.shape)[0]
+    # (the caller's own: the one that calls share stays here)
+    return CacheDesc.from_buffer_copy(_latent_desc(*pool.shape, int(page_size), *page_table.shape)[0])
 
 
 def _latent_cache(pool, page_table, page_size: int):

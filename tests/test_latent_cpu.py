@@ -150,6 +150,18 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         binding.latent_cache_desc(pool, table, 0)
 
 
+def test_a_descriptor_is_the_callers_own():
+    """Writing to a descriptor changes neither the next one nor what calls of these sizes use."""
+    pool, table = torch.zeros(64, 576, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
+    want = dict(num_pages=4, page_size=16, num_kv_heads=1, head_dim=576, max_batch=2, max_blocks=4)
+    fields = lambda d: {n: getattr(d, n) for n, _ in d._fields_}  # noqa: E731
+    a = binding.latent_cache_desc(pool, table, 16)
+    assert fields(a) == want
+    a.num_pages, a.max_blocks = 1 << 20, 1
+    assert fields(binding.latent_cache_desc(pool, table, 16)) == want
+    assert fields(binding._latent_desc(64, 576, 16, 2, 4)[0]) == want
+
+
 # ---------------------------------------------------------------- the oracle --
 
 def test_rotation_forms():
