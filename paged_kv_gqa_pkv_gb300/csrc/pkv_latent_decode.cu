@@ -36,6 +36,7 @@
 #include <cmath>
 
 #include "pkv_latent.cuh"
+#include "pkv_latent_schedule.h"
 
 namespace pkv {
 namespace {
@@ -244,30 +245,6 @@ __device__ __forceinline__ bool ragged(int n, int j) {
   return n - j * kKeys < kKeys && (n & 15) != 0;
 }
 
-// The schedule, from the sequences' tiles alone, so that it needs no other kernel's work.
-//
-// Up to as many items as workers: an item of nt tiles is cut into ceil(nt / S) equal parts, for the
-// smallest S (in steps of 1/32) at which all parts find a worker; every worker has one part, loads Q
-// once and has nothing to wait for between items. Where the longest item has at most kWholeSlack
-// tiles more than S nothing is cut at all: partial results are 256 KB each for 128 rows, written,
-// read and joined by a kernel that is otherwise done at once (a cut costs about two tiles' time).
-//
-// More items than workers, or parts that are longer than an equal share by more than a quarter and
-// kRangeCost tiles (equal ranges cost the workers a second item, with its queries' loads and another
-// partial: 16 x ~20000 keys, parts of 37 tiles against ranges of 32: 77.7 us against 85.1): the tiles
-// of all items stand in a row (at most 2^30, which the host sees to), sequence by sequence, its row blocks one
-// after another; worker w's range begins at tile w * each + min(w, more). A cut inside an item moves
-// to one of its ends if that is at most kCutReach tiles away (one tile where ranges are long), and to
-// the closer one.
-constexpr int kWholeSlack = 1;
-constexpr int kCutReach = 3;
-constexpr int kRangeCost = 3;
-__device__ __forceinline__ int move_cut(int x, int i0, int i1, int reach) {
-  if (x - i0 <= reach && x - i0 <= i1 - x) return i0;
-  if (i1 - x <= reach) return i1;
-  return x;
-}
-
 // One worker's walk over its range: an item's tiles j0 .. j1 - 1 at a time.
 struct Walk {
   int x, end;          // flat tiles: behind the current segment, the range's end
@@ -390,22 +367,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
     most = __reduce_max_sync(0xffffffffu, most);
     const int each = div_by(total, p.workers);
     const int more = total - each * p.workers.d;
-    bool parts = items <= p.workers.d;
-    int part_len = max(each + (more > 0), 1);
-    if (parts) {
-      for (;; part_len += max(1, part_len >> 5)) {
-        if (most <= part_len + kWholeSlack) {
-          part_len = max(most, 1);
-          break;
-        }
-        int n = 0;
+    const PartRule rule = part_rule(items, most, p.workers.d, each, more, [&](int len) {
+      int n = 0;
 #pragma unroll 1
-        for (int b = lane; b < p.batch; b += 32)
-          n += (key_tiles(keys_of[b]) + part_len - 1) / part_len;
-        if (__reduce_add_sync(0xffffffffu, n) * p.row_blocks.d <= p.workers.d) break;
-      }
-      parts = part_len <= each + each / 4 + kRangeCost;
-    }
+      for (int b = lane; b < p.batch; b += 32) n += (key_tiles(keys_of[b]) + len - 1) / len;
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, n)) * p.row_blocks.d;
+    });
+    const bool parts = rule.parts;
+    const int part_len = rule.len;
     const int reach = each >= 16 ? 1 : kCutReach;
     // what the scan counts: parts, or tiles
     const int x0 = parts ? worker : worker * each + min(worker, more);

@@ -358,6 +358,26 @@ def test_decode_more_rows_than_a_launch():
     assert check_decode((pool, table, q, slots, lens), 16) == 0
 
 
+@pytest.mark.parametrize("short,n_short,long", [(100, 75, 9000), (128, 60, 20000), (1, 10, 5000)])
+def test_decode_one_long_sequence_among_short_ones(short, n_short, long):
+    """Items that just fill the workers, one of them far longer: equal ranges, not parts."""
+    g = C.gen(short + long)
+    ps, H = 64, 2
+    blocks = -(-long // ps)
+    table = torch.full((n_short + 2, blocks), -1, dtype=torch.int32)
+    order = torch.randperm(2 * n_short + blocks, generator=g).to(torch.int32) + 1
+    table[1:n_short + 1, :2] = order[:2 * n_short].view(-1, 2)
+    table[n_short + 1] = order[2 * n_short:]
+    pool = C.normal(g, (len(order) + 1) * ps, 576)
+    at = n_short // 2
+    lens = [short] * n_short
+    slots = list(range(1, n_short + 1))
+    lens.insert(at, long)
+    slots.insert(at, n_short + 1)
+    q = C.normal(g, n_short + 1, 1, H, 576)
+    assert check_decode((pool, table, q, C.i32(slots), C.i32(lens)), ps) == 0
+
+
 def test_decode_errors():
     pool, table, q, slots, lens = decode_case(8, [40, 90, 33, 64], 1, 16, 16, marker=0.0)
     for b, s, n, bit in ((1, 5, 90, BAD_SLOT), (1, -2, 90, BAD_SLOT), (2, 3, -1, BAD_POS), (0, 1, 113, BAD_POS)):
