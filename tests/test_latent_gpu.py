@@ -661,6 +661,49 @@ def test_prefill_bad_starts():
         assert run_prefill(c)[2] & LAYOUT
 
 
+def test_prefill_bad_starts_touch_nothing_outside():
+    """With starts that do not ascend or pass the tensors, what lies around out and lse stays."""
+    case = prefill_case(12, [(40, 40), (60, 60), (20, 20)], 2)
+    q, kv, rows, qs, ks = case
+    n, pad = 120, 300
+    big = 1 << 30
+    for bad_q, bad_k in (([0, 100, 40, 120], None), ([0, 40, 100, 121], None), ([0, 40, 100, 100 + 256], None),
+                         (None, [0, 40, 100, 121]), (None, [0, 100, 40, 120]), ([-1, 40, 100, 120], None),
+                         ([-300, 40, 100, 120], None), ([0, big, 100, 120], None), ([0, 40, 100, big], None),
+                         ([0, -big, 100, 120], None), (None, [-5, 40, 100, 120]), (None, [0, 40, 100, big])):
+        out = torch.full((pad + n + pad, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((pad + n + pad, 2), 7.0, device="cuda")
+        c = (q, kv, rows, C.i32(bad_q) if bad_q else qs, C.i32(bad_k) if bad_k else ks)
+        assert run_prefill(c, out=out[pad:pad + n], lse=lse[pad:pad + n])[2] & LAYOUT
+        for t in (out, lse):
+            assert (t[:pad] == 7).all() and (t[pad + n:] == 7).all(), (bad_q, bad_k)
+
+
+@pytest.mark.parametrize("places", [767, 768, 769, 1100])
+def test_prefill_many_sequences(places):
+    """As many places for items as are sorted by cost, one fewer, and more, which are taken as they
+    stand: short sequences, empty ones, and a few long ones among them."""
+    long = [(300, 300), (257, 500), (1, 700)]
+    tq = sum(n for n, _ in long)
+    lens, i = [], 0
+    while tq // 256 + len(lens) + len(long) < places:
+        n = i % 4
+        lens.append((n, n + i % 3))
+        tq += n
+        i += 1
+    for k, x in enumerate(long):
+        lens.insert((k + 1) * len(lens) // 4, x)
+    case = prefill_case(places, lens, 1)
+    assert case[0].shape[0] // 256 + len(lens) == places
+    assert check_prefill(case) == 0
+
+
+def test_prefill_items_above_the_costliest_that_are_told_apart():
+    """Items of more key tiles than a sorted item's cost can say."""
+    lens = [(3, 17000), (5, 5), (2, 33000), (1, 16100), (130, 140), (1, 16000)]
+    assert check_prefill(prefill_case(19, lens, 2)) == 0
+
+
 def test_prefill_same_bits_every_time():
     case = prefill_case(13, [(300, 700), (129, 129), (1, 900)], 4)
     first = run_prefill(case)
