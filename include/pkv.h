@@ -54,8 +54,9 @@
  *    never synchronise it, and keep no state between calls, so they may be
  *    captured into a CUDA graph.
  *  - head_dim must be 128 (the pkv_latent_* calls: 576, with num_kv_heads 1);
- *    num_q_heads / num_kv_heads (the GQA group) must be 1, 2, 4 or 8; page_size must be a positive multiple of 16; bf16 tensors
- *    must be 16-byte aligned; int32/fp32 arrays 4-byte aligned.
+ *    num_q_heads / num_kv_heads (the GQA group) must be 1, 2, 4 or 8; page_size
+ *    must be a positive multiple of 16; bf16 tensors must be 16-byte aligned;
+ *    int32/fp32 arrays 4-byte aligned.
  */
 #ifndef PKV_H
 #define PKV_H
@@ -654,8 +655,9 @@ pkv_status pkv_compact_pages(const pkv_cache_desc* cache, void* k_pool, void* v_
  * same strides; otherwise no value of out may lie on one of x that the call
  * reads. Values of out must not lie on one another: strides for which the inner
  * axis's rows do not end before the outer one's next are PKV_ERR_ARG (x may
- * repeat values: a stride of 0). The stride of an axis of length 1 is ignored. A token whose position is outside [0, rope_len)
- * is not written and sets PKV_DEV_ERR_BAD_POS. Pointers need 2-byte (x, out) and
+ * repeat values: a stride of 0). The stride of an axis of length 1 is ignored. A
+ * token whose position is outside [0, rope_len) is not written and sets
+ * PKV_DEV_ERR_BAD_POS. Infinite values give what the formula gives. Pointers need 2-byte (x, out) and
  * 4-byte alignment; with 16-byte alignment of all four tensors, strides that are
  * multiples of 8 and dims of 16 (8 if interleaved) the call moves 16 bytes at a
  * time. n_tokens >= 0, num_heads >= 1.
@@ -672,7 +674,7 @@ pkv_status pkv_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stri
  * The cache of a layer is one pool, bf16 [num_pages * page_size, 576] contiguous,
  * described by a pkv_cache_desc with num_kv_heads = 1, head_dim = 576; page table,
  * slots and positions are as for pkv_append. x_new: bf16, token i's 576 values at
- * x_new + i * x_token_stride (a multiple of 8; >= 0): its latent l, then its position
+ * x_new + i * x_token_stride (a multiple of 8, of one token too; >= 0): its latent l, then its position
  * part. With norm_weight (fp32 [512], 16-byte aligned) the latent becomes
  *     l_d * norm_weight[d] / sqrt(mean_d(l_d^2) + norm_eps)
  * (norm_eps finite and >= 0, else PKV_ERR_ARG; ignored without a weight), without
@@ -736,7 +738,9 @@ size_t pkv_latent_decode_workspace_size(const pkv_cache_desc* cache, int batch, 
  * or +infinity gives NaN for out and lse, never 0 / -inf; one all of whose scores are
  * -infinity gives 0 / -inf. Of the tokens that do not see a row below n, lse is as
  * without it, but a NaN or infinity in its latent may reach their out in that dim.
- * n_q 1 .. 64; num_heads 1 .. 1024; batch any count >= 0 (above 512 rows the call runs
+ * n_q 1 .. 64; num_heads 1 .. 1024; the tiles of 128 keys that a slot can have, times
+ * ceil(n_q * num_heads / 128), at most 2^30, else PKV_ERR_ARG (page tables of more than
+ * 2^28 keys with the most query rows); batch any count >= 0 (above 512 rows the call runs
  * as equal launches that share the workspace); page_size any multiple of 16; scale
  * finite and > 0. workspace: at least pkv_latent_decode_workspace_size() bytes,
  * 256-byte aligned, owned by the caller, no initialisation needed; calls that

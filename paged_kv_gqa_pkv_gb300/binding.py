@@ -822,8 +822,8 @@ def _latent_cache(pool, page_table, page_size: int):
 def pkv_latent_append(pool, page_table, x_new, batch_idx, input_pos, page_size: int, rope_cos,
                       rope_sin, norm_weight=None, norm_eps: float = 1e-6, interleaved: bool = False,
                       dev_err=None, stream=None) -> None:
-    """Writes new tokens' rows x_new [N, 576] bf16 (a view of any token stride: the latent,
-    then the position part) into the pool [num_pages * page_size, 576] through the page
+    """Writes new tokens' rows x_new [N, 576] bf16 (a view of any token stride that is a multiple of 8,
+    also where N is 1: the latent, then the position part) into the pool [num_pages * page_size, 576] through the page
     table: the latent normalised with ``norm_weight`` fp32 [512] if given, the position
     part rotated by the fp32 tables [L, 32] at input_pos [N]."""
     dev, desc_p, pool_p, table = _latent_cache(pool, page_table, page_size)

@@ -200,12 +200,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // A warp takes a token: lane l holds the latent's 16-byte pieces l and l + 32, and lanes 0..7 four
-// pairs each of the position part. The squares of all
-// 512 values are summed in fp32 by shuffles; norm and rotation stay in fp32 and each value is
-// rounded to bf16 once. What bounds it is the latency of two dependent reads (position, then page
+// pairs each of the position part. The squares of all 512 values are summed in fp32 by shuffles (once
+// more, scaled, where they leave its range); norm and rotation stay in fp32 and each value is rounded
+// to bf16 once. What bounds it is the latency of two dependent reads (position, then page
 // and angles) before the writes: the row is read beside the first of them, and norm and weights do
-// not wait for the page. Measured in a graph: 128 tokens 1.9 us, 16384 tokens 10.1 us (37.9 MB,
-// 3.8 TB/s; eight pairs a lane, for more registers and fewer warps, 10.8; CTAs of eight warps 11.5;
+// not wait for the page. Measured in a graph: 64 tokens 2.0 us, 16384 tokens 10.2 us (38.1 MB,
+// 3.7 TB/s; eight pairs a lane, for more registers and fewer warps, 10.8; CTAs of eight warps 11.5;
 // two tokens a warp 13.1; the page looked at first 13.8).
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kAppendWarps * 32)

@@ -516,9 +516,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                                3 * g + lane % per);
           }
           // The rows of a tile come from memory into L2 a tile before they are loaded: what shared
-          // memory holds in flight (72 KB) does not cover the latency under load. (64 x ~768 keys,
-          // none / 1 / 2 / 3 / 6 tiles ahead: 28.6 / 26.5 / 27.5 / 28.6 / 29.8 us; 76 x 2048: 45.9 /
-          // 41.4 / 42.8 / 45.3 / 54.0.)
+          // memory holds in flight (72 KB) does not cover the latency under load. (None / 1 / 2 / 3
+          // tiles ahead, 16 and 128 heads: 64 x U[512, 1024] keys 24.3 / 23.3 / 24.6 / 25.3 and 27.0 /
+          // 25.8 / 27.0 / 27.8 us, in pages of 16 rows 25.9 / 26.5 / 27.4 / 28.1 and 28.1 / 28.8 / 29.2 /
+          // 29.7; 64 x U[2048, 8191] 82.0 / 75.6 / 78.9 / 81.6 and 97.3 / 92.7 / 97.3 / 99.7; one
+          // sequence of 4000 15.9 / 15.8 / 15.7 / 15.8.)
           const int ahead = in + kAhead;
           const int at = lane >> box_sh;
           if (row > 0 && (at == ahead || (in == 0 && at > 0 && at < ahead)))

@@ -27,8 +27,8 @@
 // instruction of an issuing thread takes ~100-250 cycles, for it queues behind exponentials; so
 // there are few (a tile's keys have one barrier), and those that need not be waited for last are
 // waited for before P. Measured with 32 heads: 24 prompts of 64 .. 1024 tokens 124 us (0.74
-// PFLOP/s; the floor of their bytes is 71), 8 chunks of 512 behind 512 .. 4096 164 us (1.31
-// PFLOP/s of 1.99). Tiles forced half a period apart by a barrier: 3 % slower (what each gains, the
+// PFLOP/s; the floor of their bytes is 71), 8 chunks of 512 behind 512 .. 4096 165 us (1.30
+// PFLOP/s of 1.99; 172 to 179 us once the card has run them for 20 ms and lowers its clock). Tiles forced half a period apart by a barrier: 3 % slower (what each gains, the
 // ring's eight slots take back: a tile's keys land where the slower tile has read values).
 #include <atomic>
 #include <cmath>

@@ -27,6 +27,22 @@ namespace latent {
 // after another; worker w's range begins at tile w * each + min(w, more). A cut inside an item moves
 // to one of its ends if that is at most kCutReach tiles away (one tile where ranges are long), and to
 // the closer one.
+//
+// Both sides of the borders, measured with pages of 64 (us; 76 workers; n x k: n items of k tiles):
+// - whole against parts, 16 query rows: 8 x 2 10.5 / 11.0, 8 x 3 12.0 / 11.4, 8 x 4 13.6 / 11.3; 38 x 3
+//   14.3 / 16.1, 38 x 4 16.0 / 16.4, 38 x 8 21.1 / 20.5. 128 rows, whose partials are eight times as
+//   large: 8 x 2 11.1 / 13.2, 8 x 3 12.8 / 13.4, 8 x 5 15.9 / 14.6; 25 x 3 14.6 / 20.0, 25 x 8 21.6 /
+//   24.7, 25 x 12 27.3 / 26.5; 38 x 4 17.4 / 22.4, 38 x 12 28.8 / 30.1. So one tile is right up to a few
+//   dozen parts of few rows; many parts of 128 rows are worth having from six or so tiles on, which
+//   the rule does not know.
+// - parts against ranges. Parts by the rule (S / equal share): 16 x U[8, 32] (5 / 4) 21.9 / 25.6 with 16
+//   rows, 26.3 / 28.9 with 128; 16 x U[16, 64] (10 / 8) 30.8 / 33.5, 36.8 / 44.3; 40 x U[16, 64] (28 / 21
+//   and 31 / 23) 56.6 / 54.1, 69.1 / 75.4. Ranges by the rule: 40 x U[64, 125] (66 / 50) 124.5 / 104.7,
+//   138.8 / 123.8; 70 x U[1, 63] (44 / 32 and 37 / 27) 103.5 / 78.0, 103.1 / 96.1; but 64 x U[8, 32] (24 / 16)
+//   56.1 / 49.2, 60.4 / 66.8 and 70 x U[1, 16] (12 / 7 and 14 / 8) 37.0 / 35.5, 40.1 / 47.9.
+// - a reach of 1 / 3 / 5 tiles, 16 and 128 rows: ranges of 8 tiles 34.7 / 33.4 / 33.3 and 49.6 / 43.9 /
+//   42.2; of 18 tiles 49.3 / 49.9 / 53.2 and 74.2 / 66.7 / 64.6; of 40 86.1 / 86.2 / 90.6 and 111.3 / 108.9 /
+//   106.2; of 82 161 / 170 / 174 and 194 / 192 / 190.
 constexpr int kWholeSlack = 1;
 constexpr int kCutReach = 3;
 constexpr int kRangeCost = 3;
